@@ -51,7 +51,8 @@ typedef enum {
   MXQ_ERR_UNSUPPORTED = -4, /* valid request this library does not handle */
   MXQ_ERR_CUDA = -5,        /* launch failed                              */
   MXQ_ERR_BAD_OFFS = -6,    /* device-side: offs not a valid partition    */
-  MXQ_ERR_TIMEOUT = -7      /* device-side: a pipeline wait gave up       */
+  MXQ_ERR_TIMEOUT = -7,     /* device-side: a pipeline wait gave up       */
+  MXQ_ERR_BAD_PAGE = -8     /* device-side: a page, length or row out of range */
 } mxq_status;
 
 typedef enum { MXQ_BF16 = 0, MXQ_F16 = 1, MXQ_F32 = 2 } mxq_dtype;
@@ -151,6 +152,157 @@ int quantize_cache_packed(const void* in, int dtype, int64_t rows, int64_t chann
 int dequantize_cache_packed(const void* codes, const void* scales, int64_t rows, int64_t channels,
                             int format, int32_t block_size, void* out, int out_dtype,
                             void* stream);
+
+/* The paged cache
+ * ---------------
+ * The stored cache form of quantize_cache_packed, kept in pages, and the
+ * attention that reads it.  Shared by the four calls below:
+ *
+ *  codes, scales  device: one tensor's pages (K's or V's), as
+ *           quantize_cache_packed writes values [num_pages, kv_heads,
+ *           page_size, head_dim]: codes [num_pages, kv_heads, page_size,
+ *           head_dim] bytes (fp8) or head_dim / 2 (mxfp4, nvfp4), scales
+ *           [num_pages, kv_heads, page_size, head_dim / block_size] bytes.
+ *           K and V may be the same buffers where they are only read.
+ *  page_table  device, int32 [n_seqs, max_pages], 4-byte aligned: the pages
+ *           of each sequence in order.  Only the entries that a sequence's
+ *           length reaches are read.
+ *  lengths  device, int32 [n_seqs], 4-byte aligned: each sequence's tokens,
+ *           at most max_pages * page_size.  Zero is a length.
+ *  format, block_size  as quantize_cache_packed: head_dim % block_size == 0,
+ *           and block_size even for mxfp4 and nvfp4.
+ *  dev_status  device int32 (nullable, 4-byte aligned).  A page index outside
+ *           [0, num_pages), a length outside [0, max_pages * page_size] or a
+ *           row that no position belongs to writes MXQ_ERR_BAD_PAGE there,
+ *           offs that are no prefix sums MXQ_ERR_BAD_OFFS; the tokens
+ *           concerned are left out and nothing out of range is touched.  The
+ *           kernels never write MXQ_OK: clear the word before the call.
+ *  Codes and scale bytes of the tokens that are read are expected to stand
+ *  for finite values; what lies in a page behind a sequence's last token is
+ *  never used, whatever it holds.
+ *  Errors (host) of all four: null pointers, bad enums and outputs that
+ *  overlap anything else -> MXQ_ERR_INVALID_ARG; negative sizes, kv_heads,
+ *  head_dim, page_size, num_pages or max_pages below 1, a block_size as
+ *  quantize_cache_packed refuses it -> MXQ_ERR_SHAPE; a pointer off its
+ *  boundary -> MXQ_ERR_ALIGNMENT; head_dim above 512, kv_heads above 65535, more
+ *  than 2^30 positions of a sequence or more than 2^31 - 1 pages, table
+ *  entries or sequences x heads x channels -> MXQ_ERR_UNSUPPORTED. */
+
+/* Append new tokens to a paged cache: quantize their K and V rows (exactly
+ * as quantize_cache_packed) into the pages and slots of their positions.
+ *
+ *  k, v     device, [rows, kv_heads, head_dim] elements of dtype (bf16, f16
+ *           or f32), aligned to the element; consecutive rows k_stride and
+ *           v_stride elements apart (at least kv_heads * head_dim), so that
+ *           they may be slices of one projection's output.  v may be null
+ *           (with v_codes, v_scales and v_out null): one tensor is stored.
+ *  offs     device, int32 [n_seqs], 4-byte aligned: inclusive prefix sums of
+ *           the sequences' new rows, as in the grouped GEMM; sequence b owns
+ *           rows [offs[b-1], offs[b]).  offs[n_seqs-1] may be below rows: the
+ *           rows behind it are padding and nothing is written for them.
+ *  lengths  the sequences' tokens with the new ones counted: row offs[b] - i
+ *           goes to position lengths[b] - i.
+ *  k_codes, k_scales, v_codes, v_scales  the cache (outputs: only the slots of
+ *           the new rows are written).  A page that is written belongs to one
+ *           sequence; where the table lists it for two, slots that both write
+ *           hold either's bytes.
+ *  k_out, v_out  device, [rows, kv_heads, head_dim] elements of dtype, dense
+ *           (nullable outputs): the values the stored codes stand for, as
+ *           quantize_cache gives them.
+ *  Fast path: block_size in {8,...,256} a power of two and 16-byte aligned k,
+ *  v (rows included), codes and outputs; anything else valid runs a slower
+ *  general kernel with the same results.  rows == 0: no-op. */
+int append_cache_paged(const void* k, const void* v, int dtype, int64_t rows, int64_t kv_heads,
+                       int64_t head_dim, int64_t k_stride, int64_t v_stride, const int32_t* offs,
+                       const int32_t* page_table, const int32_t* lengths, int64_t n_seqs,
+                       int64_t max_pages, int format, int32_t block_size, int64_t num_pages,
+                       int64_t page_size, void* k_codes, void* k_scales, void* v_codes,
+                       void* v_scales, void* k_out, void* v_out, int32_t* dev_status,
+                       void* stream);
+
+/* Channelwise bounds of the keys of a paged cache's pages.
+ *
+ *  bounds   device, bf16 [num_pages, kv_heads, 2, head_dim], 2-byte aligned
+ *           (output): the least and the largest value of every channel over
+ *           the page's valid tokens, rounded to bf16 (exact for what
+ *           quantize_cache_packed stores, down to bf16's subnormals).
+ *  new_tokens  the pages written are those that hold the last new_tokens
+ *           tokens of each sequence (what an append of at most that many has
+ *           touched); each is computed anew over all its tokens.  At least
+ *           max_pages * page_size: every page of every sequence.
+ *  n_seqs == 0 or new_tokens == 0: no-op. */
+int bound_cache_pages(const void* k_codes, const void* k_scales, int64_t kv_heads,
+                      int64_t head_dim, int format, int32_t block_size, int64_t num_pages,
+                      int64_t page_size, const int32_t* page_table, const int32_t* lengths,
+                      int64_t n_seqs, int64_t max_pages, int64_t new_tokens, void* bounds,
+                      int32_t* dev_status, void* stream);
+
+/* Workspace of select_cache_pages (bytes). */
+uint64_t select_cache_pages_workspace_bytes(int64_t n_seqs, int64_t kv_heads, int64_t max_pages);
+
+/* Choose the pages that each sequence's next token attends to.
+ *
+ *  q        device, [n_seqs, q_heads, head_dim] elements of dtype, aligned to
+ *           the element, sequences q_stride elements apart; q_heads is a
+ *           multiple of kv_heads, and q head j reads kv head j / (q_heads /
+ *           kv_heads).
+ *  bounds   as bound_cache_pages writes them.
+ *  selected  device, int32 [n_seqs, kv_heads, top], 4-byte aligned (output):
+ *           positions in the sequence's page table, ascending, -1 behind the
+ *           last.
+ *  The score of a page is the sum over the kv head's query heads and the
+ *  channels of max(q lo, q hi), in 64-bit floating point: an upper bound of
+ *  the summed logits (before their scale) of any of its tokens.  The first
+ *  keep_first and the last keep_last pages of the sequence are always
+ *  chosen, the rest by falling score, equal ones from the front; min(top,
+ *  pages of the sequence) in all.
+ *  workspace  device, 16-byte aligned, select_cache_pages_workspace_bytes;
+ *           clobbered, not shared by calls that overlap on the GPU.
+ *  Errors: keep_first + keep_last > top -> MXQ_ERR_SHAPE.  n_seqs == 0 or
+ *  top == 0: no-op. */
+int select_cache_pages(const void* q, int dtype, int64_t n_seqs, int64_t q_heads,
+                       int64_t kv_heads, int64_t head_dim, int64_t q_stride, const void* bounds,
+                       int64_t num_pages, int64_t page_size, const int32_t* page_table,
+                       const int32_t* lengths, int64_t max_pages, int64_t top, int64_t keep_first,
+                       int64_t keep_last, int32_t* selected, void* workspace, int32_t* dev_status,
+                       void* stream);
+
+/* Workspace of attend_cache_paged (bytes) on the current device. */
+uint64_t attend_cache_paged_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+
+/* Attention of one new token per sequence over a paged cache.
+ *
+ *  q        as in select_cache_pages.
+ *  window   tokens that a sequence's new token sees, counted from its end
+ *           (its own included); 0: all of them.
+ *  selected  device, int32 [n_seqs, kv_heads, top], 4-byte aligned (nullable,
+ *           with top 0): the pages (positions in the page table) whose tokens
+ *           are attended to, in any order.  Entries that are negative or
+ *           behind the sequence's last page are passed over; a page listed
+ *           twice counts twice.
+ *  softmax_scale  finite; the logits are softmax_scale q . k.
+ *  out      device, [n_seqs, q_heads, head_dim] elements of dtype, dense,
+ *           16-byte aligned (output): the softmax-weighted sum of the values,
+ *           rounded once to dtype.  A sequence without tokens gives zeros.
+ *  lse      device, float [n_seqs, q_heads], 4-byte aligned (nullable
+ *           output): the natural logarithm of the sum of the exponentials of
+ *           the logits; -infinity without tokens.
+ *  workspace  device, 16-byte aligned, attend_cache_paged_workspace_bytes;
+ *           clobbered, not shared by calls that overlap on the GPU.
+ *  Logits, softmax statistics and sums are f32.  A token's value blocks whose
+ *  scale is below 2^-20 of the token's largest lose bits of what lies that
+ *  far below it.
+ *  Fast path: head_dim 64, 128 or 256, page_size a multiple of 16, block_size
+ *  a power of two of at least 32 (fp8, mxfp4) or 16 (nvfp4), codes and scales
+ *  16-byte aligned; anything else valid runs a slower general kernel.
+ *  n_seqs == 0: no-op. */
+int attend_cache_paged(const void* q, int dtype, int64_t n_seqs, int64_t q_heads,
+                       int64_t kv_heads, int64_t head_dim, int64_t q_stride, const void* k_codes,
+                       const void* k_scales, const void* v_codes, const void* v_scales, int format,
+                       int32_t block_size, int64_t num_pages, int64_t page_size,
+                       const int32_t* page_table, const int32_t* lengths, int64_t max_pages,
+                       const int32_t* selected, int64_t top, int64_t window, float softmax_scale,
+                       void* out, float* lse, void* workspace, int32_t* dev_status, void* stream);
 
 /* Grouped GEMM over MXFP4-packed expert weights, dequantized on the fly
  * ([MX] MXFP4GroupedMM forward and backward).

@@ -31,3 +31,9 @@ from ._abi import (  # noqa: F401
     status_string,
     w4a4_grouped_mm,
 )
+from ._paged import (  # noqa: F401
+    append_cache_paged,
+    attend_cache_paged,
+    bound_cache_pages,
+    select_cache_pages,
+)

@@ -71,6 +71,23 @@ def lib():
         L.mxfp4_w4a4_grouped_mm.argtypes = [p, p, p, p, p, i64, i64, i64, i64, p, p, p]
         L.nvfp4_w4a4_grouped_mm.restype = i
         L.nvfp4_w4a4_grouped_mm.argtypes = [p, p, p, p, p, p, p, i64, i64, i64, i64, p, p, p]
+        f = ctypes.c_float
+        L.append_cache_paged.restype = i
+        L.append_cache_paged.argtypes = [p, p, i] + [i64] * 5 + [p, p, p, i64, i64, i, i32, i64,
+                                                                 i64] + [p] * 8
+        L.bound_cache_pages.restype = i
+        L.bound_cache_pages.argtypes = [p, p, i64, i64, i, i32, i64, i64, p, p, i64, i64, i64, p,
+                                        p, p]
+        L.select_cache_pages_workspace_bytes.restype = ctypes.c_uint64
+        L.select_cache_pages_workspace_bytes.argtypes = [i64, i64, i64]
+        L.select_cache_pages.restype = i
+        L.select_cache_pages.argtypes = [p, i, i64, i64, i64, i64, i64, p, i64, i64, p, p, i64,
+                                         i64, i64, i64, p, p, p, p]
+        L.attend_cache_paged_workspace_bytes.restype = ctypes.c_uint64
+        L.attend_cache_paged_workspace_bytes.argtypes = [i64, i64, i64]
+        L.attend_cache_paged.restype = i
+        L.attend_cache_paged.argtypes = [p, i, i64, i64, i64, i64, i64, p, p, p, p, i, i32, i64,
+                                         i64, p, p, i64, p, i64, i64, f, p, p, p, p, p]
         L.mxq_set_wait_limit_ns.restype = ctypes.c_uint64
         L.mxq_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
         _lib = L

@@ -220,6 +220,235 @@ int dequantize_cache_packed(const void* codes, const void* scales, int64_t rows,
                                         (cudaStream_t)stream);
 }
 
+// What the paged cache calls have in common: sizes, enums and the table.
+static int check_paged(int64_t n_seqs, int64_t max_pages, int64_t num_pages, int64_t page_size,
+                       int64_t kv_heads, int64_t head_dim) {
+  const int64_t lim = ((int64_t)1 << 31) - 1, pos = (int64_t)1 << 30;
+  if (n_seqs < 0 || max_pages < 1 || num_pages < 1 || page_size < 1 || kv_heads < 1 ||
+      head_dim < 1)
+    return MXQ_ERR_SHAPE;
+  if (head_dim > 512 || kv_heads > 65535 || num_pages > lim || page_size > pos / max_pages ||
+      n_seqs > lim / max_pages || kv_heads > lim / (n_seqs + 1) ||
+      kv_heads > lim / (page_size * head_dim))
+    return MXQ_ERR_UNSUPPORTED;
+  return MXQ_OK;
+}
+
+static int64_t cache_code_bytes(const PagedCache& c) {
+  return c.num_pages * c.heads * c.page * (int64_t)c.row_bytes();
+}
+static int64_t cache_scale_bytes(const PagedCache& c) {
+  return c.num_pages * c.heads * c.page * (int64_t)c.row_scales();
+}
+
+int append_cache_paged(const void* k, const void* v, int dtype, int64_t rows, int64_t kv_heads,
+                       int64_t head_dim, int64_t k_stride, int64_t v_stride, const int32_t* offs,
+                       const int32_t* page_table, const int32_t* lengths, int64_t n_seqs,
+                       int64_t max_pages, int format, int32_t block_size, int64_t num_pages,
+                       int64_t page_size, void* k_codes, void* k_scales, void* v_codes,
+                       void* v_scales, void* k_out, void* v_out, int32_t* dev_status,
+                       void* stream) {
+  int rc = check_packed_cache(dtype, rows, head_dim, format, block_size);
+  if (rc != MXQ_OK) return rc;
+  rc = check_paged(n_seqs, max_pages, num_pages, page_size, kv_heads, head_dim);
+  if (rc != MXQ_OK) return rc;
+  if (k_stride < kv_heads * head_dim || (v && v_stride < kv_heads * head_dim))
+    return MXQ_ERR_SHAPE;
+  if (rows == 0 || n_seqs == 0) return MXQ_OK;
+  if (!k || !offs || !page_table || !lengths || !k_codes || !k_scales) return MXQ_ERR_INVALID_ARG;
+  if ((v && (!v_codes || !v_scales)) || (!v && (v_codes || v_scales || v_out)))
+    return MXQ_ERR_INVALID_ARG;
+  if (rows > ((int64_t)1 << 31) - 1) return MXQ_ERR_UNSUPPORTED;
+  if (!fits(rows, k_stride) || (v && !fits(rows, v_stride)) ||
+      !fits(num_pages, kv_heads * page_size * head_dim))
+    return MXQ_ERR_SHAPE;
+  if (!elem_aligned(k, dtype) || !elem_aligned(v, dtype) || !elem_aligned(k_out, dtype) ||
+      !elem_aligned(v_out, dtype) || !word_aligned(offs) || !word_aligned(page_table) ||
+      !word_aligned(lengths) || !word_aligned(dev_status))
+    return MXQ_ERR_ALIGNMENT;
+  const PagedCache c{(uint8_t*)k_codes, (uint8_t*)k_scales, (uint8_t*)v_codes, (uint8_t*)v_scales,
+                     page_table,        lengths,            n_seqs,            max_pages,
+                     num_pages,         (int)kv_heads,      (int)head_dim,     (int)page_size,
+                     format,            block_size,         dev_status};
+  const int e = elem_bytes(dtype);
+  const int64_t row = kv_heads * head_dim, dense = rows * row * e;
+  const int64_t k_in = ((rows - 1) * k_stride + row) * e, v_in = ((rows - 1) * v_stride + row) * e;
+  if (!no_alias({{k_codes, cache_code_bytes(c)},
+                 {k_scales, cache_scale_bytes(c)},
+                 {v_codes, cache_code_bytes(c)},
+                 {v_scales, cache_scale_bytes(c)},
+                 {k_out, dense},
+                 {v_out, dense},
+                 {dev_status, 4}},
+                {{k, k_in},
+                 {v, v ? v_in : 0},
+                 {offs, n_seqs * 4},
+                 {page_table, n_seqs * max_pages * 4},
+                 {lengths, n_seqs * 4}}))
+    return MXQ_ERR_INVALID_ARG;
+  const bool fast = packed_fast(block_size, k, k_codes) && aligned16(v) && aligned16(v_codes) &&
+                    aligned16(k_out) && aligned16(v_out) && k_stride % 8 == 0 &&
+                    (!v || v_stride % 8 == 0);
+  return launch_append_cache_paged(k, v, dtype, rows, k_stride, v_stride, offs, c, k_out, v_out,
+                                   fast, (cudaStream_t)stream);
+}
+
+int bound_cache_pages(const void* k_codes, const void* k_scales, int64_t kv_heads,
+                      int64_t head_dim, int format, int32_t block_size, int64_t num_pages,
+                      int64_t page_size, const int32_t* page_table, const int32_t* lengths,
+                      int64_t n_seqs, int64_t max_pages, int64_t new_tokens, void* bounds,
+                      int32_t* dev_status, void* stream) {
+  int rc = check_packed_cache(MXQ_BF16, 0, head_dim, format, block_size);
+  if (rc != MXQ_OK) return rc;
+  rc = check_paged(n_seqs, max_pages, num_pages, page_size, kv_heads, head_dim);
+  if (rc != MXQ_OK) return rc;
+  if (new_tokens < 0) return MXQ_ERR_SHAPE;
+  if (n_seqs == 0 || new_tokens == 0) return MXQ_OK;
+  if (!k_codes || !k_scales || !page_table || !lengths || !bounds) return MXQ_ERR_INVALID_ARG;
+  if (!fits(num_pages, kv_heads * page_size * head_dim)) return MXQ_ERR_SHAPE;
+  if (!elem_aligned(bounds, MXQ_BF16) || !word_aligned(page_table) || !word_aligned(lengths) ||
+      !word_aligned(dev_status))
+    return MXQ_ERR_ALIGNMENT;
+  const PagedCache c{(uint8_t*)const_cast<void*>(k_codes),
+                     (uint8_t*)const_cast<void*>(k_scales),
+                     nullptr,
+                     nullptr,
+                     page_table,
+                     lengths,
+                     n_seqs,
+                     max_pages,
+                     num_pages,
+                     (int)kv_heads,
+                     (int)head_dim,
+                     (int)page_size,
+                     format,
+                     block_size,
+                     dev_status};
+  if (!no_alias({{bounds, num_pages * kv_heads * head_dim * 4}, {dev_status, 4}},
+                {{k_codes, cache_code_bytes(c)},
+                 {k_scales, cache_scale_bytes(c)},
+                 {page_table, n_seqs * max_pages * 4},
+                 {lengths, n_seqs * 4}}))
+    return MXQ_ERR_INVALID_ARG;
+  const bool fast = block_size % 8 == 0 && aligned16(k_codes) && aligned16(bounds);
+  return launch_bound_cache_pages(c, new_tokens, bounds, fast, (cudaStream_t)stream);
+}
+
+uint64_t select_cache_pages_workspace_bytes(int64_t n_seqs, int64_t kv_heads, int64_t max_pages) {
+  if (n_seqs < 1 || kv_heads < 1 || max_pages < 1 || !fits(n_seqs, max_pages) ||
+      !fits(n_seqs * max_pages, kv_heads))
+    return 0;
+  return (uint64_t)(n_seqs * max_pages * kv_heads) * 8;
+}
+
+int select_cache_pages(const void* q, int dtype, int64_t n_seqs, int64_t q_heads,
+                       int64_t kv_heads, int64_t head_dim, int64_t q_stride, const void* bounds,
+                       int64_t num_pages, int64_t page_size, const int32_t* page_table,
+                       const int32_t* lengths, int64_t max_pages, int64_t top, int64_t keep_first,
+                       int64_t keep_last, int32_t* selected, void* workspace, int32_t* dev_status,
+                       void* stream) {
+  if (!valid_dtype(dtype)) return MXQ_ERR_INVALID_ARG;
+  int rc = check_paged(n_seqs, max_pages, num_pages, page_size, kv_heads, head_dim);
+  if (rc != MXQ_OK) return rc;
+  if (q_heads < 1 || q_heads % kv_heads != 0 || q_stride < q_heads * head_dim || top < 0 ||
+      keep_first < 0 || keep_last < 0 || keep_first > top || keep_last > top - keep_first)
+    return MXQ_ERR_SHAPE;
+  if (n_seqs == 0 || top == 0) return MXQ_OK;
+  if (!q || !bounds || !page_table || !lengths || !selected || !workspace)
+    return MXQ_ERR_INVALID_ARG;
+  const int64_t lim = ((int64_t)1 << 31) - 1;
+  if (q_heads > lim / (n_seqs * head_dim) || top > lim / (n_seqs * kv_heads) ||
+      n_seqs * max_pages > lim / kv_heads)
+    return MXQ_ERR_UNSUPPORTED;
+  if (!fits(n_seqs, q_stride) || !fits(num_pages, kv_heads * head_dim)) return MXQ_ERR_SHAPE;
+  if (!elem_aligned(q, dtype) || !elem_aligned(bounds, MXQ_BF16) || !word_aligned(page_table) ||
+      !word_aligned(lengths) || !word_aligned(selected) || !word_aligned(dev_status) ||
+      !aligned16(workspace))
+    return MXQ_ERR_ALIGNMENT;
+  const int64_t ws = (int64_t)select_cache_pages_workspace_bytes(n_seqs, kv_heads, max_pages);
+  if (!no_alias({{selected, n_seqs * kv_heads * top * 4}, {workspace, ws}, {dev_status, 4}},
+                {{q, ((n_seqs - 1) * q_stride + q_heads * head_dim) * elem_bytes(dtype)},
+                 {bounds, num_pages * kv_heads * head_dim * 4},
+                 {page_table, n_seqs * max_pages * 4},
+                 {lengths, n_seqs * 4}}))
+    return MXQ_ERR_INVALID_ARG;
+  const PagedCache c{nullptr,   nullptr,       nullptr,       nullptr,        page_table,
+                     lengths,   n_seqs,        max_pages,     num_pages,      (int)kv_heads,
+                     (int)head_dim, (int)page_size, MXQ_FMT_FP8, (int)head_dim, dev_status};
+  return launch_select_cache_pages(q, dtype, q_heads, q_stride, bounds, c, top, keep_first,
+                                   keep_last, selected, (uint64_t*)workspace,
+                                   (cudaStream_t)stream);
+}
+
+uint64_t attend_cache_paged_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+  if (kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 || head_dim < 1 || head_dim > 512)
+    return 0;
+  return attend_workspace_bytes(q_heads, kv_heads, head_dim);
+}
+
+int attend_cache_paged(const void* q, int dtype, int64_t n_seqs, int64_t q_heads,
+                       int64_t kv_heads, int64_t head_dim, int64_t q_stride, const void* k_codes,
+                       const void* k_scales, const void* v_codes, const void* v_scales, int format,
+                       int32_t block_size, int64_t num_pages, int64_t page_size,
+                       const int32_t* page_table, const int32_t* lengths, int64_t max_pages,
+                       const int32_t* selected, int64_t top, int64_t window, float softmax_scale,
+                       void* out, float* lse, void* workspace, int32_t* dev_status, void* stream) {
+  int rc = check_packed_cache(dtype, 0, head_dim, format, block_size);
+  if (rc != MXQ_OK) return rc;
+  rc = check_paged(n_seqs, max_pages, num_pages, page_size, kv_heads, head_dim);
+  if (rc != MXQ_OK) return rc;
+  if (q_heads < 1 || q_heads % kv_heads != 0 || q_stride < q_heads * head_dim || top < 0 ||
+      window < 0)
+    return MXQ_ERR_SHAPE;
+  if (!(softmax_scale - softmax_scale == 0.0f)) return MXQ_ERR_INVALID_ARG;  // not finite
+  if (n_seqs == 0) return MXQ_OK;
+  if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !page_table || !lengths || !out ||
+      !workspace || (selected == nullptr) != (top == 0))
+    return MXQ_ERR_INVALID_ARG;
+  const int64_t lim = ((int64_t)1 << 31) - 1;
+  if (q_heads > lim / (n_seqs * head_dim) || top > lim / (n_seqs * kv_heads) ||
+      top > ((int64_t)1 << 30) / page_size)
+    return MXQ_ERR_UNSUPPORTED;
+  if (!fits(n_seqs, q_stride) || !fits(num_pages, kv_heads * page_size * head_dim))
+    return MXQ_ERR_SHAPE;
+  if (!elem_aligned(q, dtype) || !aligned16(out) || !word_aligned(lse) ||
+      !word_aligned(page_table) || !word_aligned(lengths) || !word_aligned(selected) ||
+      !word_aligned(dev_status) || !aligned16(workspace))
+    return MXQ_ERR_ALIGNMENT;
+  const PagedCache c{(uint8_t*)const_cast<void*>(k_codes),
+                     (uint8_t*)const_cast<void*>(k_scales),
+                     (uint8_t*)const_cast<void*>(v_codes),
+                     (uint8_t*)const_cast<void*>(v_scales),
+                     page_table,
+                     lengths,
+                     n_seqs,
+                     max_pages,
+                     num_pages,
+                     (int)kv_heads,
+                     (int)head_dim,
+                     (int)page_size,
+                     format,
+                     block_size,
+                     dev_status};
+  const int e = elem_bytes(dtype);
+  if (!no_alias(
+          {{out, n_seqs * q_heads * head_dim * e},
+           {lse, n_seqs * q_heads * 4},
+           {workspace, (int64_t)attend_workspace_bytes(q_heads, kv_heads, head_dim)},
+           {dev_status, 4}},
+          {{q, ((n_seqs - 1) * q_stride + q_heads * head_dim) * e},
+           {k_codes, cache_code_bytes(c)},
+           {k_scales, cache_scale_bytes(c)},
+           {v_codes, cache_code_bytes(c)},
+           {v_scales, cache_scale_bytes(c)},
+           {page_table, n_seqs * max_pages * 4},
+           {lengths, n_seqs * 4},
+           {selected, n_seqs * kv_heads * top * 4}}))
+    return MXQ_ERR_INVALID_ARG;
+  return launch_attend_cache_paged(q, dtype, q_heads, q_stride, c, selected, top, window,
+                                   softmax_scale, out, lse, workspace, (cudaStream_t)stream);
+}
+
 int mxfp4_grouped_mm(const void* a, const void* packed, const void* scales, const int32_t* offs,
                      int64_t T, int64_t E, int64_t N, int64_t K, int transpose_w, void* y,
                      int32_t* dev_status, void* stream) {
@@ -374,6 +603,7 @@ const char* mxq_status_string(int status) {
     case MXQ_ERR_CUDA: return "MXQ_ERR_CUDA";
     case MXQ_ERR_BAD_OFFS: return "MXQ_ERR_BAD_OFFS";
     case MXQ_ERR_TIMEOUT: return "MXQ_ERR_TIMEOUT";
+    case MXQ_ERR_BAD_PAGE: return "MXQ_ERR_BAD_PAGE";
     default: return "MXQ_ERR_UNKNOWN";
   }
 }
@@ -386,7 +616,9 @@ int mxq_debug_checks(int64_t* record) {
   const Reader readers[] = {check_record_abi,         check_record_elementwise,
                             check_record_cache_packed, check_record_nvfp4,
                             check_record_nvfp4_mse,    check_record_grouped_mm_general,
-                            check_record_grouped_mm_tc, check_record_w4a4};
+                            check_record_grouped_mm_tc, check_record_w4a4,
+                            check_record_cache_paged,  check_record_cache_select,
+                            check_record_cache_attend};
   int status = MXQ_OK;
   for (Reader rd : readers) {
     unsigned long long r[3];

@@ -1,0 +1,240 @@
+// Attention of one new token over a paged packed cache (sm_100a): the general
+// kernel for any head size, block size, page size and alignment, and the join
+// of the parts of pairs that were split (see cache_attend.cuh).
+//
+// General kernel: a warp takes one token at a time, lanes hold channels; per
+// query head one dot product (a warp sum), the running maximum m, sum l and
+// weighted values o of the softmax in f32: with s the token's logit in base 2,
+//   m' = max(m, s), l = l 2^(m-m') + 2^(s-m'), o = o 2^(m-m') + 2^(s-m') v.
+// The warps' sums are joined in shared memory in a fixed order.
+#include "cache_attend.cuh"
+
+namespace mxq {
+
+namespace attend {
+
+constexpr int kGeneralHeads = 4;  // query heads a warp carries at once
+
+template <int FMT>
+__device__ __forceinline__ float cache_value(const uint8_t* codes, const uint8_t* scales, int ch,
+                                             int B) {
+  const float s = scale_value<FMT>(scales[ch / B]);
+  if constexpr (FMT == MXQ_FMT_FP8) {
+    return f16lo(e4m3x2_to_f16x2(codes[ch])) * s;
+  } else {
+    const uint32_t byte = codes[ch / 2];
+    return fmaf(f16lo(e2m1x2_to_f16x2((ch & 1) ? byte >> 4 : byte & 15u)), s, 0.0f);
+  }
+}
+
+__device__ __forceinline__ float load_q(const Args& a, int dt, int64_t i) {
+  if (dt == kBF16) return elem_to_f32<kBF16>(((const uint16_t*)a.q)[i]);
+  if (dt == kF16) return elem_to_f32<kF16>(((const uint16_t*)a.q)[i]);
+  return ((const float*)a.q)[i];
+}
+
+// NC: channels per lane (head_dim at most 32 NC).
+template <int FMT, int NC>
+__global__ void __launch_bounds__(kThreads) attend_general_kernel(Args a, int dt) {
+  extern __shared__ float s_part[];  // [warps][heads][dim + 2]
+  const PagedCache& c = a.c;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = c.dim;
+  const int rb = c.row_bytes(), nb = c.row_scales(), stride = D + 2;
+  [[maybe_unused]] const int64_t n_rows = c.num_pages * c.heads * c.page;
+  walk(a, [&](const Span& s, const Target& t, int v0, int v1) {
+    const int r0 = t.tile * kGeneralHeads, heads = min(kGeneralHeads, a.group - r0);
+    float q[kGeneralHeads][NC], o[kGeneralHeads][NC], m[kGeneralHeads], l[kGeneralHeads];
+#pragma unroll
+    for (int r = 0; r < kGeneralHeads; ++r) {
+      m[r] = kLowest;
+      l[r] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int ch = lane + 32 * i;
+        o[r][i] = q[r][i] = 0.0f;
+        if (r < heads && ch < D)
+          q[r][i] = a.scale_log2 *
+                    load_q(a, dt, t.b * a.q_stride + ((int64_t)t.head * a.group + r0 + r) * D + ch);
+      }
+    }
+    for (int v = v0 + warp; v < v1; v += kWarps) {
+      const Token tok = token_at(a, s, t.b, t.head, v);
+      if (tok.row < 0 || !live(a, s, tok.pos) || !MXQ_IN_RANGE(kChkAttendIn, tok.row, n_rows))
+        continue;
+      float k[NC], x[kGeneralHeads];
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int ch = lane + 32 * i;
+        k[i] = ch < D ? cache_value<FMT>(c.k_codes + tok.row * rb, c.k_scales + tok.row * nb, ch,
+                                         c.block)
+                      : 0.0f;
+      }
+#pragma unroll
+      for (int r = 0; r < kGeneralHeads; ++r) {
+        x[r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) x[r] = fmaf(q[r][i], k[i], x[r]);
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) x[r] += __shfl_xor_sync(0xffffffffu, x[r], w);
+      }
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int ch = lane + 32 * i;
+        k[i] = ch < D ? cache_value<FMT>(c.v_codes + tok.row * rb, c.v_scales + tok.row * nb, ch,
+                                         c.block)
+                      : 0.0f;
+      }
+#pragma unroll
+      for (int r = 0; r < kGeneralHeads; ++r) {
+        const float mn = fmaxf(m[r], x[r]), keep = exp2f(m[r] - mn), p = exp2f(x[r] - mn);
+        m[r] = mn;
+        l[r] = fmaf(l[r], keep, p);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) o[r][i] = fmaf(o[r][i], keep, p * k[i]);
+      }
+    }
+    __syncthreads();  // the previous pair's sums have been read
+#pragma unroll
+    for (int r = 0; r < kGeneralHeads; ++r) {
+      float* mine = s_part + (warp * kGeneralHeads + r) * stride;
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        if (lane + 32 * i < D) mine[lane + 32 * i] = o[r][i];
+      if (lane == 0) mine[D] = m[r], mine[D + 1] = l[r];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < heads * D; i += kThreads) {
+      const int r = i / D, ch = i - r * D;
+      float top = kLowest, sum = 0.0f, val = 0.0f;
+      for (int w = 0; w < kWarps; ++w)
+        top = fmaxf(top, s_part[(w * kGeneralHeads + r) * stride + D]);
+      for (int w = 0; w < kWarps; ++w) {
+        const float* p = s_part + (w * kGeneralHeads + r) * stride;
+        const float f = exp2f(p[D] - top);
+        sum = fmaf(p[D + 1], f, sum);
+        val = fmaf(p[ch], f, val);
+      }
+      put(a, dt, t, r, ch, sum > 0.0f ? val / sum : 0.0f);
+      if (ch == 0) put_weight(a, t, r, sum > 0.0f ? top + log2f(sum) : kLowest);
+    }
+  });
+}
+
+// Join the parts of a split pair: out = sum_i o_i 2^(l_i - L), L = log2 sum
+// 2^l_i.  One block per (block of the line, head of the tile); a block whose
+// line part begins no split pair has nothing to do.
+__global__ void __launch_bounds__(kThreads) join_kernel(Args a, int dt, int n_ctas) {
+  __shared__ float s_l[kThreads];
+  __shared__ int s_count;
+  const int cta = blockIdx.x, r = blockIdx.y, D = a.c.dim;
+  const int32_t pair1 = a.hdr[2 * cta + 1];
+  if (pair1 == 0) return;
+  const int64_t pairs = (int64_t)a.c.heads * a.head_tiles, pair = pair1 - 1;
+  Target t;
+  t.b = pair / pairs;
+  const int pl = (int)(pair - t.b * pairs);
+  t.head = pl / a.head_tiles;
+  t.tile = pl - t.head * a.head_tiles;
+  t.whole = true;
+  t.slot = 0;
+  if (t.tile * a.tile_heads + r >= a.group) return;
+  // the blocks behind this one that hold the pair's further parts
+  if (threadIdx.x == 0) s_count = n_ctas - 1 - cta;
+  __syncthreads();
+  for (int i = cta + 1 + threadIdx.x; i < n_ctas; i += kThreads)
+    if (a.hdr[2 * i] != pair1) atomicMin(&s_count, i - cta - 1);
+  __syncthreads();
+  const int parts = 1 + s_count;
+  auto slot = [&](int i) { return i == 0 ? 2 * cta + 1 : 2 * (cta + i); };
+  float top = kLowest;
+  for (int i = threadIdx.x; i < parts; i += kThreads)
+    top = fmaxf(top, a.part_l[(int64_t)slot(i) * a.tile_heads + r]);
+  s_l[threadIdx.x] = top;
+  __syncthreads();
+  for (int w = kThreads / 2; w > 0; w >>= 1) {
+    if ((int)threadIdx.x < w) s_l[threadIdx.x] = fmaxf(s_l[threadIdx.x], s_l[threadIdx.x + w]);
+    __syncthreads();
+  }
+  top = s_l[0];
+  for (int ch = threadIdx.x; ch < D; ch += kThreads) {
+    float sum = 0.0f, val = 0.0f;
+    for (int i = 0; i < parts; ++i) {
+      const int64_t at = (int64_t)slot(i) * a.tile_heads + r;
+      const float l = a.part_l[at], f = l <= kLowest ? 0.0f : exp2f(l - top);
+      sum += f;
+      val = fmaf(a.part_o[at * D + ch], f, val);
+    }
+    put(a, dt, t, r, ch, sum > 0.0f ? val / sum : 0.0f);
+    if (ch == 0) put_weight(a, t, r, sum > 0.0f ? top + log2f(sum) : kLowest);
+  }
+}
+
+template <int FMT>
+int launch_general(const Args& a, int dt, int grid, cudaStream_t st) {
+  const int smem = kWarps * kGeneralHeads * (a.c.dim + 2) * 4;
+  auto go = [&](auto kernel) {
+    if (smem > 48 * 1024 && allow_dynamic_smem((const void*)kernel, smem) != cudaSuccess)
+      return (int)MXQ_ERR_CUDA;
+    kernel<<<grid, kThreads, smem, st>>>(a, dt);
+    return (int)MXQ_OK;
+  };
+  if (a.c.dim <= 64) return go(attend_general_kernel<FMT, 2>);
+  if (a.c.dim <= 128) return go(attend_general_kernel<FMT, 4>);
+  if (a.c.dim <= 256) return go(attend_general_kernel<FMT, 8>);
+  return go(attend_general_kernel<FMT, 16>);
+}
+
+constexpr int kCtasPerSm = 2;
+
+}  // namespace attend
+
+// Slots of partials: two a block, of at most 16 heads of a tile each.
+uint64_t attend_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+  (void)q_heads, (void)kv_heads;
+  const uint64_t slots = 2ull * attend::kCtasPerSm * (uint64_t)num_sms();
+  return (slots * 4 + 15) / 16 * 16 + slots * 16 * (uint64_t)(head_dim + 1) * 4;
+}
+
+int launch_attend_cache_paged(const void* q, int dt, int64_t q_heads, int64_t q_stride,
+                              const PagedCache& c, const int32_t* selected, int64_t top,
+                              int64_t window, float softmax_scale, void* out, float* lse,
+                              void* workspace, cudaStream_t st) {
+  using namespace attend;
+  const int64_t lim = c.max_pages * c.page;
+  Args a;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.c = c;
+  a.selected = selected;
+  a.top = (int)top;
+  a.window = (int)(window < lim ? window : 0);  // as long as the longest: none
+  a.q_heads = (int)q_heads;
+  a.group = (int)(q_heads / c.heads);
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.out = out;
+  a.lse = lse;
+  const int max_ctas = kCtasPerSm * num_sms();
+  const int64_t slots = 2 * max_ctas;
+  a.hdr = (int32_t*)workspace;
+  a.part_l = (float*)((char*)workspace + (slots * 4 + 15) / 16 * 16);
+  a.part_o = a.part_l + slots * 16;
+  a.tile_heads = kGeneralHeads;
+  a.head_tiles = (a.group + kGeneralHeads - 1) / kGeneralHeads;
+  // no more blocks than units that there can be
+  const int64_t span = selected ? top * c.page : (a.window > 0 ? a.window + 16 : lim);
+  const int64_t units = c.n_seqs * c.heads * a.head_tiles * ((span + kUnit - 1) / kUnit);
+  const int grid = (int)(units < max_ctas ? units : max_ctas);
+  int rc;
+  switch (c.fmt) {
+    case MXQ_FMT_FP8: rc = launch_general<MXQ_FMT_FP8>(a, dt, grid, st); break;
+    case MXQ_FMT_MXFP4: rc = launch_general<MXQ_FMT_MXFP4>(a, dt, grid, st); break;
+    default: rc = launch_general<MXQ_FMT_NVFP4>(a, dt, grid, st); break;
+  }
+  if (rc != MXQ_OK) return rc;
+  join_kernel<<<dim3((unsigned)grid, (unsigned)a.tile_heads), kThreads, 0, st>>>(a, dt, grid);
+  return cudaGetLastError() == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
+}
+
+MXQ_DEFINE_CHECK_READER(check_record_cache_attend)
+
+}  // namespace mxq

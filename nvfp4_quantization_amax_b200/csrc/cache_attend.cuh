@@ -1,0 +1,241 @@
+// Attention of one new token over a paged packed cache: how the work is laid
+// over the grid, shared by the general and the tensor-core kernel.
+//
+// The positions of every (sequence, kv head, tile of query heads) are cut into
+// units of 128, the pairs' units are laid in one line, and block i of n takes
+// the i-th n-th of the line: sequences of any lengths keep all SMs busy for
+// the same time, without a plan made on the host.  A block that holds all
+// units of a pair writes its output; where a pair's units fall to several
+// blocks, each writes a partial (the normalised sum in f32 and the logarithm
+// of its weight) to one of its two workspace slots: slot 2i for a pair that
+// began in an earlier block, slot 2i + 1 for one that begins here.  A second,
+// small kernel joins them: the block after which a pair's first part lies
+// looks through the slots of the blocks behind it.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "cache_format.cuh"
+#include "mxq_device.cuh"
+#include "mxq_launch.h"
+
+namespace mxq {
+namespace attend {
+
+constexpr int kUnit = 128;  // positions
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+// Before any token: finite, so that no difference of two of them is NaN.
+constexpr float kLowest = -3.0e38f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Args {
+  const void* q;
+  int64_t q_stride;
+  PagedCache c;
+  const int32_t* selected;
+  int top, window;  // window 0: none
+  int q_heads, group, head_tiles, tile_heads;
+  float scale_log2;  // softmax scale times log2(e)
+  void* out;
+  float* lse;
+  int32_t* hdr;   // [2 n_ctas] pair + 1, or 0
+  float* part_l;  // [2 n_ctas][tile_heads] log2 of the weight
+  float* part_o;  // [2 n_ctas][tile_heads][dim]
+};
+
+// One sequence's positions: [lo, lo + n) of its tokens, or of the listed
+// pages' tokens one page after another (then lo is 0).
+struct Span {
+  int64_t len;  // tokens
+  int lo, n, units;
+};
+
+__device__ __forceinline__ Span span_of(const Args& a, int64_t b) {
+  Span s;
+  s.len = __ldg(a.c.lengths + b);
+  if (s.len < 0 || s.len > a.c.max_pages * a.c.page) {
+    if (a.c.status) *a.c.status = MXQ_ERR_BAD_PAGE;
+    s.len = 0;
+  }
+  if (a.selected) {
+    s.lo = 0;
+    s.n = s.len == 0 ? 0 : a.top * a.c.page;
+  } else {
+    const int64_t start = a.window > 0 && s.len > a.window ? s.len - a.window : 0;
+    s.lo = (int)(start & ~(int64_t)15);  // tiles of 16 stay inside pages
+    s.n = (int)(s.len - s.lo);
+  }
+  s.units = s.n > 0 ? (s.n - 1) / kUnit + 1 : 1;  // an empty pair has its output written too
+  return s;
+}
+
+// The token of position v of a span: its place in the sequence, and its row in
+// the cache ((page * heads + head) * page_size + slot) or -1 where there is
+// none (a page list's -1, a page out of range, the end of the sequence).
+struct Token {
+  int64_t pos, row;
+};
+
+__device__ __forceinline__ Token token_at(const Args& a, const Span& s, int64_t b, int head, int v) {
+  const PagedCache& c = a.c;
+  Token t;
+  int page_at, off;
+  if (a.selected) {
+    const int e = v / c.page;
+    off = v - e * c.page;
+    page_at = -1;
+    if (MXQ_IN_RANGE(kChkAttendTable, e, a.top))
+      page_at = __ldg(a.selected + (b * c.heads + head) * a.top + e);
+    if (page_at < 0 || page_at >= (s.len + c.page - 1) / c.page) return Token{-1, -1};
+  } else {
+    page_at = (s.lo + v) / c.page;
+    off = s.lo + v - page_at * c.page;
+  }
+  t.pos = (int64_t)page_at * c.page + off;
+  t.row = -1;
+  if (!MXQ_IN_RANGE(kChkAttendTable, page_at, c.max_pages)) return t;
+  const int64_t page = __ldg(c.page_table + b * c.max_pages + page_at);
+  if (page < 0 || page >= c.num_pages) {
+    if (c.status) *c.status = MXQ_ERR_BAD_PAGE;
+    return t;
+  }
+  t.row = (page * c.heads + head) * c.page + off;
+  return t;
+}
+
+// Whether the new token attends to a position.
+__device__ __forceinline__ bool live(const Args& a, const Span& s, int64_t pos) {
+  return pos >= 0 && pos < s.len && (a.window == 0 || pos >= s.len - a.window);
+}
+
+// Where a block's part of the line begins: units before it and its first
+// sequence.  All threads of the block call it.
+struct Part {
+  int64_t begin, end;  // units of the line
+  int64_t b, b_begin;  // the sequence of unit begin and that sequence's first unit
+};
+
+__device__ __forceinline__ Part part_of(const Args& a) {
+  __shared__ int64_t s_sum[kWarps];
+  __shared__ int64_t s_b[2];
+  const int64_t pairs = (int64_t)a.c.heads * a.head_tiles;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t total = 0;
+  for (int64_t b = threadIdx.x; b < a.c.n_seqs; b += kThreads)
+    total += pairs * span_of(a, b).units;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) s_sum[warp] = total;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) total += s_sum[i];
+  __syncthreads();
+  Part p;
+  // never more blocks than units: the parts of a pair lie in blocks that follow
+  // one another
+  const int64_t n = total < gridDim.x ? total : gridDim.x;
+  p.begin = min(total, total * blockIdx.x / n);
+  p.end = min(total, total * (blockIdx.x + 1) / n);
+  int64_t before = 0;
+  for (int64_t b0 = 0; b0 < a.c.n_seqs; b0 += kThreads) {
+    const int64_t b = b0 + threadIdx.x;
+    const int64_t mine = b < a.c.n_seqs ? pairs * span_of(a, b).units : 0;
+    int64_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    if (lane == 31) s_sum[warp] = sum;
+    __syncthreads();
+    int64_t first = before + sum - mine, all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) first += s_sum[i];
+      all += s_sum[i];
+    }
+    if (mine > 0 && first <= p.begin && p.begin < first + mine) s_b[0] = b, s_b[1] = first;
+    before += all;
+    __syncthreads();
+    if (before > p.begin) break;
+  }
+  p.b = s_b[0];
+  p.b_begin = s_b[1];
+  return p;
+}
+
+// Where a finished (or partial) pair is written.
+struct Target {
+  int64_t b;
+  int head, tile;
+  bool whole;
+  int slot;
+};
+
+__device__ __forceinline__ void store_out(const Args& a, int dt, int64_t i, float v) {
+  if (dt == kBF16) store_one<kBF16>(a.out, i, v);
+  else if (dt == kF16) store_one<kF16>(a.out, i, v);
+  else store_one<kF32>(a.out, i, v);
+}
+
+// The joined value of channel ch of head r of a pair, and of its weight.
+__device__ __forceinline__ void put(const Args& a, int dt, const Target& t, int r, int ch,
+                                    float v) {
+  if (t.whole) {
+    const int64_t qh = (int64_t)t.head * a.group + t.tile * a.tile_heads + r;
+    const int64_t i = (t.b * a.q_heads + qh) * a.c.dim + ch;
+    if (MXQ_IN_RANGE(kChkAttendOut, i, a.c.n_seqs * a.q_heads * a.c.dim)) store_out(a, dt, i, v);
+  } else {
+    a.part_o[((int64_t)t.slot * a.tile_heads + r) * a.c.dim + ch] = v;
+  }
+}
+__device__ __forceinline__ void put_weight(const Args& a, const Target& t, int r, float l2) {
+  if (t.whole) {
+    const int64_t qh = (int64_t)t.head * a.group + t.tile * a.tile_heads + r;
+    if (a.lse) a.lse[t.b * a.q_heads + qh] = l2 <= kLowest ? __int_as_float(0xFF800000) : l2 * kLn2;
+  } else {
+    a.part_l[(int64_t)t.slot * a.tile_heads + r] = l2;
+  }
+}
+
+// Walk a block's part of the line: work(span, b, head, tile, first position,
+// last position + 1, target) once per pair.
+template <class Work>
+__device__ __forceinline__ void walk(const Args& a, Work work) {
+  const Part p = part_of(a);
+  const int64_t pairs = (int64_t)a.c.heads * a.head_tiles;
+  int32_t hdr[2] = {0, 0};
+  int64_t u = p.begin, b = p.b, b_begin = p.b_begin;
+  while (u < p.end) {
+    const Span s = span_of(a, b);
+    const int64_t pl = (u - b_begin) / s.units;  // pair of the sequence
+    const int j0 = (int)(u - b_begin - pl * s.units);
+    const int j1 = (int)min((int64_t)s.units, j0 + (p.end - u));
+    Target t;
+    t.b = b;
+    t.head = (int)(pl / a.head_tiles);
+    t.tile = (int)(pl - (int64_t)t.head * a.head_tiles);
+    t.whole = j0 == 0 && j1 == s.units;
+    t.slot = 2 * blockIdx.x + (j0 == 0 ? 1 : 0);
+    if (!t.whole) hdr[j0 == 0 ? 1 : 0] = (int32_t)(b * pairs + pl + 1);
+    work(s, t, j0 * kUnit, min(s.n, j1 * kUnit));
+    u += j1 - j0;
+    if (u == b_begin + pairs * s.units) {
+      b_begin = u;
+      ++b;
+    }
+  }
+  if (threadIdx.x == 0) {
+    a.hdr[2 * blockIdx.x] = hdr[0];
+    a.hdr[2 * blockIdx.x + 1] = hdr[1];
+  }
+}
+
+}  // namespace attend
+
+// Tensor-core kernel (cache_attend_tc.cuh); false: these sizes are not its.
+bool launch_attend_tc(const attend::Args& a, int dt, int grid, cudaStream_t st);
+
+}  // namespace mxq

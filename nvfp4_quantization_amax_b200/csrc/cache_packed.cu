@@ -21,6 +21,7 @@
 //   scale), quantize_cache, _power_of_two_ceiling.
 //  "nemo_automodel.components.quantization.mxfp4": module docstring (low
 //   nibble = even column).
+#include "cache_format.cuh"
 #include "mxq.h"
 #include "mxq_device.cuh"
 #include "mxq_launch.h"
@@ -31,111 +32,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
-
-template <int FMT>
-struct PackedFormat;
-template <>
-struct PackedFormat<MXQ_FMT_FP8> {
-  static constexpr int kLo = -126, kHi = 127, kQExp = 8;
-  static constexpr uint32_t kQFrac = 0x600000u;  // 448 = 1.75 * 2^8
-};
-template <>
-struct PackedFormat<MXQ_FMT_MXFP4> {
-  static constexpr int kLo = -126, kHi = 127, kQExp = 2;
-  static constexpr uint32_t kQFrac = 0x400000u;  // 6 = 1.5 * 2^2
-};
-template <>
-struct PackedFormat<MXQ_FMT_NVFP4> {
-  static constexpr int kLo = -9, kHi = 8, kQExp = 2;
-  static constexpr uint32_t kQFrac = 0x400000u;
-};
-
-// Least k with 2^k * qmax >= amax, clamped to the format's range.
-template <int FMT>
-__device__ __forceinline__ int group_scale_exp(uint32_t amax_f32bits) {
-  using F = PackedFormat<FMT>;
-  if (amax_f32bits == 0) return F::kLo;
-  int k = floor_log2_f32bits(amax_f32bits) - F::kQExp +
-          (frac23_f32bits(amax_f32bits) > F::kQFrac ? 1 : 0);
-  return k < F::kLo ? F::kLo : (k > F::kHi ? F::kHi : k);
-}
-
-// Scale byte of 2^k.  E4M3 of 2^k, k in [-9, 8]: subnormal 2^(k+9) / 2^-9
-// steps below 2^-6, biased exponent (k + 7) above.
-template <int FMT>
-__device__ __forceinline__ uint32_t scale_byte(int k) {
-  if constexpr (FMT == MXQ_FMT_NVFP4) {
-    return k >= -6 ? (uint32_t)(k + 7) << 3 : 1u << (k + 9);
-  } else {
-    return (uint32_t)(k + 127);
-  }
-}
-
-template <int FMT>
-__device__ __forceinline__ float scale_value(uint32_t byte) {
-  if constexpr (FMT == MXQ_FMT_NVFP4) {
-    return f16lo(e4m3x2_to_f16x2(byte));
-  } else {
-    return byte == 0xFFu ? __uint_as_float(0x7FC00000u) : exp2i((int)byte - 127);
-  }
-}
-
-// Element codes of eight values x * 2^-k.  fp8: E4M3 (sign of zero kept);
-// fp4: E2M1 with the sign bit iff x < 0 (fmaf(x, inv, +0) turns -0 into +0
-// and keeps the sign of a negative product that underflows).
-template <int FMT>
-__device__ __forceinline__ uint2 encode8(const float* x, float inv) {
-  if constexpr (FMT == MXQ_FMT_FP8) {
-    uint32_t b[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = e4m3x2(x[2 * j] * inv, x[2 * j + 1] * inv);
-    return make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
-  } else {
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = fmaf(x[j], inv, 0.0f);
-    return make_uint2(e2m1x8(v), 0u);
-  }
-}
-
-// Eight decoded values (code times scale, exact in f32).
-template <int FMT>
-__device__ __forceinline__ void decode8(uint2 c, float s, float* v) {
-  if constexpr (FMT == MXQ_FMT_FP8) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t w = j < 2 ? c.x : c.y;
-      const uint32_t h2 = e4m3x2_to_f16x2((w >> (16 * (j & 1))) & 0xFFFFu);
-      v[2 * j] = f16lo(h2) * s;
-      v[2 * j + 1] = f16hi(h2) * s;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t h2 = e2m1x2_to_f16x2((c.x >> (8 * j)) & 0xFFu);
-      v[2 * j] = fmaf(f16lo(h2), s, 0.0f);  // zero magnitudes give +0
-      v[2 * j + 1] = fmaf(f16hi(h2), s, 0.0f);
-    }
-  }
-}
-
-template <int FMT>
-__device__ __forceinline__ void store_codes(void* codes, int64_t item, uint2 c) {
-  if constexpr (FMT == MXQ_FMT_FP8) {
-    *(uint2*)((char*)codes + item * 8) = c;
-  } else {
-    *(uint32_t*)((char*)codes + item * 4) = c.x;
-  }
-}
-
-template <int FMT>
-__device__ __forceinline__ uint2 load_codes(const void* codes, int64_t item) {
-  if constexpr (FMT == MXQ_FMT_FP8) {
-    return __ldg((const uint2*)((const char*)codes + item * 8));
-  } else {
-    return make_uint2(__ldg((const uint32_t*)((const char*)codes + item * 4)), 0u);
-  }
-}
 
 template <int DT, int FMT, int LPB>
 __global__ void __launch_bounds__(kThreads)
@@ -208,18 +104,6 @@ unpack_cache_kernel(const void* __restrict__ codes, const uint8_t* __restrict__ 
 
 // General kernels: any block size the format allows (even for fp4), any
 // alignment; channels % B == 0.  One thread per (row, group).
-template <int DT>
-__device__ __forceinline__ uint32_t elem_bits_at(const void* p, int64_t i) {
-  if constexpr (ElemTraits<DT>::kBytes == 2) return ((const uint16_t*)p)[i];
-  else return ((const uint32_t*)p)[i];
-}
-
-template <int DT>
-__device__ __forceinline__ void store_one(void* p, int64_t i, float v) {
-  if constexpr (ElemTraits<DT>::kBytes == 2) ((uint16_t*)p)[i] = pack2<DT>(v, 0.0f) & 0xFFFFu;
-  else ((float*)p)[i] = v;
-}
-
 template <int DT, int FMT>
 __global__ void __launch_bounds__(kThreads)
 pack_cache_general_kernel(const void* __restrict__ in, uint8_t* __restrict__ codes,

@@ -1,0 +1,378 @@
+// Writing a paged packed cache: new rows quantized into their pages, and the
+// channelwise bounds of the pages' keys (sm_100a).
+//
+// append: row t of sequence b (offs[b-1] <= t < offs[b]) is the token at
+// position p = lengths[b] - (offs[b] - t); its codes go to slot p mod S of
+// page page_table[b][p / S].  Quantization is that of the packed cache: per
+// group of B channels k = the least exponent with 2^k qmax >= amax, code =
+// cast(x 2^-k).  One pass: K and V are read once, codes and scale bytes (and,
+// where asked for, the values they stand for) written once; bound by HBM for
+// prompts and by the launch for a single step.
+//
+// bounds: lo / hi [page][head][channel] = the least / largest value over the
+// page's valid tokens.  Every page is computed from its codes alone, so the
+// result does not depend on what was there before (a page that was freed and
+// taken again, a slot that was written twice).
+#include "cache_format.cuh"
+#include "mxq.h"
+#include "mxq_device.cuh"
+#include "mxq_launch.h"
+
+namespace mxq {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct AppendArgs {
+  const void *k, *v;
+  void *k_out, *v_out;
+  const int32_t* offs;
+  int64_t rows, k_stride, v_stride;
+  int tokens_per_cta;
+  PagedCache c;
+};
+
+// Slot (page * S + position in the page) of row t, or -1: padding, or a row
+// whose position or page is out of range (reported).
+__device__ __forceinline__ int64_t slot_of_row(const AppendArgs& a, int64_t t) {
+  int lo = 0, hi = (int)a.c.n_seqs;  // the first b with offs[b] > t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.offs + mid) > t) hi = mid;
+    else lo = mid + 1;
+  }
+  if (lo == a.c.n_seqs) return -1;
+  const int64_t end = __ldg(a.offs + lo), begin = lo > 0 ? __ldg(a.offs + lo - 1) : 0;
+  const int64_t len = __ldg(a.c.lengths + lo), pos = len - (end - t);
+  if (begin < 0 || begin > t || end > a.rows) {
+    if (a.c.status) *a.c.status = MXQ_ERR_BAD_OFFS;
+    return -1;
+  }
+  int64_t page = -1;
+  if (pos >= 0 && len <= a.c.max_pages * a.c.page)
+    page = __ldg(a.c.page_table + lo * a.c.max_pages + pos / a.c.page);
+  if (page < 0 || page >= a.c.num_pages) {
+    if (a.c.status) *a.c.status = MXQ_ERR_BAD_PAGE;
+    return -1;
+  }
+  return page * a.c.page + pos % a.c.page;
+}
+
+// Block 0 looks over the whole of offs: a sequence whose end lies before its
+// start owns no row, and so would go unnoticed by the rows.
+__device__ __forceinline__ void check_offs(const AppendArgs& a) {
+  if (blockIdx.x != 0 || !a.c.status) return;
+  for (int64_t b = threadIdx.x; b < a.c.n_seqs; b += blockDim.x)
+    if (a.offs[b] < (b > 0 ? a.offs[b - 1] : 0) || a.offs[b] > a.rows)
+      *a.c.status = MXQ_ERR_BAD_OFFS;
+}
+
+constexpr int kMaxCtaTokens = 32;
+
+// Fast path.  An item is 8 channels of one row of K or V; a block takes
+// tokens_per_cta tokens (all heads, K and V), about 4 items a thread, so that
+// each thread has several loads in flight; B/8 lanes share a group's maximum.
+// The slot of each token is looked up once per block.
+template <int DT, int FMT, int LPB>
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
+  __shared__ int64_t s_slot[kMaxCtaTokens];
+  constexpr int kUnroll = ElemTraits<DT>::kBytes == 2 ? 4 : 2;
+  const PagedCache& c = a.c;
+  const int64_t t0 = (int64_t)blockIdx.x * a.tokens_per_cta;
+  const int n_tok = (int)min((int64_t)a.tokens_per_cta, a.rows - t0);
+  const int per_head = c.dim / 8, per_row = c.heads * per_head;
+  const int per_tok = per_row * (a.v ? 2 : 1), n_items = n_tok * per_tok;
+  check_offs(a);
+  if ((int)threadIdx.x < n_tok) s_slot[threadIdx.x] = slot_of_row(a, t0 + threadIdx.x);
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  for (int base = threadIdx.x & ~31; base < n_items; base += kThreads * kUnroll) {
+    uint32_t bits[kUnroll][8];
+    int64_t dst[kUnroll], src[kUnroll];
+    bool is_v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int item = base + u * kThreads + lane;
+      dst[u] = -1;
+      if (item >= n_items) continue;
+      const int tok = item / per_tok;
+      int rem = item - tok * per_tok;
+      is_v[u] = rem >= per_row;
+      if (is_v[u]) rem -= per_row;
+      const int64_t slot = s_slot[tok];
+      if (slot < 0) continue;
+      const int head = rem / per_head, c8 = rem - head * per_head;
+      const int64_t page = slot / c.page, off = slot - page * c.page;
+      dst[u] = ((page * c.heads + head) * c.page + off) * per_head + c8;  // in items
+      src[u] = (t0 + tok) * per_row + rem;                                // dense, in items
+      const int64_t row = (t0 + tok) * ((is_v[u] ? a.v_stride : a.k_stride) / 8) + rem;
+      if (MXQ_IN_RANGE(kChkAppendIn, t0 + tok, a.rows)) load8<DT>(is_v[u] ? a.v : a.k, row, bits[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const bool valid = dst[u] >= 0;
+      uint32_t m = 0;
+      if (valid) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, mag_as_f32_bits<DT>(bits[u][j]));
+      }
+#pragma unroll
+      for (int o = 1; o < LPB; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (!valid) continue;
+      const int k = group_scale_exp<FMT>(m);
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = elem_to_f32<DT>(bits[u][j]);
+      const uint2 code = encode8<FMT>(x, exp2i(-k));
+      if (MXQ_IN_RANGE(kChkAppendOut, dst[u], c.num_pages * c.heads * c.page * per_head))
+        store_codes<FMT>(is_v[u] ? c.v_codes : c.k_codes, dst[u], code);
+      if ((lane & (LPB - 1)) == 0 &&
+          MXQ_IN_RANGE(kChkAppendScale, dst[u] / LPB,
+                       c.num_pages * c.heads * c.page * (int64_t)c.row_scales()))
+        (is_v[u] ? c.v_scales : c.k_scales)[dst[u] / LPB] = (uint8_t)scale_byte<FMT>(k);
+      void* out = is_v[u] ? a.v_out : a.k_out;
+      if (out) {
+        float y[8];
+        decode8<FMT>(code, exp2i(k), y);
+        if (MXQ_IN_RANGE(kChkAppendOut, src[u], a.rows * per_row)) store8<DT>(out, src[u], y);
+      }
+    }
+  }
+}
+
+// General path: any block size, stride and alignment.  One thread per (row, K
+// or V, head, group).
+template <int DT, int FMT>
+__global__ void __launch_bounds__(kThreads) append_general_kernel(AppendArgs a) {
+  const PagedCache& c = a.c;
+  const int B = c.block, nb = c.row_scales(), rb = c.row_bytes();
+  const int two = a.v ? 2 : 1;
+  const int64_t per_tok = (int64_t)two * c.heads * nb, n = a.rows * per_tok;
+  [[maybe_unused]] const int64_t n_rows = c.num_pages * c.heads * c.page;
+  check_offs(a);
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * kThreads) {
+    const int64_t t = i / per_tok;
+    const int rem = (int)(i - t * per_tok);
+    const bool is_v = rem >= c.heads * nb;
+    const int hg = is_v ? rem - c.heads * nb : rem, head = hg / nb, g = hg - head * nb;
+    const int64_t slot = slot_of_row(a, t);
+    if (slot < 0) continue;
+    const int64_t page = slot / c.page, row = (page * c.heads + head) * c.page + slot % c.page;
+    const void* in = is_v ? a.v : a.k;
+    const int64_t src = t * (is_v ? a.v_stride : a.k_stride) + head * c.dim + g * B;
+    const int64_t dense = (t * c.heads + head) * c.dim + g * B;
+    uint8_t* codes = (is_v ? c.v_codes : c.k_codes) + row * rb;
+    void* out = is_v ? a.v_out : a.k_out;
+    if (!MXQ_IN_RANGE(kChkAppendIn, t, a.rows) || !MXQ_IN_RANGE(kChkAppendOut, row, n_rows))
+      continue;
+    uint32_t m = 0;
+    for (int j = 0; j < B; ++j) m = max(m, mag_as_f32_bits<DT>(elem_bits_at<DT>(in, src + j)));
+    const int k = group_scale_exp<FMT>(m);
+    const float inv = exp2i(-k), s = exp2i(k);
+    (is_v ? c.v_scales : c.k_scales)[row * nb + g] = (uint8_t)scale_byte<FMT>(k);
+    for (int j = 0; j < B; j += 2) {
+      const bool pair = j + 1 < B;
+      const float x0 = elem_to_f32<DT>(elem_bits_at<DT>(in, src + j));
+      const float x1 = pair ? elem_to_f32<DT>(elem_bits_at<DT>(in, src + j + 1)) : 0.0f;
+      uint32_t h2;
+      if constexpr (FMT == MXQ_FMT_FP8) {
+        const uint32_t b = e4m3x2(x0 * inv, x1 * inv);
+        codes[g * B + j] = (uint8_t)b;
+        if (pair) codes[g * B + j + 1] = (uint8_t)(b >> 8);
+        h2 = e4m3x2_to_f16x2(b);
+      } else {
+        const uint32_t b = e2m1x2(fmaf(x0, inv, 0.0f), fmaf(x1, inv, 0.0f));
+        codes[(g * B + j) / 2] = (uint8_t)b;
+        h2 = e2m1x2_to_f16x2(b);
+      }
+      if (out) {
+        const float y0 = f16lo(h2) * s, y1 = f16hi(h2) * s;
+        // fp4 zero magnitudes give +0, an fp8 zero keeps its sign
+        store_one<DT>(out, dense + j, FMT == MXQ_FMT_FP8 ? y0 : y0 + 0.0f);
+        if (pair) store_one<DT>(out, dense + j + 1, FMT == MXQ_FMT_FP8 ? y1 : y1 + 0.0f);
+      }
+    }
+  }
+}
+
+template <int DT, int FMT>
+void launch_append_fmt(AppendArgs a, bool fast, cudaStream_t st) {
+  const int64_t per_tok = (int64_t)a.c.heads * (a.c.dim / 8) * (a.v ? 2 : 1);
+  // items are counted in 32 bits, up to 32 tokens of a block
+  if (!fast || per_tok > (1 << 24)) {
+    const int64_t n = a.rows * a.c.heads * a.c.row_scales() * (a.v ? 2 : 1);
+    append_general_kernel<DT, FMT>
+        <<<wave_grid((const void*)append_general_kernel<DT, FMT>, kThreads, n, kThreads), kThreads,
+           0, st>>>(a);
+    return;
+  }
+  a.tokens_per_cta = (int)(per_tok >= 1024 ? 1 : 1024 / per_tok);
+  if (a.tokens_per_cta > kMaxCtaTokens) a.tokens_per_cta = kMaxCtaTokens;
+  const unsigned grid = (unsigned)((a.rows + a.tokens_per_cta - 1) / a.tokens_per_cta);
+  switch (a.c.block / 8) {
+    case 1: append_kernel<DT, FMT, 1><<<grid, kThreads, 0, st>>>(a); break;
+    case 2: append_kernel<DT, FMT, 2><<<grid, kThreads, 0, st>>>(a); break;
+    case 4: append_kernel<DT, FMT, 4><<<grid, kThreads, 0, st>>>(a); break;
+    case 8: append_kernel<DT, FMT, 8><<<grid, kThreads, 0, st>>>(a); break;
+    case 16: append_kernel<DT, FMT, 16><<<grid, kThreads, 0, st>>>(a); break;
+    default: append_kernel<DT, FMT, 32><<<grid, kThreads, 0, st>>>(a); break;
+  }
+}
+
+template <int DT>
+void launch_append_dt(const AppendArgs& a, bool fast, cudaStream_t st) {
+  switch (a.c.fmt) {
+    case MXQ_FMT_FP8: launch_append_fmt<DT, MXQ_FMT_FP8>(a, fast, st); break;
+    case MXQ_FMT_MXFP4: launch_append_fmt<DT, MXQ_FMT_MXFP4>(a, fast, st); break;
+    default: launch_append_fmt<DT, MXQ_FMT_NVFP4>(a, fast, st); break;
+  }
+}
+
+// ---------------------------------------------------------------- bounds
+
+struct BoundArgs {
+  PagedCache c;
+  int64_t new_tokens;
+  uint16_t* bounds;
+};
+
+// Value of channel ch of a row of codes; the product is exact.
+template <int FMT>
+__device__ __forceinline__ float value_at(const uint8_t* codes, const uint8_t* scales, int ch,
+                                          int B) {
+  const float s = scale_value<FMT>(scales[ch / B]);
+  if constexpr (FMT == MXQ_FMT_FP8) {
+    return f16lo(e4m3x2_to_f16x2(codes[ch])) * s;
+  } else {
+    const uint32_t byte = codes[ch / 2];
+    return fmaf(f16lo(e2m1x2_to_f16x2((ch & 1) ? byte >> 4 : byte & 15u)), s, 0.0f);
+  }
+}
+
+// One block per (page of a sequence, head); pages counted from the sequence's
+// last.  VEC = 8: a thread holds 8 channels' bounds over every (threads /
+// (D/8))-th row, and the rows' threads are joined in shared memory.  VEC = 1:
+// a thread holds one channel over all rows, for any block size and alignment.
+template <int FMT, int VEC>
+__global__ void __launch_bounds__(kThreads) bound_kernel(BoundArgs a) {
+  extern __shared__ float s_part[];  // [row threads][2][D], VEC = 8 only
+  const PagedCache& c = a.c;
+  const int64_t b = blockIdx.y;
+  const int head = blockIdx.z;
+  const int64_t len = c.lengths[b];
+  if (len < 0 || len > c.max_pages * c.page) {
+    if (c.status) *c.status = MXQ_ERR_BAD_PAGE;
+    return;
+  }
+  const int64_t n_pages = (len + c.page - 1) / c.page, j = n_pages - 1 - blockIdx.x;
+  if (j < 0 || (j + 1) * c.page <= len - a.new_tokens) return;
+  const int64_t page = c.page_table[b * c.max_pages + j];
+  if (page < 0 || page >= c.num_pages) {
+    if (c.status) *c.status = MXQ_ERR_BAD_PAGE;
+    return;
+  }
+  const int rows = (int)min((int64_t)c.page, len - j * c.page);
+  const int rb = c.row_bytes(), nb = c.row_scales();
+  const int64_t row0 = (page * c.heads + head) * c.page;
+  const uint8_t* codes = c.k_codes + row0 * rb;
+  const uint8_t* scales = c.k_scales + row0 * nb;
+  uint16_t* out = a.bounds + (page * c.heads + head) * 2 * c.dim;
+  [[maybe_unused]] const int64_t n_rows = c.num_pages * c.heads * c.page;
+  const float inf = __int_as_float(0x7F800000);
+  if constexpr (VEC == 8) {
+    const int per_row = c.dim / 8, n_thr = kThreads / per_row;  // rows at a time
+    const int r = threadIdx.x / per_row, c8 = threadIdx.x - r * per_row;
+    float lo[8], hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lo[i] = inf, hi[i] = -inf;
+    if (r < n_thr) {
+#pragma unroll 4
+      for (int s = r; s < rows; s += n_thr) {
+        if (!MXQ_IN_RANGE(kChkBoundIn, row0 + s, n_rows)) continue;
+        float v[8];
+        decode8<FMT>(load_codes<FMT>(codes, (int64_t)s * per_row + c8),
+                     scale_value<FMT>(__ldg(scales + s * nb + c8 * 8 / c.block)), v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) lo[i] = fminf(lo[i], v[i]), hi[i] = fmaxf(hi[i], v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s_part[(r * 2) * c.dim + c8 * 8 + i] = lo[i];
+        s_part[(r * 2 + 1) * c.dim + c8 * 8 + i] = hi[i];
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * c.dim; i += kThreads) {
+      float v = s_part[i];
+      for (int q = 1; q < min(n_thr, rows); ++q) {
+        const float w = s_part[q * 2 * c.dim + i];
+        v = i < c.dim ? fminf(v, w) : fmaxf(v, w);
+      }
+      out[i] = (uint16_t)(pack2<kBF16>(v, 0.0f) & 0xFFFFu);
+    }
+  } else {
+    for (int ch = threadIdx.x; ch < c.dim; ch += kThreads) {
+      float lo = inf, hi = -inf;
+      for (int s = 0; s < rows; ++s) {
+        if (!MXQ_IN_RANGE(kChkBoundIn, row0 + s, n_rows)) continue;
+        const float v = value_at<FMT>(codes + (int64_t)s * rb, scales + (int64_t)s * nb, ch, c.block);
+        lo = fminf(lo, v);
+        hi = fmaxf(hi, v);
+      }
+      out[ch] = (uint16_t)(pack2<kBF16>(lo, 0.0f) & 0xFFFFu);
+      out[c.dim + ch] = (uint16_t)(pack2<kBF16>(hi, 0.0f) & 0xFFFFu);
+    }
+  }
+}
+
+template <int FMT>
+void launch_bound_fmt(const BoundArgs& a, bool fast, dim3 grid, cudaStream_t st) {
+  if (fast) {
+    const int n_thr = kThreads / (a.c.dim / 8);
+    bound_kernel<FMT, 8><<<grid, kThreads, (size_t)n_thr * 2 * a.c.dim * 4, st>>>(a);
+  } else {
+    bound_kernel<FMT, 1><<<grid, kThreads, 0, st>>>(a);
+  }
+}
+
+}  // namespace
+
+int launch_append_cache_paged(const void* k, const void* v, int dt, int64_t rows, int64_t k_stride,
+                              int64_t v_stride, const int32_t* offs, const PagedCache& c,
+                              void* k_out, void* v_out, bool fast, cudaStream_t st) {
+  const AppendArgs a{k, v, k_out, v_out, offs, rows, k_stride, v_stride, 1, c};
+  switch (dt) {
+    case kBF16: launch_append_dt<kBF16>(a, fast, st); break;
+    case kF16: launch_append_dt<kF16>(a, fast, st); break;
+    default: launch_append_dt<kF32>(a, fast, st); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
+}
+
+int launch_bound_cache_pages(const PagedCache& c, int64_t new_tokens, void* bounds, bool fast,
+                             cudaStream_t st) {
+  // the last new_tokens tokens lie in at most this many pages
+  int64_t pages = (new_tokens - 1) / c.page + 2;
+  if (new_tokens > c.max_pages * c.page || pages > c.max_pages) pages = c.max_pages;
+  const BoundArgs a{c, new_tokens, (uint16_t*)bounds};
+  // grid.y ends at 65535: longer batches go in parts (heads are at most that)
+  for (int64_t b = 0; b < c.n_seqs; b += 65535) {
+    BoundArgs part = a;
+    part.c.page_table += b * c.max_pages;
+    part.c.lengths += b;
+    part.c.n_seqs = c.n_seqs - b < 65535 ? c.n_seqs - b : 65535;
+    const dim3 grid((unsigned)pages, (unsigned)part.c.n_seqs, (unsigned)c.heads);
+    switch (c.fmt) {
+      case MXQ_FMT_FP8: launch_bound_fmt<MXQ_FMT_FP8>(part, fast, grid, st); break;
+      case MXQ_FMT_MXFP4: launch_bound_fmt<MXQ_FMT_MXFP4>(part, fast, grid, st); break;
+      default: launch_bound_fmt<MXQ_FMT_NVFP4>(part, fast, grid, st); break;
+    }
+  }
+  return cudaGetLastError() == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
+}
+
+MXQ_DEFINE_CHECK_READER(check_record_cache_paged)
+
+}  // namespace mxq

@@ -46,6 +46,9 @@ enum MxqCheckId {
   kChkGemmGenIn, kChkGemmGenW, kChkGemmGenOut,
   kChkGemmTcOut, kChkGemmTcScale, kChkGemmTcSmem, kChkGemmTcTmem,
   kChkW4Out, kChkW4Scale, kChkW4Smem, kChkGemmTcW,
+  kChkAppendIn, kChkAppendOut, kChkAppendScale, kChkBoundIn, kChkBoundScale, kChkBoundOut,
+  kChkSelectIn, kChkSelectWs, kChkSelectOut,
+  kChkAttendIn, kChkAttendScale, kChkAttendOut, kChkAttendWs, kChkAttendTable,
   kChkSelfTest = 99
 };
 

@@ -48,6 +48,33 @@ int launch_nvfp4_quantize_mse(const void* x, int dt, int64_t rows, int64_t K, vo
 uint32_t* noalloc_scratch(size_t need_bytes, int* status);
 int launch_nvfp4_dequantize(const void* packed, const void* block_scales, const float* global_scale,
                             int64_t rows, int64_t K, void* out, int dt, cudaStream_t st);
+
+// A paged cache as the kernels see it: K's and V's pages (V may be absent or
+// the same), the page table and the lengths.
+struct PagedCache {
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  const int32_t *page_table, *lengths;
+  int64_t n_seqs, max_pages, num_pages;
+  int heads, dim, page, fmt, block;
+  int32_t* status;
+  // Bytes of one token's codes and scales of one head.
+  __host__ __device__ int row_bytes() const { return fmt == 0 ? dim : dim / 2; }
+  __host__ __device__ int row_scales() const { return dim / block; }
+};
+int launch_append_cache_paged(const void* k, const void* v, int dt, int64_t rows, int64_t k_stride,
+                              int64_t v_stride, const int32_t* offs, const PagedCache& c,
+                              void* k_out, void* v_out, bool fast, cudaStream_t st);
+int launch_bound_cache_pages(const PagedCache& c, int64_t new_tokens, void* bounds, bool fast,
+                             cudaStream_t st);
+int launch_select_cache_pages(const void* q, int dt, int64_t q_heads, int64_t q_stride,
+                              const void* bounds, const PagedCache& c, int64_t top,
+                              int64_t keep_first, int64_t keep_last, int32_t* selected,
+                              uint64_t* keys, cudaStream_t st);
+int launch_attend_cache_paged(const void* q, int dt, int64_t q_heads, int64_t q_stride,
+                              const PagedCache& c, const int32_t* selected, int64_t top,
+                              int64_t window, float softmax_scale, void* out, float* lse,
+                              void* workspace, cudaStream_t st);
+uint64_t attend_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim);
 uint64_t set_wait_limit_ns(uint64_t ns);
 uint64_t get_wait_limit_ns();
 int launch_nvfp4_w4a4_grouped_mm(const void* xq, const void* xs, const float* xg,
@@ -67,6 +94,9 @@ int check_record_nvfp4_mse(unsigned long long* out);
 int check_record_grouped_mm_general(unsigned long long* out);
 int check_record_grouped_mm_tc(unsigned long long* out);
 int check_record_w4a4(unsigned long long* out);
+int check_record_cache_paged(unsigned long long* out);
+int check_record_cache_select(unsigned long long* out);
+int check_record_cache_attend(unsigned long long* out);
 int launch_grouped_mm(const void* a, const void* packed, const void* scales, const int32_t* offs,
                       int64_t T, int64_t E, int64_t N, int64_t K, int transpose_w, void* y,
                       int32_t* dev_status, cudaStream_t st);
