@@ -293,8 +293,8 @@ uint64_t attend_cache_paged_workspace_bytes(int64_t q_heads, int64_t kv_heads, i
  *  scale is below 2^-20 of the token's largest lose bits of what lies that
  *  far below it.
  *  Fast path: head_dim 64, 128 or 256, page_size a multiple of 16, block_size
- *  a power of two of at least 32 (fp8, mxfp4) or 16 (nvfp4), codes and scales
- *  16-byte aligned; anything else valid runs a slower general kernel.
+ *  a power of two of at least 32 (fp8), 32 (mxfp4) or 16 (nvfp4), codes and
+ *  scales 16-byte aligned; anything else valid runs a slower general kernel.
  *  n_seqs == 0: no-op. */
 int attend_cache_paged(const void* q, int dtype, int64_t n_seqs, int64_t q_heads,
                        int64_t kv_heads, int64_t head_dim, int64_t q_stride, const void* k_codes,

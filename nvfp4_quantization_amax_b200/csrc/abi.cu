@@ -618,7 +618,9 @@ int mxq_debug_checks(int64_t* record) {
                             check_record_nvfp4_mse,    check_record_grouped_mm_general,
                             check_record_grouped_mm_tc, check_record_w4a4,
                             check_record_cache_paged,  check_record_cache_select,
-                            check_record_cache_attend};
+                            check_record_cache_attend, check_record_attend_fp8_64,
+                            check_record_attend_fp8_128, check_record_attend_fp8_256,
+                            check_record_attend_fp4};
   int status = MXQ_OK;
   for (Reader rd : readers) {
     unsigned long long r[3];

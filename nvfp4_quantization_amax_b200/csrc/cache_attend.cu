@@ -27,12 +27,6 @@ __device__ __forceinline__ float cache_value(const uint8_t* codes, const uint8_t
   }
 }
 
-__device__ __forceinline__ float load_q(const Args& a, int dt, int64_t i) {
-  if (dt == kBF16) return elem_to_f32<kBF16>(((const uint16_t*)a.q)[i]);
-  if (dt == kF16) return elem_to_f32<kF16>(((const uint16_t*)a.q)[i]);
-  return ((const float*)a.q)[i];
-}
-
 // NC: channels per lane (head_dim at most 32 NC).
 template <int FMT, int NC>
 __global__ void __launch_bounds__(kThreads) attend_general_kernel(Args a, int dt) {
@@ -186,6 +180,30 @@ int launch_general(const Args& a, int dt, int grid, cudaStream_t st) {
 
 constexpr int kCtasPerSm = 2;
 
+// Whether the tensor-core kernels have these sizes: see the header's fast path.
+bool tc_fits(const Args& a) {
+  const PagedCache& c = a.c;
+  auto aligned = [](const void* p) { return ((uintptr_t)p & 15) == 0; };
+  if (c.dim != 64 && c.dim != 128 && c.dim != 256) return false;
+  if (c.page % 16 != 0 || !aligned(c.k_codes) || !aligned(c.k_scales) || !aligned(c.v_codes) ||
+      !aligned(c.v_scales))
+    return false;
+  // tiles of 16 tokens are counted in 31 bits
+  if (c.num_pages > (((int64_t)1 << 31) - 1) / ((int64_t)c.heads * (c.page / 16))) return false;
+  if (c.fmt == MXQ_FMT_NVFP4) return c.block == 16;
+  if (c.fmt == MXQ_FMT_MXFP4) return c.block == 32;
+  return c.block >= 32 && (c.block & (c.block - 1)) == 0;
+}
+
+int launch_tc_any(const Args& a, int dt, int64_t units, int* grid, cudaStream_t st) {
+  if (a.c.fmt == MXQ_FMT_MXFP4) return tc_mxfp4(a, dt, units, grid, st);
+  if (a.c.fmt == MXQ_FMT_NVFP4) return tc_nvfp4(a, dt, units, grid, st);
+  const int nb = a.c.row_scales();
+  if (a.c.dim == 64) return tc_fp8_64(a, dt, nb, units, grid, st);
+  if (a.c.dim == 128) return tc_fp8_128(a, dt, nb, units, grid, st);
+  return tc_fp8_256(a, dt, nb, units, grid, st);
+}
+
 }  // namespace attend
 
 // Slots of partials: two a block, of at most 16 heads of a tile each.
@@ -218,18 +236,21 @@ int launch_attend_cache_paged(const void* q, int dt, int64_t q_heads, int64_t q_
   a.hdr = (int32_t*)workspace;
   a.part_l = (float*)((char*)workspace + (slots * 4 + 15) / 16 * 16);
   a.part_o = a.part_l + slots * 16;
-  a.tile_heads = kGeneralHeads;
-  a.head_tiles = (a.group + kGeneralHeads - 1) / kGeneralHeads;
+  // the tensor-core kernel carries 8 heads, or 16 where that does not overfill
+  // its registers (one f16 term, up to 128 channels): K and V are read once
+  // for all of a tile
+  const bool tc = tc_fits(a);
+  a.tile_heads = !tc ? kGeneralHeads : a.group > 8 && dt == kBF16 && c.dim <= 128 ? 16 : 8;
+  a.head_tiles = (a.group + a.tile_heads - 1) / a.tile_heads;
   // no more blocks than units that there can be
   const int64_t span = selected ? top * c.page : (a.window > 0 ? a.window + 16 : lim);
   const int64_t units = c.n_seqs * c.heads * a.head_tiles * ((span + kUnit - 1) / kUnit);
-  const int grid = (int)(units < max_ctas ? units : max_ctas);
+  int grid = (int)(units < max_ctas ? units : max_ctas);
   int rc;
-  switch (c.fmt) {
-    case MXQ_FMT_FP8: rc = launch_general<MXQ_FMT_FP8>(a, dt, grid, st); break;
-    case MXQ_FMT_MXFP4: rc = launch_general<MXQ_FMT_MXFP4>(a, dt, grid, st); break;
-    default: rc = launch_general<MXQ_FMT_NVFP4>(a, dt, grid, st); break;
-  }
+  if (tc) rc = launch_tc_any(a, dt, units, &grid, st);
+  else if (c.fmt == MXQ_FMT_FP8) rc = launch_general<MXQ_FMT_FP8>(a, dt, grid, st);
+  else if (c.fmt == MXQ_FMT_MXFP4) rc = launch_general<MXQ_FMT_MXFP4>(a, dt, grid, st);
+  else rc = launch_general<MXQ_FMT_NVFP4>(a, dt, grid, st);
   if (rc != MXQ_OK) return rc;
   join_kernel<<<dim3((unsigned)grid, (unsigned)a.tile_heads), kThreads, 0, st>>>(a, dt, grid);
   return cudaGetLastError() == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;

@@ -109,6 +109,12 @@ __device__ __forceinline__ bool live(const Args& a, const Span& s, int64_t pos) 
   return pos >= 0 && pos < s.len && (a.window == 0 || pos >= s.len - a.window);
 }
 
+__device__ __forceinline__ float load_q(const Args& a, int dt, int64_t i) {
+  if (dt == kBF16) return elem_to_f32<kBF16>(((const uint16_t*)a.q)[i]);
+  if (dt == kF16) return elem_to_f32<kF16>(((const uint16_t*)a.q)[i]);
+  return ((const float*)a.q)[i];
+}
+
 // Where a block's part of the line begins: units before it and its first
 // sequence.  All threads of the block call it.
 struct Part {
@@ -233,9 +239,13 @@ __device__ __forceinline__ void walk(const Args& a, Work work) {
   }
 }
 
+// The tensor-core kernels of each format and head size: `nb` scales a row, a
+// grid of at most `units` blocks (returned in *grid).
+int tc_fp8_64(const Args& a, int dt, int nb, int64_t units, int* grid, cudaStream_t st);
+int tc_fp8_128(const Args& a, int dt, int nb, int64_t units, int* grid, cudaStream_t st);
+int tc_fp8_256(const Args& a, int dt, int nb, int64_t units, int* grid, cudaStream_t st);
+int tc_mxfp4(const Args& a, int dt, int64_t units, int* grid, cudaStream_t st);
+int tc_nvfp4(const Args& a, int dt, int64_t units, int* grid, cudaStream_t st);
+
 }  // namespace attend
-
-// Tensor-core kernel (cache_attend_tc.cuh); false: these sizes are not its.
-bool launch_attend_tc(const attend::Args& a, int dt, int grid, cudaStream_t st);
-
 }  // namespace mxq

@@ -1,0 +1,602 @@
+// Attention of one new token over a paged packed cache on the tensor cores
+// (sm_100a): the kernel behind cache_attend_fp8_*.cu and
+// cache_attend_fp4.cu.  How the work is laid over the grid is in
+// cache_attend.cuh.
+//
+// A byte of K or V meets the G query heads of its kv head, 4 G flop with fp8:
+// at G = 8 and the speed of HBM more than f32 arithmetic gives, and far less
+// than the tensor cores'.  So the codes go to f16 in registers (E4M3 and E2M1
+// are exact there) and through mma.m16n8k16 with f32 sums; the kernel is bound
+// by HBM, and its second limit is the issue of the conversions.  (A tcgen05
+// tile needs 128 rows of one operand: with tokens as rows it would leave the
+// head side, 8 wide, no better filled and the codes would have to be decoded
+// into TMEM first.)
+//
+// Per warp, 16 tokens at a time (one tile; a page holds whole tiles):
+//  - S = K Q^T: rows are tokens, columns 8 heads.  K comes from shared memory
+//    by ldmatrix (four bytes of a row a lane), the order of the channels in the
+//    sum is the codes' own and Q is laid out to match.
+//  - softmax in base 2 with a running reference m that is moved only when a
+//    logit exceeds it by 2^4, so most tiles need no warp maximum and no
+//    rescaling of the sums.
+//  - O^T = V^T P^T: rows are channels, columns heads.  A lane reads 1/8 of a
+//    row of four tokens, two tokens' codes are paired byte by byte (or nibble
+//    by nibble) so that one conversion gives the pair the instruction wants,
+//    and P turns from S's layout to the operand's by movmatrix.
+//
+// Scales.  E8M0 scales (fp8, mxfp4) reach 2^+-127, beyond f16.  K: the sum over
+// each scale block is multiplied by its scale in f32.  V: the token's largest
+// scale exponent r joins the weight in the exponent, 2^(s - m + r - R), with a
+// running whole reference R, so a token of huge values and no weight costs no
+// other token its bits; what is left of a block's scale is 2^(k - r) <= 1 and
+// multiplies the codes in f16 (exact down to 2^-21 (fp8), 2^-26 (mxfp4) of
+// the token's largest scale).  E4M3 scales (nvfp4) times E2M1 codes are exact
+// in f16.
+//
+// Rounding.  Q is scaled by a power of two into f16 and held in TERMS terms
+// (one is exact for bf16 and f16; f32: 22 bits), the weights in TERMS terms:
+// one f16 (2^-11, below bf16's step) for bf16 results, two (22 bits) for f16
+// and f32.
+//
+// A warp loads its own tiles by 16-byte cp.async through STAGES buffers; the
+// chunks of a row are swizzled so that ldmatrix (8 rows, one chunk) and V's
+// reads (4 rows, 2 chunks) touch every bank once.
+#pragma once
+
+#include "cache_attend.cuh"
+#include "sm100_primitives.cuh"
+
+namespace mxq {
+namespace attend {
+
+constexpr int kTile = 16;           // tokens
+constexpr float kLag = 4.0f;        // how far a logit may exceed the reference
+constexpr float kWeightExp = 11.0f; // weights are held times 2^11: at most 2^15
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+  uint16_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=h"(r) : "r"(a) : "memory");
+  return r;
+}
+template <int WORDS>
+__device__ __forceinline__ void lds_words(uint32_t* r, uint32_t a) {
+  if constexpr (WORDS == 1)
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(a) : "memory");
+  else if constexpr (WORDS == 2)
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
+  else
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) { return pack2<kF16>(lo, hi); }
+// 2^(byte - 127) in f32, byte 0 included.
+__device__ __forceinline__ float e8m0(uint32_t byte) {
+  return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
+}
+
+// The four byte pairs of two words, as f16 pairs: fp8 bytes (lo, hi) of 16
+// bits; fp4 nibble pairs of a byte.
+template <int FMT>
+__device__ __forceinline__ uint32_t cvt_pair(uint32_t w, int i) {
+  if constexpr (FMT == MXQ_FMT_FP8) return e4m3x2_to_f16x2((w >> (16 * i)) & 0xFFFFu);
+  else return e2m1x2_to_f16x2((w >> (8 * i)) & 0xFFu);
+}
+
+// Place of 16-byte chunk `col` of row `row` in a tile of rows of CH chunks.
+// ROWS8: read 8 rows of one chunk at a time (K, ldmatrix); else four rows two
+// apart, the whole rows in 32-lane order (V).
+template <int CH, bool ROWS8>
+__host__ __device__ constexpr int place(int row, int col) {
+  if (CH >= 8) return row * CH + (col ^ (row & 7));
+  if (CH == 4) {
+    const int line = row >> 1;
+    return line * 8 + (((row & 1) * 4 + col) ^ (ROWS8 ? (line & 3) : (line & 3) << 1));
+  }
+  const int line = row >> 2;
+  return line * 8 + (((row & 3) * 2 + col) ^ (ROWS8 ? (line & 1) : (line & 1) << 1));
+}
+
+// FMT; D: channels; NB: scales of a row; NT: tiles of 8 heads a warp carries;
+// TERMS: f16 terms of queries and weights.
+template <int FMT, int D, int NB, int NT, int TERMS>
+struct Tc {
+  static constexpr int RB = FMT == MXQ_FMT_FP8 ? D : D / 2;  // bytes of a row
+  static constexpr int CH = RB / 16;
+  static constexpr int SC = 16 * NB;  // scale bytes of a tile
+  static constexpr int STAGE = 2 * (16 * RB + SC);
+  static constexpr int MIN_CTAS = NT == 1 && TERMS == 1 && D <= 128 ? 2 : 1;
+  static constexpr int SMEM = MIN_CTAS == 2 ? 108 * 1024 : 220 * 1024;
+  static constexpr int INFO = 64 * 8;  // bytes: a warp's ring of tile places
+  static constexpr int FIT = (SMEM / kWarps - INFO) / STAGE;
+  static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+  static constexpr int PER_WARP = INFO + STAGES * STAGE;
+  static constexpr int PART = kWarps * 8 * NT * (D + 4) * 4;  // the warps' sums at the end
+  static constexpr int BYTES = kWarps * PER_WARP > PART ? kWarps * PER_WARP : PART;
+  static constexpr int CPL = D / 8;   // channels of V a lane holds
+  static constexpr int KS = D / 16;   // k steps of S
+  static constexpr int MT = D / 16;   // channel tiles of O
+  static constexpr bool kAbsolute = FMT == MXQ_FMT_NVFP4;  // scales that f16 holds
+  static constexpr bool kRelative = !kAbsolute && NB > 1;
+  static constexpr int B = D / NB;    // channels of a scale
+  static constexpr int OFF = !kRelative ? 0 : FMT == MXQ_FMT_FP8 ? 7 : 12;
+  static_assert(STAGES >= 3, "too few buffers");
+
+  // Channel of the i-th value of V that the lanes of group g hold.
+  static __device__ __forceinline__ int channel(int g, int i) {
+    return FMT == MXQ_FMT_FP8 && D == 256 ? (i >> 4) * 128 + g * 16 + (i & 15) : g * CPL + i;
+  }
+};
+
+template <class T, int FMT, int D, int NB, int NT, int TERMS>
+__device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float s_m[kWarps][8 * NT], s_r[kWarps][8 * NT], s_l[kWarps][8 * NT];
+  const PagedCache& c = a.c;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
+  uint8_t* const mine = smem + warp * T::PER_WARP;
+  int2* const info = (int2*)mine;
+  const uint32_t buf0 = sm100::smem_addr(mine + T::INFO);
+  const int tiles_per_page = c.page / kTile;
+  [[maybe_unused]] const int64_t n_tiles = c.num_pages * c.heads * tiles_per_page;
+
+  // this lane's places: 16-byte chunks it copies, rows it reads
+  uint32_t dst_k[T::CH / 2], dst_v[T::CH / 2];
+#pragma unroll
+  for (int i = 0; i < T::CH / 2; ++i) {
+    const int at = lane + 32 * i, row = at / T::CH, col = at % T::CH;
+    dst_k[i] = place<T::CH, true>(row, col) * 16;
+    dst_v[i] = 16 * T::RB + place<T::CH, false>(row, col) * 16;
+  }
+
+  walk(a, [&](const Span& s, const Target& tg, int v0, int v1) {
+    const int first = v0 / kTile + warp;
+    const int n = max(0, ((v1 + kTile - 1) / kTile - first + kWarps - 1) / kWarps);
+    const int r0 = tg.tile * 8 * NT;  // first head of the tile in its group
+
+    // Places of tiles i .. i + 31: row of the cache in tiles (or -1), and the
+    // live tokens [lo, hi) of the tile.
+    auto look_up = [&](int i) {
+      int2 p = make_int2(-1, 0);
+      if (i + lane < n) {
+        const Token tok = token_at(a, s, tg.b, tg.head, (first + (i + lane) * kWarps) * kTile);
+        if (tok.row >= 0) {
+          const int64_t start = a.window > 0 ? s.len - a.window : 0;
+          const int lo = (int)max((int64_t)0, min((int64_t)kTile, start - tok.pos));
+          const int hi = (int)max((int64_t)0, min((int64_t)kTile, s.len - tok.pos));
+          if (lo < hi) p = make_int2((int)(tok.row / kTile), lo | hi << 8);
+        }
+      }
+      info[(i + lane) & 63] = p;
+    };
+    auto issue = [&](int i) {
+      if (i < n) {
+        if ((i & 31) == 0) {
+          look_up(i);
+          __syncwarp();
+        }
+        const int tile = info[i & 63].x;
+        const uint32_t dst = buf0 + (i % T::STAGES) * T::STAGE;
+        if (tile >= 0 && MXQ_IN_RANGE(kChkAttendIn, tile, n_tiles)) {
+          const int64_t at = (int64_t)tile * (16 * T::RB) + lane * 16;
+#pragma unroll
+          for (int j = 0; j < T::CH / 2; ++j) cp_async16(dst + dst_k[j], c.k_codes + at + 512 * j);
+#pragma unroll
+          for (int j = 0; j < T::CH / 2; ++j) cp_async16(dst + dst_v[j], c.v_codes + at + 512 * j);
+          const int64_t sat = (int64_t)tile * T::SC;
+          if (lane < NB) cp_async16(dst + 32 * T::RB + lane * 16, c.k_scales + sat + lane * 16);
+          else if (lane >= 16 && lane < 16 + NB)
+            cp_async16(dst + 32 * T::RB + T::SC + (lane - 16) * 16,
+                       c.v_scales + sat + (lane - 16) * 16);
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < T::STAGES - 1; ++i) issue(i);
+
+    // Q in the layout of the second operand of S: lane (g, t) holds head g's
+    // channels, four (fp8) or eight (fp4) a chunk, in the order of the codes.
+    uint32_t q[TERMS][NT][T::KS][2];
+    float qf[NT][2];  // of columns 2 t, 2 t + 1: softmax scale x 2^(Q's exponent)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = r0 + nt * 8 + g;
+      float x[T::KS][4], top = 0.0f;
+      const int64_t at = tg.b * a.q_stride + ((int64_t)tg.head * a.group + r) * D;
+#pragma unroll
+      for (int k = 0; k < T::KS; ++k) {
+        const int ch = FMT == MXQ_FMT_FP8 ? k * 16 + t4 * 4 : (k >> 1) * 32 + t4 * 8 + (k & 1) * 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[k][j] = r < a.group ? load_q(a, dt, at + ch + j) : 0.0f;
+          top = fmaxf(top, fabsf(x[k][j]));
+        }
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // largest magnitude to [2^13, 2^14)
+      const int e = top > 0.0f ? floor_log2_f32bits(__float_as_uint(top)) - 13 : 0;
+      const float f1 = exp2i(max(-126, min(127, -(e / 2)))), f2 = exp2i(max(-126, min(127, -(e - e / 2))));
+#pragma unroll
+      for (int k = 0; k < T::KS; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float x0 = x[k][2 * j] * f1 * f2, x1 = x[k][2 * j + 1] * f1 * f2;
+          const uint32_t h = half2_of(x0, x1);
+          q[0][nt][k][j] = h;
+          if constexpr (TERMS == 2) q[1][nt][k][j] = half2_of(x0 - f16lo(h), x1 - f16hi(h));
+        }
+      const float back = a.scale_log2 * exp2f((float)e);
+      qf[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t4);
+      qf[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4);
+    }
+
+    float o[T::MT][NT][4], m[NT][2], R[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) m[nt][j] = kLowest, R[nt][j] = T::kAbsolute ? 0.0f : -256.0f, l[nt][j] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < T::MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
+    }
+
+    for (int i = 0; i < n; ++i) {
+      cp_async_wait<T::STAGES - 2>();
+      __syncwarp();
+      issue(i + T::STAGES - 1);
+      const uint32_t kb = buf0 + (i % T::STAGES) * T::STAGE, vb = kb + 16 * T::RB,
+                     ks = kb + 32 * T::RB, vs = ks + T::SC;
+      const int live_rows = info[i & 63].y, lo = live_rows & 255, hi = live_rows >> 8;
+      const bool part = lo > 0 || hi < kTile;
+      if (part) {  // rows behind the end, or before the window: no bytes of theirs count
+#pragma unroll
+        for (int j = 0; j < T::CH / 2; ++j) {
+          const int row = (lane + 32 * j) / T::CH;
+          if (row < lo || row >= hi)
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(kb + dst_v[j]), "r"(0)
+                         : "memory");
+        }
+        if constexpr (T::kAbsolute)
+          for (int j = lane; j < T::SC; j += 32)
+            if (j / NB < lo || j / NB >= hi)
+              asm volatile("st.shared.u8 [%0], %1;" ::"r"(vs + j), "h"((uint16_t)0) : "memory");
+        __syncwarp();
+      }
+
+      // ---- S = K Q^T
+      float sacc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sacc[nt][j] = 0.0f;
+      constexpr int STEPS = FMT == MXQ_FMT_FP8 ? 1 : 2;       // k steps of a chunk
+      constexpr int BLK = T::kRelative ? T::B / 16 : T::KS;   // k steps of a scale block
+      float tmp[NT][4];
+#pragma unroll
+      for (int c2 = 0; c2 < T::CH; c2 += 2) {
+        uint32_t w[4];
+        ldmatrix4(w, kb + 16 * place<T::CH, true>((lane & 7) + (lane & 8), c2 + (lane >> 4)));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int col = c2 + h;
+          uint32_t sc0 = 0, sc1 = 0;
+          if constexpr (T::kAbsolute) {  // this lane's channels: 8 of a chunk's 32
+            const int b = (col * 32 + t4 * 8) / T::B;
+            const uint32_t b0 = lds_u8(ks + g * NB + b), b1 = lds_u8(ks + (g + 8) * NB + b);
+            sc0 = e4m3x2_to_f16x2(b0 | b0 << 8);
+            sc1 = e4m3x2_to_f16x2(b1 | b1 << 8);
+          }
+#pragma unroll
+          for (int st = 0; st < STEPS; ++st) {
+            const int k = col * STEPS + st;
+            uint32_t f[4] = {cvt_pair<FMT>(w[2 * h], 2 * st), cvt_pair<FMT>(w[2 * h + 1], 2 * st),
+                             cvt_pair<FMT>(w[2 * h], 2 * st + 1),
+                             cvt_pair<FMT>(w[2 * h + 1], 2 * st + 1)};
+            if constexpr (T::kAbsolute) {
+              f[0] = hmul2(f[0], sc0);
+              f[1] = hmul2(f[1], sc1);
+              f[2] = hmul2(f[2], sc0);
+              f[3] = hmul2(f[3], sc1);
+            }
+            if (k % BLK == 0) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) tmp[nt][j] = 0.0f;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int tm = 0; tm < TERMS; ++tm) mma16816(tmp[nt], f, q[tm][nt][k][0], q[tm][nt][k][1]);
+            if (k % BLK == BLK - 1) {
+              float f0 = 1.0f, f1 = 1.0f;
+              if constexpr (!T::kAbsolute) {
+                const int b = k / BLK;
+                f0 = e8m0(lds_u8(ks + g * NB + b));
+                f1 = e8m0(lds_u8(ks + (g + 8) * NB + b));
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                sacc[nt][0] = fmaf(tmp[nt][0], f0, sacc[nt][0]);
+                sacc[nt][1] = fmaf(tmp[nt][1], f0, sacc[nt][1]);
+                sacc[nt][2] = fmaf(tmp[nt][2], f1, sacc[nt][2]);
+                sacc[nt][3] = fmaf(tmp[nt][3], f1, sacc[nt][3]);
+              }
+            }
+          }
+        }
+      }
+
+      // ---- V's scale exponents: r of tokens g and g + 8 (less 127)
+      uint32_t rb0 = 0, rb1 = 0;
+      if constexpr (!T::kAbsolute) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          rb0 = max(rb0, lds_u8(vs + g * NB + j));
+          rb1 = max(rb1, lds_u8(vs + (g + 8) * NB + j));
+        }
+      }
+      const float rf0 = T::kAbsolute ? 0.0f : (float)(int)rb0 - 127.0f,
+                  rf1 = T::kAbsolute ? 0.0f : (float)(int)rb1 - 127.0f;
+
+      // ---- softmax; columns 2 t and 2 t + 1, rows g (0, 1) and g + 8 (2, 3)
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float x = sacc[nt][j] * qf[nt][j & 1];
+          if (part) {
+            const int row = j < 2 ? g : g + 8;
+            if (row < lo || row >= hi) x = -__int_as_float(0x7F800000);
+          }
+          sacc[nt][j] = x;
+          const float d = x - m[nt][j & 1];
+          over |= d > kLag;
+          if constexpr (!T::kAbsolute) over |= d + ((j < 2 ? rf0 : rf1) - R[nt][j & 1]) > kLag;
+        }
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float mx = fmaxf(sacc[nt][j], sacc[nt][j + 2]);
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+            const float mn = fmaxf(m[nt][j], mx), dm = m[nt][j] - mn;
+            float Rn = R[nt][j];
+            if constexpr (!T::kAbsolute) {
+              Rn = fmaxf(ceilf(sacc[nt][j] - mn + rf0), ceilf(sacc[nt][j + 2] - mn + rf1));
+#pragma unroll
+              for (int w = 4; w < 32; w <<= 1) Rn = fmaxf(Rn, __shfl_xor_sync(0xffffffffu, Rn, w));
+              Rn = fmaxf(fmaxf(Rn, -256.0f), ceilf(R[nt][j] + dm));
+            }
+            l[nt][j] *= ex2(dm);
+            const float fo = ex2(dm + (R[nt][j] - Rn));
+#pragma unroll
+            for (int mt = 0; mt < T::MT; ++mt) o[mt][nt][j] *= fo, o[mt][nt][j + 2] *= fo;
+            m[nt][j] = mn;
+            R[nt][j] = Rn;
+          }
+      }
+      uint32_t p[TERMS][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float d = sacc[nt][j] - m[nt][j & 1], e = ex2(d);
+          l[nt][j & 1] += e;
+          if constexpr (T::kAbsolute) x[j] = e * 2048.0f;
+          else x[j] = ex2(d + ((j < 2 ? rf0 : rf1) - R[nt][j & 1] + kWeightExp));
+        }
+        const uint32_t h0 = half2_of(x[0], x[1]), h1 = half2_of(x[2], x[3]);
+        p[0][nt][0] = sm100::movmatrix_trans(h0);
+        p[0][nt][1] = sm100::movmatrix_trans(h1);
+        if constexpr (TERMS == 2) {
+          p[1][nt][0] = sm100::movmatrix_trans(half2_of(x[0] - f16lo(h0), x[1] - f16hi(h0)));
+          p[1][nt][1] = sm100::movmatrix_trans(half2_of(x[2] - f16lo(h1), x[3] - f16hi(h1)));
+        }
+      }
+
+      // ---- O^T += V^T P^T: tokens 2 t, 2 t + 1 and 8 more; channels of group g
+      uint32_t ra = 0, rb = 0;  // r of tokens 2t (low) and 2t + 8 (high); 2t + 1, 2t + 9
+      if constexpr (T::kRelative) {
+        const uint32_t both = rb0 | rb1 << 16;
+        ra = __shfl_sync(0xffffffffu, both, 8 * t4);
+        rb = __shfl_sync(0xffffffffu, both, 8 * t4 + 4);
+      }
+      constexpr int LB = T::RB / 8 < 16 ? T::RB / 8 : 16;  // bytes of one read
+      constexpr int READS = T::RB / 8 / LB, W = LB / 4;
+#pragma unroll
+      for (int rd = 0; rd < READS; ++rd) {
+        uint32_t w[4][W];  // tokens 2t, 2t+1, 2t+8, 2t+9
+        const int col = (g * LB) / 16 + 8 * rd, in = (g * LB) % 16;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = 2 * t4 + (k & 1) + 8 * (k >> 1);
+          lds_words<W>(w[k], vb + 16 * place<T::CH, false>(row, col) + in);
+        }
+        constexpr int PER_WORD = FMT == MXQ_FMT_FP8 ? 4 : 8;  // channels
+        uint32_t sc[2] = {0, 0};
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const int ch0 = j * PER_WORD;  // of this read
+          // the scales of this lane's block: tokens (2t, 2t+1), (2t+8, 2t+9)
+          constexpr int SPAN = T::B / PER_WORD < W ? T::B / PER_WORD : W;  // words of one scale
+          if constexpr (T::kAbsolute || T::kRelative) {
+            if (j % SPAN == 0) {
+              const int b = T::channel(g, rd * W * PER_WORD + ch0) / T::B;
+              uint32_t x[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                x[k] = lds_u8(vs + (2 * t4 + (k & 1) + 8 * (k >> 1)) * NB + b);
+              if constexpr (T::kAbsolute) {
+                sc[0] = e4m3x2_to_f16x2(x[0] | x[1] << 8);
+                sc[1] = e4m3x2_to_f16x2(x[2] | x[3] << 8);
+              } else {
+                const int r[4] = {(int)(ra & 0xFFFF), (int)(rb & 0xFFFF), (int)(ra >> 16),
+                                  (int)(rb >> 16)};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  x[k] = (uint32_t)max(0, (int)x[k] - r[k] + T::OFF + 15) << 10;
+                sc[0] = x[0] | x[1] << 16;
+                sc[1] = x[2] | x[3] << 16;
+              }
+            }
+          }
+          uint32_t pr[2][2];  // token pairs, paired codes
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t A = w[2 * k][j], Bw = w[2 * k + 1][j];
+            if constexpr (FMT == MXQ_FMT_FP8) {
+              pr[k][0] = __byte_perm(A, Bw, 0x5140);
+              pr[k][1] = __byte_perm(A, Bw, 0x7362);
+            } else {
+              pr[k][0] = (A & 0x0F0F0F0Fu) | ((Bw << 4) & 0xF0F0F0F0u);
+              pr[k][1] = ((A >> 4) & 0x0F0F0F0Fu) | (Bw & 0xF0F0F0F0u);
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < PER_WORD / 2; ++h) {  // two channels: one tile of O
+            uint32_t f[4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              if constexpr (FMT == MXQ_FMT_FP8) {  // channels 2h, 2h + 1: both in word h
+                f[2 * k] = cvt_pair<FMT>(pr[k][h], 0);
+                f[2 * k + 1] = cvt_pair<FMT>(pr[k][h], 1);
+              } else {  // channel 2h: low nibbles' word, 2h + 1: high nibbles'
+                f[2 * k] = cvt_pair<FMT>(pr[k][0], h);
+                f[2 * k + 1] = cvt_pair<FMT>(pr[k][1], h);
+              }
+              if constexpr (T::kAbsolute || T::kRelative) {
+                f[2 * k] = hmul2(f[2 * k], sc[k]);
+                f[2 * k + 1] = hmul2(f[2 * k + 1], sc[k]);
+              }
+            }
+            const int mt = (rd * W * PER_WORD + ch0) / 2 + h;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int tm = 0; tm < TERMS; ++tm) mma16816(o[mt][nt], f, p[tm][nt][0], p[tm][nt][1]);
+          }
+        }
+      }
+    }
+
+    // ---- join the warps: [warp][head][value * 8 + group], rows of D + 4
+    cp_async_wait<0>();
+    __syncthreads();
+    float* const sums = (float*)smem;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int head = nt * 8 + 2 * t4 + j;
+        float* row = sums + (warp * 8 * NT + head) * (D + 4);
+#pragma unroll
+        for (int mt = 0; mt < T::MT; ++mt) {
+          row[(2 * mt) * 8 + g] = o[mt][nt][j];
+          row[(2 * mt + 1) * 8 + g] = o[mt][nt][j + 2];
+        }
+        float lt = l[nt][j];
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, w);
+        if (g == 0) {
+          s_m[warp][head] = m[nt][j];
+          s_r[warp][head] = R[nt][j];
+          s_l[warp][head] = lt;
+        }
+      }
+    __syncthreads();
+    const int heads = min(8 * NT, a.group - r0);
+    for (int i = threadIdx.x; i < heads * D; i += kThreads) {
+      const int r = i / D, at = i - r * D, v = at >> 3, gr = at & 7;
+      float top = kLowest, ref = -1.0e30f, sum = 0.0f, val = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        if (s_l[w][r] > 0.0f) ref = fmaxf(ref, s_m[w][r] - top + s_r[w][r]);
+      ref = ceilf(ref);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (!(s_l[w][r] > 0.0f)) continue;
+        const float d = s_m[w][r] - top;
+        sum = fmaf(s_l[w][r], exp2f(d), sum);
+        val = fmaf(sums[(w * 8 * NT + r) * (D + 4) + at], exp2f(d + s_r[w][r] - ref), val);
+      }
+      const float back = ref - kWeightExp - (float)T::OFF, half = truncf(back * 0.5f);
+      put(a, dt, tg, r, T::channel(gr, v),
+          sum > 0.0f ? val / sum * exp2f(half) * exp2f(back - half) : 0.0f);
+      if (at == 0) put_weight(a, tg, r, sum > 0.0f ? top + log2f(sum) : kLowest);
+    }
+    __syncthreads();  // the buffers are the next pair's
+  });
+}
+
+template <int FMT, int D, int NB, int NT, int TERMS>
+__global__ void __launch_bounds__(kThreads, Tc<FMT, D, NB, NT, TERMS>::MIN_CTAS)
+attend_tc_kernel(Args a, int dt) {
+  attend_tc_body<Tc<FMT, D, NB, NT, TERMS>, FMT, D, NB, NT, TERMS>(a, dt);
+}
+
+// Launch one instance on at most max_ctas blocks.
+template <int FMT, int D, int NB, int NT, int TERMS>
+int launch_tc(const Args& a, int dt, int64_t units, int* grid, cudaStream_t st) {
+  using T = Tc<FMT, D, NB, NT, TERMS>;
+  auto kernel = attend_tc_kernel<FMT, D, NB, NT, TERMS>;
+  if (allow_dynamic_smem((const void*)kernel, T::BYTES) != cudaSuccess) return MXQ_ERR_CUDA;
+  const int64_t ctas = (int64_t)T::MIN_CTAS * num_sms();
+  *grid = (int)(units < ctas ? units : ctas);
+  kernel<<<*grid, kThreads, T::BYTES, st>>>(a, dt);
+  return MXQ_OK;
+}
+
+// One format's launcher for head size D and NB scales a row.
+template <int FMT, int D, int NB>
+int launch_tc_dt(const Args& a, int dt, int64_t units, int* grid, cudaStream_t st) {
+  if (dt != kBF16) return launch_tc<FMT, D, NB, 1, 2>(a, dt, units, grid, st);
+  if constexpr (D <= 128)
+    if (a.tile_heads == 16) return launch_tc<FMT, D, NB, 2, 1>(a, dt, units, grid, st);
+  return launch_tc<FMT, D, NB, 1, 1>(a, dt, units, grid, st);
+}
+
+}  // namespace attend
+}  // namespace mxq

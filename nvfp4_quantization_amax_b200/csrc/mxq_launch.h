@@ -97,6 +97,10 @@ int check_record_w4a4(unsigned long long* out);
 int check_record_cache_paged(unsigned long long* out);
 int check_record_cache_select(unsigned long long* out);
 int check_record_cache_attend(unsigned long long* out);
+int check_record_attend_fp8_64(unsigned long long* out);
+int check_record_attend_fp8_128(unsigned long long* out);
+int check_record_attend_fp8_256(unsigned long long* out);
+int check_record_attend_fp4(unsigned long long* out);
 int launch_grouped_mm(const void* a, const void* packed, const void* scales, const int32_t* offs,
                       int64_t T, int64_t E, int64_t N, int64_t K, int transpose_w, void* y,
                       int32_t* dev_status, cudaStream_t st);
