@@ -8,6 +8,7 @@
 //   m' = max(m, s), l = l 2^(m-m') + 2^(s-m'), o = o 2^(m-m') + 2^(s-m') v.
 // The warps' sums are joined in shared memory in a fixed order.
 #include "cache_attend.cuh"
+#include "sm100_primitives.cuh"
 
 namespace mxq {
 
@@ -115,12 +116,17 @@ __global__ void __launch_bounds__(kThreads) attend_general_kernel(Args a, int dt
 }
 
 // Join the parts of a split pair: out = sum_i o_i 2^(l_i - L), L = log2 sum
-// 2^l_i.  One block per (block of the line, head of the tile); a block whose
-// line part begins no split pair has nothing to do.
-__global__ void __launch_bounds__(kThreads) join_kernel(Args a, int dt, int n_ctas) {
-  __shared__ float s_l[kThreads];
+// 2^l_i.  One block per (block of the line, some heads of the tile); a block
+// whose line part begins no split pair has nothing to do.  `per_head` warps
+// share a head's parts (a power of two, set by how many there can be), lanes
+// hold channels; the warps' sums are added in a fixed order.
+template <int NC>
+__global__ void __launch_bounds__(kThreads) join_kernel(Args a, int dt, int n_ctas, int per_head) {
+  extern __shared__ float s_part[];  // [warps][dim + 1]
   __shared__ int s_count;
-  const int cta = blockIdx.x, r = blockIdx.y, D = a.c.dim;
+  const int cta = blockIdx.x, D = a.c.dim;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  sm100::griddep_wait();
   const int32_t pair1 = a.hdr[2 * cta + 1];
   if (pair1 == 0) return;
   const int64_t pairs = (int64_t)a.c.heads * a.head_tiles, pair = pair1 - 1;
@@ -131,36 +137,80 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Args a, int dt, int n_ct
   t.tile = pl - t.head * a.head_tiles;
   t.whole = true;
   t.slot = 0;
-  if (t.tile * a.tile_heads + r >= a.group) return;
   // the blocks behind this one that hold the pair's further parts
   if (threadIdx.x == 0) s_count = n_ctas - 1 - cta;
   __syncthreads();
   for (int i = cta + 1 + threadIdx.x; i < n_ctas; i += kThreads)
-    if (a.hdr[2 * i] != pair1) atomicMin(&s_count, i - cta - 1);
+    if (a.hdr[2 * i] != pair1) {
+      atomicMin(&s_count, i - cta - 1);
+      break;
+    }
   __syncthreads();
   const int parts = 1 + s_count;
-  auto slot = [&](int i) { return i == 0 ? 2 * cta + 1 : 2 * (cta + i); };
-  float top = kLowest;
-  for (int i = threadIdx.x; i < parts; i += kThreads)
-    top = fmaxf(top, a.part_l[(int64_t)slot(i) * a.tile_heads + r]);
-  s_l[threadIdx.x] = top;
-  __syncthreads();
-  for (int w = kThreads / 2; w > 0; w >>= 1) {
-    if ((int)threadIdx.x < w) s_l[threadIdx.x] = fmaxf(s_l[threadIdx.x], s_l[threadIdx.x + w]);
-    __syncthreads();
-  }
-  top = s_l[0];
-  for (int ch = threadIdx.x; ch < D; ch += kThreads) {
-    float sum = 0.0f, val = 0.0f;
-    for (int i = 0; i < parts; ++i) {
-      const int64_t at = (int64_t)slot(i) * a.tile_heads + r;
+  const int r = (blockIdx.y * kWarps + warp) / per_head, share = warp & (per_head - 1);
+  const bool have = r < min(a.tile_heads, a.group - t.tile * a.tile_heads);
+  auto place = [&](int i) {
+    return (int64_t)(i == 0 ? 2 * cta + 1 : 2 * (cta + i)) * a.tile_heads + r;
+  };
+  float top = kLowest, sum = 0.0f, val[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) val[i] = 0.0f;
+  if (have) {
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_l[place(i)]);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+#pragma unroll 4
+    for (int i = share; i < parts; i += per_head) {
+      const int64_t at = place(i);
       const float l = a.part_l[at], f = l <= kLowest ? 0.0f : exp2f(l - top);
       sum += f;
-      val = fmaf(a.part_o[at * D + ch], f, val);
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+        if (lane + 32 * j < D) val[j] = fmaf(a.part_o[at * D + lane + 32 * j], f, val[j]);
     }
-    put(a, dt, t, r, ch, sum > 0.0f ? val / sum : 0.0f);
-    if (ch == 0) put_weight(a, t, r, sum > 0.0f ? top + log2f(sum) : kLowest);
   }
+  float* mine = s_part + warp * (D + 1);
+#pragma unroll
+  for (int j = 0; j < NC; ++j)
+    if (lane + 32 * j < D) mine[lane + 32 * j] = val[j];
+  if (lane == 0) mine[D] = sum;
+  __syncthreads();
+  if (!have || share != 0) return;
+  for (int w = 1; w < per_head; ++w) {
+    const float* other = mine + w * (D + 1);
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      if (lane + 32 * j < D) val[j] += other[lane + 32 * j];
+    sum += other[D];
+  }
+#pragma unroll
+  for (int j = 0; j < NC; ++j)
+    if (lane + 32 * j < D) put(a, dt, t, r, lane + 32 * j, sum > 0.0f ? val[j] / sum : 0.0f);
+  if (lane == 0) put_weight(a, t, r, sum > 0.0f ? top + log2f(sum) : kLowest);
+}
+
+// Launched with programmatic stream serialization: it takes its place while
+// the attention kernel's last blocks run and waits for them on the device.
+int launch_join(const Args& a, int dt, int grid, cudaStream_t st) {
+  const int64_t pairs = a.c.n_seqs * a.c.heads * a.head_tiles;
+  const int64_t parts = grid / pairs + 2;  // of an average pair
+  int per_head = 1;
+  while (per_head < kWarps && per_head * 4 < parts) per_head *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)((a.tile_heads * per_head + kWarps - 1) / kWarps));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kWarps * (a.c.dim + 1) * 4;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t err;
+  if (a.c.dim <= 128) err = cudaLaunchKernelEx(&cfg, join_kernel<4>, a, dt, grid, per_head);
+  else if (a.c.dim <= 256) err = cudaLaunchKernelEx(&cfg, join_kernel<8>, a, dt, grid, per_head);
+  else err = cudaLaunchKernelEx(&cfg, join_kernel<16>, a, dt, grid, per_head);
+  return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
 
 template <int FMT>
@@ -252,8 +302,7 @@ int launch_attend_cache_paged(const void* q, int dt, int64_t q_heads, int64_t q_
   else if (c.fmt == MXQ_FMT_MXFP4) rc = launch_general<MXQ_FMT_MXFP4>(a, dt, grid, st);
   else rc = launch_general<MXQ_FMT_NVFP4>(a, dt, grid, st);
   if (rc != MXQ_OK) return rc;
-  join_kernel<<<dim3((unsigned)grid, (unsigned)a.tile_heads), kThreads, 0, st>>>(a, dt, grid);
-  return cudaGetLastError() == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
+  return launch_join(a, dt, grid, st);
 }
 
 MXQ_DEFINE_CHECK_READER(check_record_cache_attend)

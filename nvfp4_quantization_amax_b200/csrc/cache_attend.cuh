@@ -1,8 +1,9 @@
 // Attention of one new token over a paged packed cache: how the work is laid
 // over the grid, shared by the general and the tensor-core kernel.
 //
-// The positions of every (sequence, kv head, tile of query heads) are cut into
-// units of 128, the pairs' units are laid in one line, and block i of n takes
+// The positions of every (sequence, kv head, tile of query heads), a pair, are
+// cut into units of 128, the pairs' units are laid in one line, each behind a
+// few units' length for what a pair costs by itself, and block i of n takes
 // the i-th n-th of the line: sequences of any lengths keep all SMs busy for
 // the same time, without a plan made on the host.  A block that holds all
 // units of a pair writes its output; where a pair's units fall to several
@@ -23,6 +24,9 @@ namespace mxq {
 namespace attend {
 
 constexpr int kUnit = 128;  // positions
+// What a pair costs beside its units (queries, the first loads' latency, the
+// join of the warps), in units: the line is laid in units plus this.
+constexpr int kPairCost = 6;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 // Before any token: finite, so that no difference of two of them is NaN.
@@ -118,8 +122,8 @@ __device__ __forceinline__ float load_q(const Args& a, int dt, int64_t i) {
 // Where a block's part of the line begins: units before it and its first
 // sequence.  All threads of the block call it.
 struct Part {
-  int64_t begin, end;  // units of the line
-  int64_t b, b_begin;  // the sequence of unit begin and that sequence's first unit
+  int64_t begin, end;  // of the line
+  int64_t b, b_begin;  // the sequence at begin and where it starts
 };
 
 __device__ __forceinline__ Part part_of(const Args& a) {
@@ -129,7 +133,7 @@ __device__ __forceinline__ Part part_of(const Args& a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t total = 0;
   for (int64_t b = threadIdx.x; b < a.c.n_seqs; b += kThreads)
-    total += pairs * span_of(a, b).units;
+    total += pairs * (span_of(a, b).units + kPairCost);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   if (lane == 0) s_sum[warp] = total;
@@ -139,15 +143,16 @@ __device__ __forceinline__ Part part_of(const Args& a) {
   for (int i = 0; i < kWarps; ++i) total += s_sum[i];
   __syncthreads();
   Part p;
-  // never more blocks than units: the parts of a pair lie in blocks that follow
-  // one another
-  const int64_t n = total < gridDim.x ? total : gridDim.x;
+  // no part is shorter than two units: the parts of a pair lie in blocks that
+  // follow one another, and are worth their join
+  const int64_t most = total / 2;
+  const int64_t n = most < gridDim.x ? most : gridDim.x;
   p.begin = min(total, total * blockIdx.x / n);
   p.end = min(total, total * (blockIdx.x + 1) / n);
   int64_t before = 0;
   for (int64_t b0 = 0; b0 < a.c.n_seqs; b0 += kThreads) {
     const int64_t b = b0 + threadIdx.x;
-    const int64_t mine = b < a.c.n_seqs ? pairs * span_of(a, b).units : 0;
+    const int64_t mine = b < a.c.n_seqs ? pairs * (span_of(a, b).units + kPairCost) : 0;
     int64_t sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -216,19 +221,22 @@ __device__ __forceinline__ void walk(const Args& a, Work work) {
   int64_t u = p.begin, b = p.b, b_begin = p.b_begin;
   while (u < p.end) {
     const Span s = span_of(a, b);
-    const int64_t pl = (u - b_begin) / s.units;  // pair of the sequence
-    const int j0 = (int)(u - b_begin - pl * s.units);
-    const int j1 = (int)min((int64_t)s.units, j0 + (p.end - u));
+    const int64_t length = s.units + kPairCost;
+    const int64_t pl = (u - b_begin) / length;  // pair of the sequence
+    const int64_t x0 = u - b_begin - pl * length, x1 = min(length, x0 + (p.end - u));
+    const int j0 = (int)max((int64_t)0, x0 - kPairCost), j1 = (int)max((int64_t)0, x1 - kPairCost);
     Target t;
     t.b = b;
     t.head = (int)(pl / a.head_tiles);
     t.tile = (int)(pl - (int64_t)t.head * a.head_tiles);
     t.whole = j0 == 0 && j1 == s.units;
     t.slot = 2 * blockIdx.x + (j0 == 0 ? 1 : 0);
-    if (!t.whole) hdr[j0 == 0 ? 1 : 0] = (int32_t)(b * pairs + pl + 1);
-    work(s, t, j0 * kUnit, min(s.n, j1 * kUnit));
-    u += j1 - j0;
-    if (u == b_begin + pairs * s.units) {
+    if (j1 > j0) {
+      if (!t.whole) hdr[j0 == 0 ? 1 : 0] = (int32_t)(b * pairs + pl + 1);
+      work(s, t, j0 * kUnit, min(s.n, j1 * kUnit));
+    }
+    u += x1 - x0;
+    if (u == b_begin + pairs * length) {
       b_begin = u;
       ++b;
     }

@@ -80,22 +80,24 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
-  uint16_t r;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=h"(r) : "r"(a) : "memory");
-  return r;
-}
-template <int WORDS>
-__device__ __forceinline__ void lds_words(uint32_t* r, uint32_t a) {
-  if constexpr (WORDS == 1)
+// BYTES (a power of two) bytes of shared memory, little-endian in words.
+template <int BYTES>
+__device__ __forceinline__ void lds_bytes(uint32_t* r, uint32_t a) {
+  if constexpr (BYTES <= 2) {
+    uint16_t h;
+    if constexpr (BYTES == 1) asm volatile("ld.shared.u8 %0, [%1];" : "=h"(h) : "r"(a) : "memory");
+    else asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(a) : "memory");
+    r[0] = h;
+  } else if constexpr (BYTES == 4) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(a) : "memory");
-  else if constexpr (WORDS == 2)
+  } else if constexpr (BYTES == 8) {
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
-  else
+  } else {
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(a)
                  : "memory");
+  }
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -103,17 +105,35 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) { return pack2<kF16>(lo, hi); }
-// 2^(byte - 127) in f32, byte 0 included.
-__device__ __forceinline__ float e8m0(uint32_t byte) {
-  return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
+// Two E8M0 bytes (low first) as f32.
+__device__ __forceinline__ void e8m0x2(uint32_t two, float& lo, float& hi) {
+  uint32_t b;
+  asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(b) : "h"((uint16_t)two));
+  lo = __uint_as_float(b << 16);
+  hi = __uint_as_float(b & 0xFFFF0000u);
 }
 
-// The four byte pairs of two words, as f16 pairs: fp8 bytes (lo, hi) of 16
-// bits; fp4 nibble pairs of a byte.
+// The values of a word of codes as f16 pairs in the codes' order: two of four
+// E4M3 bytes, four of eight E2M1 nibbles.  The unpacking of the word inside
+// the asm lets each conversion take its byte where it lies.
 template <int FMT>
-__device__ __forceinline__ uint32_t cvt_pair(uint32_t w, int i) {
-  if constexpr (FMT == MXQ_FMT_FP8) return e4m3x2_to_f16x2((w >> (16 * i)) & 0xFFFFu);
-  else return e2m1x2_to_f16x2((w >> (8 * i)) & 0xFFu);
+struct Codes {
+  static constexpr int kPairs = FMT == MXQ_FMT_FP8 ? 2 : 4;
+};
+template <int FMT>
+__device__ __forceinline__ void decode_word(uint32_t w, uint32_t* r) {
+  if constexpr (FMT == MXQ_FMT_FP8) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(r[0]), "=r"(r[1])
+        : "r"(w));
+  } else {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(w));
+  }
 }
 
 // Place of 16-byte chunk `col` of row `row` in a tile of rows of CH chunks.
@@ -202,6 +222,11 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
       }
       info[(i + lane) & 63] = p;
     };
+    uint32_t fill = buf0, use = buf0;  // the buffers to load and to read next
+    auto next = [&](uint32_t at) {
+      at += T::STAGE;
+      return at == buf0 + T::STAGES * T::STAGE ? buf0 : at;
+    };
     auto issue = [&](int i) {
       if (i < n) {
         if ((i & 31) == 0) {
@@ -209,7 +234,7 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
           __syncwarp();
         }
         const int tile = info[i & 63].x;
-        const uint32_t dst = buf0 + (i % T::STAGES) * T::STAGE;
+        const uint32_t dst = fill;
         if (tile >= 0 && MXQ_IN_RANGE(kChkAttendIn, tile, n_tiles)) {
           const int64_t at = (int64_t)tile * (16 * T::RB) + lane * 16;
 #pragma unroll
@@ -223,6 +248,7 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
                        c.v_scales + sat + (lane - 16) * 16);
         }
       }
+      fill = next(fill);
       cp_async_commit();
     };
 #pragma unroll
@@ -265,11 +291,14 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
       qf[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4);
     }
 
+    // R is kept as R + 2^23 + 127 - 11: a scale byte in the low bits of 2^23's
+    // pattern less that is the byte's exponent - R + 11, exactly
+    constexpr float kShift = 8388608.0f + 127.0f - kWeightExp;
     float o[T::MT][NT][4], m[NT][2], R[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) m[nt][j] = kLowest, R[nt][j] = T::kAbsolute ? 0.0f : -256.0f, l[nt][j] = 0.0f;
+      for (int j = 0; j < 2; ++j) m[nt][j] = kLowest, R[nt][j] = kShift - 256.0f, l[nt][j] = 0.0f;
 #pragma unroll
       for (int i = 0; i < T::MT; ++i)
 #pragma unroll
@@ -280,8 +309,8 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
       cp_async_wait<T::STAGES - 2>();
       __syncwarp();
       issue(i + T::STAGES - 1);
-      const uint32_t kb = buf0 + (i % T::STAGES) * T::STAGE, vb = kb + 16 * T::RB,
-                     ks = kb + 32 * T::RB, vs = ks + T::SC;
+      const uint32_t kb = use, vb = kb + 16 * T::RB, ks = kb + 32 * T::RB, vs = ks + T::SC;
+      use = next(use);
       const int live_rows = info[i & 63].y, lo = live_rows & 255, hi = live_rows >> 8;
       const bool part = lo > 0 || hi < kTile;
       if (part) {  // rows behind the end, or before the window: no bytes of theirs count
@@ -300,14 +329,30 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
       }
 
       // ---- S = K Q^T
-      float sacc[NT][4];
+      uint32_t sw0[(NB + 3) / 4], sw1[(NB + 3) / 4];  // scale bytes of tokens g, g + 8
+      lds_bytes<NB>(sw0, ks + g * NB);
+      lds_bytes<NB>(sw1, ks + (g + 8) * NB);
+      float sacc[NT][4], tmp[NT][4];
+      constexpr int STEPS = Codes<FMT>::kPairs / 2;          // k steps of a chunk
+      constexpr int BLK = T::kRelative ? T::B / 16 : T::KS;  // k steps of a scale block
+      uint32_t abs0[T::CH], abs1[T::CH];  // nvfp4: this lane's scale of each chunk, twice
+      if constexpr (T::kAbsolute) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int q4 = 0; q4 < (T::CH + 3) / 4; ++q4) {
+          const uint32_t sel = t4 < 2 ? 0x6420 : 0x7531;  // 8 of a chunk's 32 channels
+          const uint32_t x0 = __byte_perm(sw0[2 * q4], NB > 4 ? sw0[2 * q4 + 1 < (NB + 3) / 4 ? 2 * q4 + 1 : 0] : 0u, sel);
+          const uint32_t x1 = __byte_perm(sw1[2 * q4], NB > 4 ? sw1[2 * q4 + 1 < (NB + 3) / 4 ? 2 * q4 + 1 : 0] : 0u, sel);
+          uint32_t y0[2], y1[2];
+          decode_word<MXQ_FMT_FP8>(x0, y0);
+          decode_word<MXQ_FMT_FP8>(x1, y1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sacc[nt][j] = 0.0f;
-      constexpr int STEPS = FMT == MXQ_FMT_FP8 ? 1 : 2;       // k steps of a chunk
-      constexpr int BLK = T::kRelative ? T::B / 16 : T::KS;   // k steps of a scale block
-      float tmp[NT][4];
+          for (int j = 0; j < 4; ++j)
+            if (q4 * 4 + j < T::CH) {
+              abs0[q4 * 4 + j] = __byte_perm(y0[j >> 1], 0, j & 1 ? 0x3232 : 0x1010);
+              abs1[q4 * 4 + j] = __byte_perm(y1[j >> 1], 0, j & 1 ? 0x3232 : 0x1010);
+            }
+        }
+      }
 #pragma unroll
       for (int c2 = 0; c2 < T::CH; c2 += 2) {
         uint32_t w[4];
@@ -315,24 +360,18 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int col = c2 + h;
-          uint32_t sc0 = 0, sc1 = 0;
-          if constexpr (T::kAbsolute) {  // this lane's channels: 8 of a chunk's 32
-            const int b = (col * 32 + t4 * 8) / T::B;
-            const uint32_t b0 = lds_u8(ks + g * NB + b), b1 = lds_u8(ks + (g + 8) * NB + b);
-            sc0 = e4m3x2_to_f16x2(b0 | b0 << 8);
-            sc1 = e4m3x2_to_f16x2(b1 | b1 << 8);
-          }
+          uint32_t x0[4], x1[4];
+          decode_word<FMT>(w[2 * h], x0);
+          decode_word<FMT>(w[2 * h + 1], x1);
 #pragma unroll
           for (int st = 0; st < STEPS; ++st) {
             const int k = col * STEPS + st;
-            uint32_t f[4] = {cvt_pair<FMT>(w[2 * h], 2 * st), cvt_pair<FMT>(w[2 * h + 1], 2 * st),
-                             cvt_pair<FMT>(w[2 * h], 2 * st + 1),
-                             cvt_pair<FMT>(w[2 * h + 1], 2 * st + 1)};
+            uint32_t f[4] = {x0[2 * st], x1[2 * st], x0[2 * st + 1], x1[2 * st + 1]};
             if constexpr (T::kAbsolute) {
-              f[0] = hmul2(f[0], sc0);
-              f[1] = hmul2(f[1], sc1);
-              f[2] = hmul2(f[2], sc0);
-              f[3] = hmul2(f[3], sc1);
+              f[0] = hmul2(f[0], abs0[col]);
+              f[1] = hmul2(f[1], abs1[col]);
+              f[2] = hmul2(f[2], abs0[col]);
+              f[3] = hmul2(f[3], abs1[col]);
             }
             if (k % BLK == 0) {
 #pragma unroll
@@ -345,67 +384,103 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 #pragma unroll
               for (int tm = 0; tm < TERMS; ++tm) mma16816(tmp[nt], f, q[tm][nt][k][0], q[tm][nt][k][1]);
             if (k % BLK == BLK - 1) {
+              const int b = k / BLK;
               float f0 = 1.0f, f1 = 1.0f;
               if constexpr (!T::kAbsolute) {
-                const int b = k / BLK;
-                f0 = e8m0(lds_u8(ks + g * NB + b));
-                f1 = e8m0(lds_u8(ks + (g + 8) * NB + b));
+                float skip;
+                const int at = (b & 3) >> 1;  // half of its word
+                if (b & 1) {
+                  e8m0x2(sw0[b >> 2] >> (16 * at), skip, f0);
+                  e8m0x2(sw1[b >> 2] >> (16 * at), skip, f1);
+                } else {
+                  e8m0x2(sw0[b >> 2] >> (16 * at), f0, skip);
+                  e8m0x2(sw1[b >> 2] >> (16 * at), f1, skip);
+                }
               }
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                sacc[nt][0] = fmaf(tmp[nt][0], f0, sacc[nt][0]);
-                sacc[nt][1] = fmaf(tmp[nt][1], f0, sacc[nt][1]);
-                sacc[nt][2] = fmaf(tmp[nt][2], f1, sacc[nt][2]);
-                sacc[nt][3] = fmaf(tmp[nt][3], f1, sacc[nt][3]);
-              }
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float fj = j < 2 ? f0 : f1;
+                  if constexpr (T::kAbsolute) sacc[nt][j] = tmp[nt][j];
+                  else if (b == 0) sacc[nt][j] = tmp[nt][j] * fj;
+                  else sacc[nt][j] = fmaf(tmp[nt][j], fj, sacc[nt][j]);
+                }
             }
           }
         }
       }
 
-      // ---- V's scale exponents: r of tokens g and g + 8 (less 127)
-      uint32_t rb0 = 0, rb1 = 0;
+      // ---- V's scale bytes: the largest r of tokens g (low half) and g + 8
+      uint32_t both = 0;
+      float rf0 = 0.0f, rf1 = 0.0f;  // 2^23 + r
       if constexpr (!T::kAbsolute) {
+        lds_bytes<NB>(sw0, vs + g * NB);
+        lds_bytes<NB>(sw1, vs + (g + 8) * NB);
+        if constexpr (NB == 1) {
+          both = sw0[0] | sw1[0] << 16;
+        } else if constexpr (NB == 2) {
+          const uint32_t y = __byte_perm(sw0[0], sw1[0], 0x5410);  // two bytes of each
+          both = __vmaxu2(y & 0x00FF00FFu, (y >> 8) & 0x00FF00FFu);
+        } else {
+          uint32_t y0 = 0, y1 = 0;
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          rb0 = max(rb0, lds_u8(vs + g * NB + j));
-          rb1 = max(rb1, lds_u8(vs + (g + 8) * NB + j));
-        }
-      }
-      const float rf0 = T::kAbsolute ? 0.0f : (float)(int)rb0 - 127.0f,
-                  rf1 = T::kAbsolute ? 0.0f : (float)(int)rb1 - 127.0f;
-
-      // ---- softmax; columns 2 t and 2 t + 1, rows g (0, 1) and g + 8 (2, 3)
-      bool over = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float x = sacc[nt][j] * qf[nt][j & 1];
-          if (part) {
-            const int row = j < 2 ? g : g + 8;
-            if (row < lo || row >= hi) x = -__int_as_float(0x7F800000);
+          for (int j = 0; j < NB / 4; ++j) {
+            const uint32_t z0 = __vmaxu2(sw0[j] & 0x00FF00FFu, (sw0[j] >> 8) & 0x00FF00FFu);
+            const uint32_t z1 = __vmaxu2(sw1[j] & 0x00FF00FFu, (sw1[j] >> 8) & 0x00FF00FFu);
+            y0 = j ? __vmaxu2(y0, z0) : z0;
+            y1 = j ? __vmaxu2(y1, z1) : z1;
           }
-          sacc[nt][j] = x;
-          const float d = x - m[nt][j & 1];
-          over |= d > kLag;
-          if constexpr (!T::kAbsolute) over |= d + ((j < 2 ? rf0 : rf1) - R[nt][j & 1]) > kLag;
+          both = __vmaxu2(__byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632));
         }
-      if (__any_sync(0xffffffffu, over)) {
+        rf0 = __uint_as_float((both & 0xFFFFu) | 0x4B000000u);
+        rf1 = __uint_as_float(__byte_perm(both, 0x4B000000u, 0x7432));
+      }
+
+      // ---- softmax; columns 2 t and 2 t + 1, rows g (0, 1) and g + 8 (2, 3):
+      // d = s - m, x = d + r - R + 11 (nvfp4: r = R = 0)
+      float d[NT][4], x[NT][4], over = -1.0f;
+      auto relate = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            d[nt][j] = fmaf(sacc[nt][j], qf[nt][j & 1], -m[nt][j & 1]);
+            if (part) {
+              const int row = j < 2 ? g : g + 8;
+              if (row < lo || row >= hi) d[nt][j] = -__int_as_float(0x7F800000);
+            }
+            if constexpr (!T::kAbsolute) x[nt][j] = d[nt][j] + ((j < 2 ? rf0 : rf1) - R[nt][j & 1]);
+          }
+      };
+      relate();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        over = fmaxf(fmaxf(over, fmaxf(d[nt][0], d[nt][1])), fmaxf(d[nt][2], d[nt][3]));
+        if constexpr (!T::kAbsolute)
+          over = fmaxf(over, fmaxf(fmaxf(x[nt][0], x[nt][1]), fmaxf(x[nt][2], x[nt][3])) - kWeightExp);
+      }
+      if (__any_sync(0xffffffffu, over > kLag)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float mx = fmaxf(sacc[nt][j], sacc[nt][j + 2]);
+            const bool live0 = !(part && (g < lo || g >= hi)),
+                       live1 = !(part && (g + 8 < lo || g + 8 >= hi));
+            const float a0 = live0 ? sacc[nt][j] * qf[nt][j] : kLowest;
+            const float a1 = live1 ? sacc[nt][j + 2] * qf[nt][j] : kLowest;
+            float mn = fmaxf(m[nt][j], fmaxf(a0, a1));
 #pragma unroll
-            for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-            const float mn = fmaxf(m[nt][j], mx), dm = m[nt][j] - mn;
+            for (int w = 4; w < 32; w <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
+            const float dm = m[nt][j] - mn;
             float Rn = R[nt][j];
             if constexpr (!T::kAbsolute) {
-              Rn = fmaxf(ceilf(sacc[nt][j] - mn + rf0), ceilf(sacc[nt][j + 2] - mn + rf1));
+              float e = -256.0f;
+              if (live0) e = fmaxf(e, ceilf(a0 - mn) + (rf0 - 8388735.0f));
+              if (live1) e = fmaxf(e, ceilf(a1 - mn) + (rf1 - 8388735.0f));
 #pragma unroll
-              for (int w = 4; w < 32; w <<= 1) Rn = fmaxf(Rn, __shfl_xor_sync(0xffffffffu, Rn, w));
-              Rn = fmaxf(fmaxf(Rn, -256.0f), ceilf(R[nt][j] + dm));
+              for (int w = 4; w < 32; w <<= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, w));
+              Rn = fmaxf(e, ceilf((R[nt][j] - kShift) + dm)) + kShift;
             }
             l[nt][j] *= ex2(dm);
             const float fo = ex2(dm + (R[nt][j] - Rn));
@@ -414,36 +489,42 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
             m[nt][j] = mn;
             R[nt][j] = Rn;
           }
+        relate();
       }
       uint32_t p[TERMS][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float x[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float d = sacc[nt][j] - m[nt][j & 1], e = ex2(d);
+          const float e = ex2(d[nt][j]);
           l[nt][j & 1] += e;
-          if constexpr (T::kAbsolute) x[j] = e * 2048.0f;
-          else x[j] = ex2(d + ((j < 2 ? rf0 : rf1) - R[nt][j & 1] + kWeightExp));
+          if constexpr (T::kAbsolute) x[nt][j] = e * 2048.0f;
+          else x[nt][j] = ex2(x[nt][j]);
         }
-        const uint32_t h0 = half2_of(x[0], x[1]), h1 = half2_of(x[2], x[3]);
+        const uint32_t h0 = half2_of(x[nt][0], x[nt][1]), h1 = half2_of(x[nt][2], x[nt][3]);
         p[0][nt][0] = sm100::movmatrix_trans(h0);
         p[0][nt][1] = sm100::movmatrix_trans(h1);
         if constexpr (TERMS == 2) {
-          p[1][nt][0] = sm100::movmatrix_trans(half2_of(x[0] - f16lo(h0), x[1] - f16hi(h0)));
-          p[1][nt][1] = sm100::movmatrix_trans(half2_of(x[2] - f16lo(h1), x[3] - f16hi(h1)));
+          p[1][nt][0] = sm100::movmatrix_trans(
+              half2_of(x[nt][0] - f16lo(h0), x[nt][1] - f16hi(h0)));
+          p[1][nt][1] = sm100::movmatrix_trans(
+              half2_of(x[nt][2] - f16lo(h1), x[nt][3] - f16hi(h1)));
         }
       }
 
       // ---- O^T += V^T P^T: tokens 2 t, 2 t + 1 and 8 more; channels of group g
-      uint32_t ra = 0, rb = 0;  // r of tokens 2t (low) and 2t + 8 (high); 2t + 1, 2t + 9
+      uint32_t rr[2] = {0, 0};  // r of tokens (2t, 2t + 1) and (2t + 8, 2t + 9)
       if constexpr (T::kRelative) {
-        const uint32_t both = rb0 | rb1 << 16;
-        ra = __shfl_sync(0xffffffffu, both, 8 * t4);
-        rb = __shfl_sync(0xffffffffu, both, 8 * t4 + 4);
+        const uint32_t ra = __shfl_sync(0xffffffffu, both, 8 * t4);
+        const uint32_t rb = __shfl_sync(0xffffffffu, both, 8 * t4 + 4);
+        rr[0] = __byte_perm(ra, rb, 0x5410);
+        rr[1] = __byte_perm(ra, rb, 0x7632);
       }
       constexpr int LB = T::RB / 8 < 16 ? T::RB / 8 : 16;  // bytes of one read
       constexpr int READS = T::RB / 8 / LB, W = LB / 4;
+      constexpr int PER_WORD = 2 * Codes<FMT>::kPairs;  // channels
+      // words of one scale
+      constexpr int SPAN = T::B / PER_WORD < W ? T::B / PER_WORD : W;
 #pragma unroll
       for (int rd = 0; rd < READS; ++rd) {
         uint32_t w[4][W];  // tokens 2t, 2t+1, 2t+8, 2t+9
@@ -451,70 +532,59 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int row = 2 * t4 + (k & 1) + 8 * (k >> 1);
-          lds_words<W>(w[k], vb + 16 * place<T::CH, false>(row, col) + in);
+          lds_bytes<LB>(w[k], vb + 16 * place<T::CH, false>(row, col) + in);
         }
-        constexpr int PER_WORD = FMT == MXQ_FMT_FP8 ? 4 : 8;  // channels
         uint32_t sc[2] = {0, 0};
 #pragma unroll
         for (int j = 0; j < W; ++j) {
           const int ch0 = j * PER_WORD;  // of this read
           // the scales of this lane's block: tokens (2t, 2t+1), (2t+8, 2t+9)
-          constexpr int SPAN = T::B / PER_WORD < W ? T::B / PER_WORD : W;  // words of one scale
           if constexpr (T::kAbsolute || T::kRelative) {
             if (j % SPAN == 0) {
               const int b = T::channel(g, rd * W * PER_WORD + ch0) / T::B;
-              uint32_t x[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                x[k] = lds_u8(vs + (2 * t4 + (k & 1) + 8 * (k >> 1)) * NB + b);
-              if constexpr (T::kAbsolute) {
-                sc[0] = e4m3x2_to_f16x2(x[0] | x[1] << 8);
-                sc[1] = e4m3x2_to_f16x2(x[2] | x[3] << 8);
-              } else {
-                const int r[4] = {(int)(ra & 0xFFFF), (int)(rb & 0xFFFF), (int)(ra >> 16),
-                                  (int)(rb >> 16)};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  x[k] = (uint32_t)max(0, (int)x[k] - r[k] + T::OFF + 15) << 10;
-                sc[0] = x[0] | x[1] << 16;
-                sc[1] = x[2] | x[3] << 16;
+              for (int k = 0; k < 2; ++k) {
+                uint32_t s0, s1;
+                lds_bytes<1>(&s0, vs + (2 * t4 + 8 * k) * NB + b);
+                lds_bytes<1>(&s1, vs + (2 * t4 + 1 + 8 * k) * NB + b);
+                if constexpr (T::kAbsolute) {
+                  sc[k] = e4m3x2_to_f16x2(s1 * 256 + s0);
+                } else {
+                  // exponents k - r + OFF + 15 >= 0 in both halves
+                  const uint32_t y = s1 * 65536 + s0 + (T::OFF + 15) * 0x00010001u;
+                  sc[k] = (__vmaxu2(y, rr[k]) - rr[k]) << 10;
+                }
               }
             }
           }
-          uint32_t pr[2][2];  // token pairs, paired codes
+          uint32_t f[2][PER_WORD];  // token pairs, channels
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint32_t A = w[2 * k][j], Bw = w[2 * k + 1][j];
             if constexpr (FMT == MXQ_FMT_FP8) {
-              pr[k][0] = __byte_perm(A, Bw, 0x5140);
-              pr[k][1] = __byte_perm(A, Bw, 0x7362);
+              decode_word<FMT>(__byte_perm(A, Bw, 0x5140), f[k]);
+              decode_word<FMT>(__byte_perm(A, Bw, 0x7362), f[k] + 2);
             } else {
-              pr[k][0] = (A & 0x0F0F0F0Fu) | ((Bw << 4) & 0xF0F0F0F0u);
-              pr[k][1] = ((A >> 4) & 0x0F0F0F0Fu) | (Bw & 0xF0F0F0F0u);
+              uint32_t even[4], odd[4];
+              decode_word<FMT>((A & 0x0F0F0F0Fu) | ((Bw << 4) & 0xF0F0F0F0u), even);
+              decode_word<FMT>(((A >> 4) & 0x0F0F0F0Fu) | (Bw & 0xF0F0F0F0u), odd);
+#pragma unroll
+              for (int h = 0; h < 4; ++h) f[k][2 * h] = even[h], f[k][2 * h + 1] = odd[h];
+            }
+            if constexpr (T::kAbsolute || T::kRelative) {
+#pragma unroll
+              for (int h = 0; h < PER_WORD; ++h) f[k][h] = hmul2(f[k][h], sc[k]);
             }
           }
 #pragma unroll
           for (int h = 0; h < PER_WORD / 2; ++h) {  // two channels: one tile of O
-            uint32_t f[4];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              if constexpr (FMT == MXQ_FMT_FP8) {  // channels 2h, 2h + 1: both in word h
-                f[2 * k] = cvt_pair<FMT>(pr[k][h], 0);
-                f[2 * k + 1] = cvt_pair<FMT>(pr[k][h], 1);
-              } else {  // channel 2h: low nibbles' word, 2h + 1: high nibbles'
-                f[2 * k] = cvt_pair<FMT>(pr[k][0], h);
-                f[2 * k + 1] = cvt_pair<FMT>(pr[k][1], h);
-              }
-              if constexpr (T::kAbsolute || T::kRelative) {
-                f[2 * k] = hmul2(f[2 * k], sc[k]);
-                f[2 * k + 1] = hmul2(f[2 * k + 1], sc[k]);
-              }
-            }
+            const uint32_t af[4] = {f[0][2 * h], f[0][2 * h + 1], f[1][2 * h], f[1][2 * h + 1]};
             const int mt = (rd * W * PER_WORD + ch0) / 2 + h;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int tm = 0; tm < TERMS; ++tm) mma16816(o[mt][nt], f, p[tm][nt][0], p[tm][nt][1]);
+              for (int tm = 0; tm < TERMS; ++tm)
+                mma16816(o[mt][nt], af, p[tm][nt][0], p[tm][nt][1]);
           }
         }
       }
@@ -540,7 +610,7 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
         for (int w = 4; w < 32; w <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, w);
         if (g == 0) {
           s_m[warp][head] = m[nt][j];
-          s_r[warp][head] = R[nt][j];
+          s_r[warp][head] = T::kAbsolute ? 0.0f : R[nt][j] - kShift;
           s_l[warp][head] = lt;
         }
       }
