@@ -14,6 +14,8 @@ namespace mxq {
 
 namespace attend {
 
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kGeneralHeads = 4;  // query heads a warp carries at once
 
 template <int FMT>
@@ -36,7 +38,7 @@ __global__ void __launch_bounds__(kThreads) attend_general_kernel(Args a, int dt
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = c.dim;
   const int rb = c.row_bytes(), nb = c.row_scales(), stride = D + 2;
   [[maybe_unused]] const int64_t n_rows = c.num_pages * c.heads * c.page;
-  walk(a, [&](const Span& s, const Target& t, int v0, int v1) {
+  walk<kWarps>(a, [&](const Span& s, const Target& t, int v0, int v1) {
     const int r0 = t.tile * kGeneralHeads, heads = min(kGeneralHeads, a.group - r0);
     float q[kGeneralHeads][NC], o[kGeneralHeads][NC], m[kGeneralHeads], l[kGeneralHeads];
 #pragma unroll
@@ -228,7 +230,7 @@ int launch_general(const Args& a, int dt, int grid, cudaStream_t st) {
   return go(attend_general_kernel<FMT, 16>);
 }
 
-constexpr int kCtasPerSm = 2;
+constexpr int kCtasPerSm = 4;  // at most, of any of the kernels
 
 // Whether the tensor-core kernels have these sizes: see the header's fast path.
 bool tc_fits(const Args& a) {

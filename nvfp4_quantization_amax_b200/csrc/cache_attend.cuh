@@ -27,8 +27,6 @@ constexpr int kUnit = 128;  // positions
 // What a pair costs beside its units (queries, the first loads' latency, the
 // join of the warps), in units: the line is laid in units plus this.
 constexpr int kPairCost = 6;
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 // Before any token: finite, so that no difference of two of them is NaN.
 constexpr float kLowest = -3.0e38f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -126,14 +124,19 @@ struct Part {
   int64_t b, b_begin;  // the sequence at begin and where it starts
 };
 
+template <int kWarps>
 __device__ __forceinline__ Part part_of(const Args& a) {
+  constexpr int kThreads = 32 * kWarps;
   __shared__ int64_t s_sum[kWarps];
   __shared__ int64_t s_b[2];
   const int64_t pairs = (int64_t)a.c.heads * a.head_tiles;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t total = 0;
-  for (int64_t b = threadIdx.x; b < a.c.n_seqs; b += kThreads)
-    total += pairs * (span_of(a, b).units + kPairCost);
+  auto length = [&](int64_t b) {
+    return b < a.c.n_seqs ? pairs * (span_of(a, b).units + kPairCost) : 0;
+  };
+  const int64_t one = length(threadIdx.x);  // all there is for up to kThreads sequences
+  int64_t total = one;
+  for (int64_t b = threadIdx.x + kThreads; b < a.c.n_seqs; b += kThreads) total += length(b);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   if (lane == 0) s_sum[warp] = total;
@@ -152,7 +155,7 @@ __device__ __forceinline__ Part part_of(const Args& a) {
   int64_t before = 0;
   for (int64_t b0 = 0; b0 < a.c.n_seqs; b0 += kThreads) {
     const int64_t b = b0 + threadIdx.x;
-    const int64_t mine = b < a.c.n_seqs ? pairs * (span_of(a, b).units + kPairCost) : 0;
+    const int64_t mine = b0 == 0 ? one : length(b);
     int64_t sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -213,9 +216,9 @@ __device__ __forceinline__ void put_weight(const Args& a, const Target& t, int r
 
 // Walk a block's part of the line: work(span, b, head, tile, first position,
 // last position + 1, target) once per pair.
-template <class Work>
+template <int kWarps, class Work>
 __device__ __forceinline__ void walk(const Args& a, Work work) {
-  const Part p = part_of(a);
+  const Part p = part_of<kWarps>(a);
   const int64_t pairs = (int64_t)a.c.heads * a.head_tiles;
   int32_t hdr[2] = {0, 0};
   int64_t u = p.begin, b = p.b, b_begin = p.b_begin;

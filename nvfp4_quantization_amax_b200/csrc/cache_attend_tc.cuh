@@ -49,6 +49,8 @@
 namespace mxq {
 namespace attend {
 
+constexpr int kTcThreads = 128;
+constexpr int kTcWarps = kTcThreads / 32;
 constexpr int kTile = 16;           // tokens
 constexpr float kLag = 4.0f;        // how far a logit may exceed the reference
 constexpr float kWeightExp = 11.0f; // weights are held times 2^11: at most 2^15
@@ -64,14 +66,29 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same with a zero addend.
+__device__ __forceinline__ void mma16816_first(float* c, const uint32_t* a, uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ void ldmatrix4(uint32_t* r, uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes, or zeros where `bytes` is 0 (nothing is read then).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -151,21 +168,31 @@ __host__ __device__ constexpr int place(int row, int col) {
 }
 
 // FMT; D: channels; NB: scales of a row; NT: tiles of 8 heads a warp carries;
-// TERMS: f16 terms of queries and weights.
+// TERMS: f16 terms of queries and weights.  A warp takes U tiles of 16 tokens
+// at a time: two of fp4, whose bytes bring twice the conversions, so that the
+// loop's own instructions are shared and two chains run side by side; one of
+// fp8, where two would not leave room for three buffers.
 template <int FMT, int D, int NB, int NT, int TERMS>
 struct Tc {
   static constexpr int RB = FMT == MXQ_FMT_FP8 ? D : D / 2;  // bytes of a row
+  static constexpr int U = FMT == MXQ_FMT_FP8 ? 1 : 2;
   static constexpr int CH = RB / 16;
   static constexpr int SC = 16 * NB;  // scale bytes of a tile
-  static constexpr int STAGE = 2 * (16 * RB + SC);
-  static constexpr int MIN_CTAS = NT == 1 && TERMS == 1 && D <= 128 ? 2 : 1;
-  static constexpr int SMEM = MIN_CTAS == 2 ? 108 * 1024 : 220 * 1024;
-  static constexpr int INFO = 64 * 8;  // bytes: a warp's ring of tile places
-  static constexpr int FIT = (SMEM / kWarps - INFO) / STAGE;
+  static constexpr int SCALES = U * 32 * RB;               // where a buffer's scales begin
+  static constexpr int STAGE = U * 2 * (16 * RB + SC);     // [tile][K, V], then their scales
+  static constexpr int MIN_CTAS = NT == 1 && TERMS == 1 && D <= 128 ? 4 : 2;
+  static constexpr int SMEM = (MIN_CTAS == 4 ? 55 : 110) * 1024;
+  static constexpr int INFO = 32 * 16;  // bytes: a warp's ring of tile places
+  static constexpr int QB = TERMS * NT * D * 16;  // bytes of Q: 8 heads of f16 in D channels
+  static constexpr int FIT = ((SMEM - QB) / kTcWarps - INFO) / STAGE;
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int PER_WARP = INFO + STAGES * STAGE;
-  static constexpr int PART = kWarps * 8 * NT * (D + 4) * 4;  // the warps' sums at the end
-  static constexpr int BYTES = kWarps * PER_WARP > PART ? kWarps * PER_WARP : PART;
+  // the warps' sums at the end: [warp][head][group][value], a group's values one
+  // word apart from the next's and heads 4 (mod 16) apart, so that the lanes of a
+  // warp store to 32 banks
+  static constexpr int GROUP = D / 8 + 1, ROW = (8 * GROUP + 11) / 16 * 16 + 4;
+  static constexpr int PART = kTcWarps * 8 * NT * ROW * 4;
+  static constexpr int BYTES = QB + (kTcWarps * PER_WARP > PART ? kTcWarps * PER_WARP : PART);
   static constexpr int CPL = D / 8;   // channels of V a lane holds
   static constexpr int KS = D / 16;   // k steps of S
   static constexpr int MT = D / 16;   // channel tiles of O
@@ -173,54 +200,83 @@ struct Tc {
   static constexpr bool kRelative = !kAbsolute && NB > 1;
   static constexpr int B = D / NB;    // channels of a scale
   static constexpr int OFF = !kRelative ? 0 : FMT == MXQ_FMT_FP8 ? 7 : 12;
-  static_assert(STAGES >= 3, "too few buffers");
+  static_assert(STAGES >= 2 && STAGES <= 8, "too few buffers");
 
-  // Channel of the i-th value of V that the lanes of group g hold.
+  // Channel of the i-th value of V that the lanes of group g hold, and where a
+  // channel's sum lies in its row.
+  static constexpr bool kHalves = FMT == MXQ_FMT_FP8 && D == 256;  // two reads 128 channels apart
   static __device__ __forceinline__ int channel(int g, int i) {
-    return FMT == MXQ_FMT_FP8 && D == 256 ? (i >> 4) * 128 + g * 16 + (i & 15) : g * CPL + i;
+    return kHalves ? (i >> 4) * 128 + g * 16 + (i & 15) : g * CPL + i;
+  }
+  static __device__ __forceinline__ int sum_at(int ch) {
+    return kHalves ? (ch >> 4 & 7) * GROUP + (ch >> 7) * 16 + (ch & 15)
+                   : ch / CPL * GROUP + ch % CPL;
   }
 };
 
 template <class T, int FMT, int D, int NB, int NT, int TERMS>
 __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[kWarps][8 * NT], s_r[kWarps][8 * NT], s_l[kWarps][8 * NT];
+  extern __shared__ __align__(128) uint8_t s_all[];
+  uint8_t* const smem = s_all + T::QB;  // the warps' buffers, then their sums
+  __shared__ float s_m[kTcWarps][8 * NT], s_r[kTcWarps][8 * NT], s_l[kTcWarps][8 * NT];
+  __shared__ float s_qf[8 * NT], s_back[2][8 * NT];
+  constexpr int U = T::U;
   const PagedCache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
   uint8_t* const mine = smem + warp * T::PER_WARP;
-  int2* const info = (int2*)mine;
+  int4* const info = (int4*)mine;  // two tiles (or -1), their live tokens
   const uint32_t buf0 = sm100::smem_addr(mine + T::INFO);
   const int tiles_per_page = c.page / kTile;
   [[maybe_unused]] const int64_t n_tiles = c.num_pages * c.heads * tiles_per_page;
 
-  // this lane's places: 16-byte chunks it copies, rows it reads
-  uint32_t dst_k[T::CH / 2], dst_v[T::CH / 2];
+  // this lane's places: 16-byte chunks it copies; the rows and chunks of K that
+  // ldmatrix reads; tokens 2t and 2t + 1 of V (8 rows on is a constant further)
+  uint32_t dst_k[T::CH / 2], dst_v[T::CH / 2], src_k[T::CH / 2], src_v[2];
+  constexpr int LB = T::RB / 8 < 16 ? T::RB / 8 : 16;  // bytes of V a lane reads at once
 #pragma unroll
   for (int i = 0; i < T::CH / 2; ++i) {
     const int at = lane + 32 * i, row = at / T::CH, col = at % T::CH;
     dst_k[i] = place<T::CH, true>(row, col) * 16;
     dst_v[i] = 16 * T::RB + place<T::CH, false>(row, col) * 16;
+    src_k[i] = place<T::CH, true>(lane & 15, 2 * i + (lane >> 4)) * 16;
   }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    src_v[i] = 16 * T::RB + place<T::CH, false>(2 * t4 + i, g * LB / 16) * 16 + g * LB % 16;
+  constexpr int EIGHT = place<T::CH, false>(8, 0) * 16;
+  const uint32_t q_at = sm100::smem_addr(s_all) + lane * 16;
+  // the 16 bytes of scales it copies: [tile][K, V][chunk], over the lanes
+  constexpr int SCHUNKS = U * 2 * NB, SROUNDS = (SCHUNKS + 31) / 32;
+  const bool copies_scales = SCHUNKS >= 32 || lane < SCHUNKS;
+  const int s_tile = SROUNDS > 1 ? 0 : (lane / (2 * NB)) % U;
+  const uint8_t* const s_from =
+      ((lane / NB) % 2 ? c.v_scales : c.k_scales) + (lane % NB) * 16;
 
-  walk(a, [&](const Span& s, const Target& tg, int v0, int v1) {
-    const int first = v0 / kTile + warp;
-    const int n = max(0, ((v1 + kTile - 1) / kTile - first + kWarps - 1) / kWarps);
+  walk<kTcWarps>(a, [&](const Span& s, const Target& tg, int v0, int v1) {
+    // this warp's turns: U tiles each, kTcWarps turns apart
+    const int first = v0 / (kTile * U) + warp;
+    const int n = max(0, ((v1 + kTile * U - 1) / (kTile * U) - first + kTcWarps - 1) / kTcWarps);
     const int r0 = tg.tile * 8 * NT;  // first head of the tile in its group
 
-    // Places of tiles i .. i + 31: row of the cache in tiles (or -1), and the
-    // live tokens [lo, hi) of the tile.
+    // Places of turns i .. i + 15: the tiles' rows of the cache in tiles (or
+    // -1), and the live tokens [lo, hi) of each, lo | hi << 8 in 16 bits.
     auto look_up = [&](int i) {
-      int2 p = make_int2(-1, 0);
-      if (i + lane < n) {
-        const Token tok = token_at(a, s, tg.b, tg.head, (first + (i + lane) * kWarps) * kTile);
-        if (tok.row >= 0) {
-          const int64_t start = a.window > 0 ? s.len - a.window : 0;
-          const int lo = (int)max((int64_t)0, min((int64_t)kTile, start - tok.pos));
-          const int hi = (int)max((int64_t)0, min((int64_t)kTile, s.len - tok.pos));
-          if (lo < hi) p = make_int2((int)(tok.row / kTile), lo | hi << 8);
-        }
+      if (lane >= 16) return;
+      int4 p = make_int4(-1, -1, 0, 0);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int v = (first + (i + lane) * kTcWarps) * (kTile * U) + u * kTile;
+        if (i + lane >= n || v >= v1) continue;
+        const Token tok = token_at(a, s, tg.b, tg.head, v);
+        if (tok.row < 0) continue;
+        const int64_t start = a.window > 0 ? s.len - a.window : 0;
+        const int lo = (int)max((int64_t)0, min((int64_t)kTile, start - tok.pos));
+        const int hi = (int)max((int64_t)0, min((int64_t)kTile, s.len - tok.pos));
+        if (lo >= hi || !MXQ_IN_RANGE(kChkAttendIn, tok.row / kTile, n_tiles)) continue;
+        (u ? p.y : p.x) = (int)(tok.row / kTile);
+        p.z |= (lo | hi << 8) << (16 * u);
       }
-      info[(i + lane) & 63] = p;
+      info[(i + lane) & 31] = p;
     };
     uint32_t fill = buf0, use = buf0;  // the buffers to load and to read next
     auto next = [&](uint32_t at) {
@@ -228,24 +284,30 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
       return at == buf0 + T::STAGES * T::STAGE ? buf0 : at;
     };
     auto issue = [&](int i) {
-      if (i < n) {
-        if ((i & 31) == 0) {
-          look_up(i);
-          __syncwarp();
-        }
-        const int tile = info[i & 63].x;
-        const uint32_t dst = fill;
-        if (tile >= 0 && MXQ_IN_RANGE(kChkAttendIn, tile, n_tiles)) {
-          const int64_t at = (int64_t)tile * (16 * T::RB) + lane * 16;
+      if ((i & 15) == 0) {
+        look_up(i);
+        __syncwarp();
+      }
+      const int4 p = info[i & 31];
 #pragma unroll
-          for (int j = 0; j < T::CH / 2; ++j) cp_async16(dst + dst_k[j], c.k_codes + at + 512 * j);
+      for (int u = 0; u < U; ++u) {
+        const int tile = u ? p.y : p.x;
+        const uint32_t bytes = tile >= 0 ? 16 : 0;
+        const int64_t at = (int64_t)max(tile, 0) * (16 * T::RB) + lane * 16;
+        const uint32_t dst = fill + u * (32 * T::RB);
 #pragma unroll
-          for (int j = 0; j < T::CH / 2; ++j) cp_async16(dst + dst_v[j], c.v_codes + at + 512 * j);
-          const int64_t sat = (int64_t)tile * T::SC;
-          if (lane < NB) cp_async16(dst + 32 * T::RB + lane * 16, c.k_scales + sat + lane * 16);
-          else if (lane >= 16 && lane < 16 + NB)
-            cp_async16(dst + 32 * T::RB + T::SC + (lane - 16) * 16,
-                       c.v_scales + sat + (lane - 16) * 16);
+        for (int j = 0; j < T::CH / 2; ++j)
+          cp_async16(dst + dst_k[j], c.k_codes + at + 512 * j, bytes);
+#pragma unroll
+        for (int j = 0; j < T::CH / 2; ++j)
+          cp_async16(dst + dst_v[j], c.v_codes + at + 512 * j, bytes);
+      }
+      if (copies_scales) {
+#pragma unroll
+        for (int j = 0; j < SROUNDS; ++j) {
+          const int tile = (U == 2 && (SROUNDS > 1 ? j : s_tile)) ? p.y : p.x;
+          cp_async16(fill + T::SCALES + (lane + 32 * j) * 16, s_from + (int64_t)max(tile, 0) * T::SC,
+                     tile >= 0 ? 16 : 0);
         }
       }
       fill = next(fill);
@@ -254,42 +316,69 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 #pragma unroll
     for (int i = 0; i < T::STAGES - 1; ++i) issue(i);
 
-    // Q in the layout of the second operand of S: lane (g, t) holds head g's
-    // channels, four (fp8) or eight (fp4) a chunk, in the order of the codes.
-    uint32_t q[TERMS][NT][T::KS][2];
-    float qf[NT][2];  // of columns 2 t, 2 t + 1: softmax scale x 2^(Q's exponent)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = r0 + nt * 8 + g;
+    // Q in the layout of the second operand of S, in shared memory: lane (g, t)
+    // of a warp holds head g's channels, four (fp8) or eight (fp4) a chunk, in
+    // the order of the codes; two k steps in 16 bytes.  One warp lays a tile.
+    if (warp < NT) {
+      const int r = r0 + warp * 8 + g;
       float x[T::KS][4], top = 0.0f;
       const int64_t at = tg.b * a.q_stride + ((int64_t)tg.head * a.group + r) * D;
+      auto channel = [&](int k) {
+        return FMT == MXQ_FMT_FP8 ? k * 16 + t4 * 4 : (k >> 1) * 32 + t4 * 8 + (k & 1) * 4;
+      };
+      if (r < a.group && dt != kF32 && ((uintptr_t)a.q & 7) == 0 && (a.q_stride & 3) == 0) {
+        uint2 w[T::KS];  // four channels in 8 bytes
 #pragma unroll
-      for (int k = 0; k < T::KS; ++k) {
-        const int ch = FMT == MXQ_FMT_FP8 ? k * 16 + t4 * 4 : (k >> 1) * 32 + t4 * 8 + (k & 1) * 4;
+        for (int k = 0; k < T::KS; ++k)
+          w[k] = __ldg((const uint2*)((const uint16_t*)a.q + at + channel(k)));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[k][j] = r < a.group ? load_q(a, dt, at + ch + j) : 0.0f;
-          top = fmaxf(top, fabsf(x[k][j]));
+        for (int k = 0; k < T::KS; ++k) {
+          const uint32_t h[2] = {w[k].x, w[k].y};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const bool bf = TERMS == 1 || dt == kBF16;  // one term: bf16 only
+            x[k][2 * j] = bf ? elem_to_f32<kBF16>(h[j] & 0xFFFFu) : f16lo(h[j]);
+            x[k][2 * j + 1] = bf ? elem_to_f32<kBF16>(h[j] >> 16) : f16hi(h[j]);
+          }
         }
+      } else {
+#pragma unroll
+        for (int k = 0; k < T::KS; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            x[k][j] = r < a.group ? load_q(a, dt, at + channel(k) + j) : 0.0f;
       }
+#pragma unroll
+      for (int k = 0; k < T::KS; ++k)
+        top = fmaxf(top, fmaxf(max3(fabsf(x[k][0]), fabsf(x[k][1]), fabsf(x[k][2])), fabsf(x[k][3])));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // largest magnitude to [2^13, 2^14)
       const int e = top > 0.0f ? floor_log2_f32bits(__float_as_uint(top)) - 13 : 0;
-      const float f1 = exp2i(max(-126, min(127, -(e / 2)))), f2 = exp2i(max(-126, min(127, -(e - e / 2))));
+      const float f1 = exp2i(-(e / 2)), f2 = exp2i(-(e - e / 2));
 #pragma unroll
-      for (int k = 0; k < T::KS; ++k)
+      for (int k = 0; k < T::KS; k += 2) {
+        uint32_t h[4], low[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float x0 = x[k][2 * j] * f1 * f2, x1 = x[k][2 * j + 1] * f1 * f2;
-          const uint32_t h = half2_of(x0, x1);
-          q[0][nt][k][j] = h;
-          if constexpr (TERMS == 2) q[1][nt][k][j] = half2_of(x0 - f16lo(h), x1 - f16hi(h));
+        for (int j = 0; j < 4; ++j) {
+          const float x0 = x[k + (j >> 1)][2 * (j & 1)] * f1 * f2,
+                      x1 = x[k + (j >> 1)][2 * (j & 1) + 1] * f1 * f2;
+          h[j] = half2_of(x0, x1);
+          low[j] = half2_of(x0 - f16lo(h[j]), x1 - f16hi(h[j]));
         }
-      const float back = a.scale_log2 * exp2f((float)e);
-      qf[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t4);
-      qf[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4);
+        uint4* to = (uint4*)(s_all + (warp * (T::KS / 2) + k / 2) * 512 + lane * 16);
+        *to = make_uint4(h[0], h[1], h[2], h[3]);
+        if constexpr (TERMS == 2)
+          to[NT * (T::KS / 2) * 32] = make_uint4(low[0], low[1], low[2], low[3]);
+      }
+      if (t4 == 0) s_qf[warp * 8 + g] = a.scale_log2 * exp2f((float)e);
     }
+    __syncthreads();
+    float qf[NT][2];  // of columns 2 t, 2 t + 1: softmax scale x 2^(Q's exponent)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) qf[nt][j] = s_qf[nt * 8 + 2 * t4 + j];
 
     // R is kept as R + 2^23 + 127 - 11: a scale byte in the low bits of 2^23's
     // pattern less that is the byte's exponent - R + 11, exactly
@@ -298,41 +387,20 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) m[nt][j] = kLowest, R[nt][j] = kShift - 256.0f, l[nt][j] = 0.0f;
+      for (int j = 0; j < 2; ++j) m[nt][j] = 0.0f, R[nt][j] = kShift, l[nt][j] = 0.0f;
 #pragma unroll
       for (int i = 0; i < T::MT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
     }
 
-    for (int i = 0; i < n; ++i) {
-      cp_async_wait<T::STAGES - 2>();
-      __syncwarp();
-      issue(i + T::STAGES - 1);
-      const uint32_t kb = use, vb = kb + 16 * T::RB, ks = kb + 32 * T::RB, vs = ks + T::SC;
-      use = next(use);
-      const int live_rows = info[i & 63].y, lo = live_rows & 255, hi = live_rows >> 8;
-      const bool part = lo > 0 || hi < kTile;
-      if (part) {  // rows behind the end, or before the window: no bytes of theirs count
-#pragma unroll
-        for (int j = 0; j < T::CH / 2; ++j) {
-          const int row = (lane + 32 * j) / T::CH;
-          if (row < lo || row >= hi)
-            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(kb + dst_v[j]), "r"(0)
-                         : "memory");
-        }
-        if constexpr (T::kAbsolute)
-          for (int j = lane; j < T::SC; j += 32)
-            if (j / NB < lo || j / NB >= hi)
-              asm volatile("st.shared.u8 [%0], %1;" ::"r"(vs + j), "h"((uint16_t)0) : "memory");
-        __syncwarp();
-      }
-
-      // ---- S = K Q^T
+    // sacc = K Q^T of a tile (Q's power of two apart): rows g, g + 8, columns
+    // 2 t, 2 t + 1 of each 8 heads
+    auto scores = [&](uint32_t kb, uint32_t ks, float (*sacc)[4]) {
       uint32_t sw0[(NB + 3) / 4], sw1[(NB + 3) / 4];  // scale bytes of tokens g, g + 8
       lds_bytes<NB>(sw0, ks + g * NB);
       lds_bytes<NB>(sw1, ks + (g + 8) * NB);
-      float sacc[NT][4], tmp[NT][4];
+      float tmp[NT][4];
       constexpr int STEPS = Codes<FMT>::kPairs / 2;          // k steps of a chunk
       constexpr int BLK = T::kRelative ? T::B / 16 : T::KS;  // k steps of a scale block
       uint32_t abs0[T::CH], abs1[T::CH];  // nvfp4: this lane's scale of each chunk, twice
@@ -356,7 +424,16 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 #pragma unroll
       for (int c2 = 0; c2 < T::CH; c2 += 2) {
         uint32_t w[4];
-        ldmatrix4(w, kb + 16 * place<T::CH, true>((lane & 7) + (lane & 8), c2 + (lane >> 4)));
+        ldmatrix4(w, kb + src_k[c2 / 2]);
+        uint32_t q[TERMS][NT][2 * STEPS][2];  // of this pair of chunks' k steps
+#pragma unroll
+        for (int tm = 0; tm < TERMS; ++tm)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k2 = 0; k2 < STEPS; ++k2)
+              lds_bytes<16>(&q[tm][nt][2 * k2][0],
+                            q_at + ((tm * NT + nt) * (T::KS / 2) + c2 * STEPS / 2 + k2) * 512);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int col = c2 + h;
@@ -373,16 +450,14 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
               f[2] = hmul2(f[2], abs0[col]);
               f[3] = hmul2(f[3], abs1[col]);
             }
-            if (k % BLK == 0) {
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) tmp[nt][j] = 0.0f;
-            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int tm = 0; tm < TERMS; ++tm) mma16816(tmp[nt], f, q[tm][nt][k][0], q[tm][nt][k][1]);
+              for (int tm = 0; tm < TERMS; ++tm) {
+                const uint32_t* b = q[tm][nt][h * STEPS + st];
+                if (k % BLK == 0 && tm == 0) mma16816_first(tmp[nt], f, b[0], b[1]);
+                else mma16816(tmp[nt], f, b[0], b[1]);
+              }
             if (k % BLK == BLK - 1) {
               const int b = k / BLK;
               float f0 = 1.0f, f1 = 1.0f;
@@ -410,117 +485,168 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
           }
         }
       }
+    };
+
+    constexpr uint32_t FULL = U == 2 ? 0x10001000u : 0x1000u;
+    const float none = __int_as_float(0xFF800000);
+    bool have = false;  // whether a token has been seen: m and R are set
+    for (int i = 0; i < n; ++i) {
+      cp_async_wait<T::STAGES - 2>();
+      __syncwarp();
+      issue(i + T::STAGES - 1);
+      const uint32_t kb = use, sb = kb + T::SCALES;
+      use = next(use);
+      const uint32_t live_rows = (uint32_t)info[i & 31].z;
+      if (live_rows == 0) continue;
+      const bool part = live_rows != FULL;
+      // whether a row of tile u is behind the end or before the window
+      auto dead = [&](int u, int row) {
+        return row < (int)(live_rows >> (16 * u) & 255) || row >= (int)(live_rows >> (16 * u + 8) & 255);
+      };
+      if (part) {  // no bytes of dead rows count
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+          for (int j = 0; j < T::CH / 2; ++j)
+            if (dead(u, (lane + 32 * j) / T::CH))
+              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(kb + u * (32 * T::RB) +
+                                                                        dst_v[j]),
+                           "r"(0)
+                           : "memory");
+          if constexpr (T::kAbsolute)
+            for (int j = lane; j < T::SC; j += 32)
+              if (dead(u, j / NB))
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(sb + (2 * u + 1) * T::SC + j),
+                             "h"((uint16_t)0)
+                             : "memory");
+        }
+        __syncwarp();
+      }
 
       // ---- V's scale bytes: the largest r of tokens g (low half) and g + 8
-      uint32_t both = 0;
-      float rf0 = 0.0f, rf1 = 0.0f;  // 2^23 + r
+      uint32_t both[U];
+      float rf[U][2];  // 2^23 + r
       if constexpr (!T::kAbsolute) {
-        lds_bytes<NB>(sw0, vs + g * NB);
-        lds_bytes<NB>(sw1, vs + (g + 8) * NB);
-        if constexpr (NB == 1) {
-          both = sw0[0] | sw1[0] << 16;
-        } else if constexpr (NB == 2) {
-          const uint32_t y = __byte_perm(sw0[0], sw1[0], 0x5410);  // two bytes of each
-          both = __vmaxu2(y & 0x00FF00FFu, (y >> 8) & 0x00FF00FFu);
-        } else {
-          uint32_t y0 = 0, y1 = 0;
 #pragma unroll
-          for (int j = 0; j < NB / 4; ++j) {
-            const uint32_t z0 = __vmaxu2(sw0[j] & 0x00FF00FFu, (sw0[j] >> 8) & 0x00FF00FFu);
-            const uint32_t z1 = __vmaxu2(sw1[j] & 0x00FF00FFu, (sw1[j] >> 8) & 0x00FF00FFu);
-            y0 = j ? __vmaxu2(y0, z0) : z0;
-            y1 = j ? __vmaxu2(y1, z1) : z1;
+        for (int u = 0; u < U; ++u) {
+          uint32_t y0[(NB + 3) / 4], y1[(NB + 3) / 4];
+          lds_bytes<NB>(y0, sb + (2 * u + 1) * T::SC + g * NB);
+          lds_bytes<NB>(y1, sb + (2 * u + 1) * T::SC + (g + 8) * NB);
+          if constexpr (NB == 1) {
+            both[u] = y0[0] | y1[0] << 16;
+          } else if constexpr (NB == 2) {
+            const uint32_t y = __byte_perm(y0[0], y1[0], 0x5410);  // two bytes of each
+            both[u] = __vmaxu2(y & 0x00FF00FFu, (y >> 8) & 0x00FF00FFu);
+          } else {
+            uint32_t z0 = 0, z1 = 0;
+#pragma unroll
+            for (int j = 0; j < NB / 4; ++j) {
+              const uint32_t w0 = __vmaxu2(y0[j] & 0x00FF00FFu, (y0[j] >> 8) & 0x00FF00FFu);
+              const uint32_t w1 = __vmaxu2(y1[j] & 0x00FF00FFu, (y1[j] >> 8) & 0x00FF00FFu);
+              z0 = j ? __vmaxu2(z0, w0) : w0;
+              z1 = j ? __vmaxu2(z1, w1) : w1;
+            }
+            both[u] = __vmaxu2(__byte_perm(z0, z1, 0x5410), __byte_perm(z0, z1, 0x7632));
           }
-          both = __vmaxu2(__byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632));
+          rf[u][0] = __uint_as_float((both[u] & 0xFFFFu) | 0x4B000000u);
+          rf[u][1] = __uint_as_float(__byte_perm(both[u], 0x4B000000u, 0x7432));
         }
-        rf0 = __uint_as_float((both & 0xFFFFu) | 0x4B000000u);
-        rf1 = __uint_as_float(__byte_perm(both, 0x4B000000u, 0x7432));
       }
 
-      // ---- softmax; columns 2 t and 2 t + 1, rows g (0, 1) and g + 8 (2, 3):
-      // d = s - m, x = d + r - R + 11 (nvfp4: r = R = 0)
-      float d[NT][4], x[NT][4], over = -1.0f;
-      auto relate = [&]() {
+      // d = s - m of columns 2 t and 2 t + 1, rows g (0, 1) and g + 8 (2, 3);
+      // where one exceeds its reference, the references move and S is taken
+      // again (three times at most: the second move is exact)
+      float d[U][NT][4];
+      for (int turn = 0; turn < 4; ++turn) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int u = 0; u < U; ++u) scores(kb + u * (32 * T::RB), sb + 2 * u * T::SC, d[u]);
+        float over = -1.0f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            d[nt][j] = fmaf(sacc[nt][j], qf[nt][j & 1], -m[nt][j & 1]);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[u][nt][j] = d[u][nt][j] * qf[nt][j & 1] - m[nt][j & 1];
             if (part) {
-              const int row = j < 2 ? g : g + 8;
-              if (row < lo || row >= hi) d[nt][j] = -__int_as_float(0x7F800000);
-            }
-            if constexpr (!T::kAbsolute) x[nt][j] = d[nt][j] + ((j < 2 ? rf0 : rf1) - R[nt][j & 1]);
-          }
-      };
-      relate();
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        over = fmaxf(fmaxf(over, fmaxf(d[nt][0], d[nt][1])), fmaxf(d[nt][2], d[nt][3]));
-        if constexpr (!T::kAbsolute)
-          over = fmaxf(over, fmaxf(fmaxf(x[nt][0], x[nt][1]), fmaxf(x[nt][2], x[nt][3])) - kWeightExp);
-      }
-      if (__any_sync(0xffffffffu, over > kLag)) {
+              for (int j = 0; j < 4; ++j)
+                if (dead(u, j < 2 ? g : g + 8)) d[u][nt][j] = none;
+            }
+            over = max3(over, d[u][nt][0], d[u][nt][1]);
+            over = max3(over, d[u][nt][2], d[u][nt][3]);
+            if constexpr (!T::kAbsolute) {
+              const float x0 = d[u][nt][0] + (rf[u][0] - R[nt][0]),
+                          x1 = d[u][nt][1] + (rf[u][0] - R[nt][1]),
+                          x2 = d[u][nt][2] + (rf[u][1] - R[nt][0]),
+                          x3 = d[u][nt][3] + (rf[u][1] - R[nt][1]);
+              over = max3(over, max3(x0, x1, x2) - kWeightExp, x3 - kWeightExp);
+            }
+          }
+        if (!__any_sync(0xffffffffu, over > kLag) && have) break;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const bool live0 = !(part && (g < lo || g >= hi)),
-                       live1 = !(part && (g + 8 < lo || g + 8 >= hi));
-            const float a0 = live0 ? sacc[nt][j] * qf[nt][j] : kLowest;
-            const float a1 = live1 ? sacc[nt][j + 2] * qf[nt][j] : kLowest;
-            float mn = fmaxf(m[nt][j], fmaxf(a0, a1));
+            float up = have ? 0.0f : none;
 #pragma unroll
-            for (int w = 4; w < 32; w <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
-            const float dm = m[nt][j] - mn;
+            for (int u = 0; u < U; ++u) up = max3(up, d[u][nt][j], d[u][nt][j + 2]);
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, w));
+            const float mn = m[nt][j] + up, dm = have ? m[nt][j] - mn : 0.0f;
             float Rn = R[nt][j];
             if constexpr (!T::kAbsolute) {
               float e = -256.0f;
-              if (live0) e = fmaxf(e, ceilf(a0 - mn) + (rf0 - 8388735.0f));
-              if (live1) e = fmaxf(e, ceilf(a1 - mn) + (rf1 - 8388735.0f));
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+                e = max3(e, ceilf(d[u][nt][j] - up) + (rf[u][0] - 8388735.0f),
+                         ceilf(d[u][nt][j + 2] - up) + (rf[u][1] - 8388735.0f));
 #pragma unroll
               for (int w = 4; w < 32; w <<= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, w));
-              Rn = fmaxf(e, ceilf((R[nt][j] - kShift) + dm)) + kShift;
+              Rn = (have ? fmaxf(e, ceilf((R[nt][j] - kShift) + dm)) : e) + kShift;
             }
             l[nt][j] *= ex2(dm);
-            const float fo = ex2(dm + (R[nt][j] - Rn));
+            const float fo = have ? ex2(dm + (R[nt][j] - Rn)) : 1.0f;
 #pragma unroll
             for (int mt = 0; mt < T::MT; ++mt) o[mt][nt][j] *= fo, o[mt][nt][j + 2] *= fo;
             m[nt][j] = mn;
             R[nt][j] = Rn;
           }
-        relate();
+        have = true;
       }
+
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+      const uint32_t vb = kb + u * (32 * T::RB), vs = sb + (2 * u + 1) * T::SC;
       uint32_t p[TERMS][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        float x[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float e = ex2(d[nt][j]);
+          const float e = ex2(d[u][nt][j]);
           l[nt][j & 1] += e;
-          if constexpr (T::kAbsolute) x[nt][j] = e * 2048.0f;
-          else x[nt][j] = ex2(x[nt][j]);
+          if constexpr (T::kAbsolute) x[j] = e * 2048.0f;
+          else x[j] = ex2(d[u][nt][j] + (rf[u][j >> 1] - R[nt][j & 1]));
         }
-        const uint32_t h0 = half2_of(x[nt][0], x[nt][1]), h1 = half2_of(x[nt][2], x[nt][3]);
+        const uint32_t h0 = half2_of(x[0], x[1]), h1 = half2_of(x[2], x[3]);
         p[0][nt][0] = sm100::movmatrix_trans(h0);
         p[0][nt][1] = sm100::movmatrix_trans(h1);
         if constexpr (TERMS == 2) {
           p[1][nt][0] = sm100::movmatrix_trans(
-              half2_of(x[nt][0] - f16lo(h0), x[nt][1] - f16hi(h0)));
+              half2_of(x[0] - f16lo(h0), x[1] - f16hi(h0)));
           p[1][nt][1] = sm100::movmatrix_trans(
-              half2_of(x[nt][2] - f16lo(h1), x[nt][3] - f16hi(h1)));
+              half2_of(x[2] - f16lo(h1), x[3] - f16hi(h1)));
         }
       }
 
       // ---- O^T += V^T P^T: tokens 2 t, 2 t + 1 and 8 more; channels of group g
       uint32_t rr[2] = {0, 0};  // r of tokens (2t, 2t + 1) and (2t + 8, 2t + 9)
       if constexpr (T::kRelative) {
-        const uint32_t ra = __shfl_sync(0xffffffffu, both, 8 * t4);
-        const uint32_t rb = __shfl_sync(0xffffffffu, both, 8 * t4 + 4);
+        const uint32_t ra = __shfl_sync(0xffffffffu, both[u], 8 * t4);
+        const uint32_t rb = __shfl_sync(0xffffffffu, both[u], 8 * t4 + 4);
         rr[0] = __byte_perm(ra, rb, 0x5410);
         rr[1] = __byte_perm(ra, rb, 0x7632);
       }
-      constexpr int LB = T::RB / 8 < 16 ? T::RB / 8 : 16;  // bytes of one read
       constexpr int READS = T::RB / 8 / LB, W = LB / 4;
       constexpr int PER_WORD = 2 * Codes<FMT>::kPairs;  // channels
       // words of one scale
@@ -528,12 +654,9 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 #pragma unroll
       for (int rd = 0; rd < READS; ++rd) {
         uint32_t w[4][W];  // tokens 2t, 2t+1, 2t+8, 2t+9
-        const int col = (g * LB) / 16 + 8 * rd, in = (g * LB) % 16;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = 2 * t4 + (k & 1) + 8 * (k >> 1);
-          lds_bytes<LB>(w[k], vb + 16 * place<T::CH, false>(row, col) + in);
-        }
+        for (int k = 0; k < 4; ++k)
+          lds_bytes<LB>(w[k], vb + src_v[k & 1] + (k >> 1) * EIGHT + rd * 128);
         uint32_t sc[2] = {0, 0};
 #pragma unroll
         for (int j = 0; j < W; ++j) {
@@ -588,9 +711,10 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
           }
         }
       }
+      }
     }
 
-    // ---- join the warps: [warp][head][value * 8 + group], rows of D + 4
+    // ---- join the warps
     cp_async_wait<0>();
     __syncthreads();
     float* const sums = (float*)smem;
@@ -599,11 +723,11 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int head = nt * 8 + 2 * t4 + j;
-        float* row = sums + (warp * 8 * NT + head) * (D + 4);
+        float* row = sums + (warp * 8 * NT + head) * T::ROW + g * T::GROUP;
 #pragma unroll
         for (int mt = 0; mt < T::MT; ++mt) {
-          row[(2 * mt) * 8 + g] = o[mt][nt][j];
-          row[(2 * mt + 1) * 8 + g] = o[mt][nt][j + 2];
+          row[2 * mt] = o[mt][nt][j];
+          row[2 * mt + 1] = o[mt][nt][j + 2];
         }
         float lt = l[nt][j];
 #pragma unroll
@@ -616,33 +740,47 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
       }
     __syncthreads();
     const int heads = min(8 * NT, a.group - r0);
-    for (int i = threadIdx.x; i < heads * D; i += kThreads) {
-      const int r = i / D, at = i - r * D, v = at >> 3, gr = at & 7;
-      float top = kLowest, ref = -1.0e30f, sum = 0.0f, val = 0.0f;
+    // a warp's factor 2^(m - top + R - ref) goes to s_r; out = sum x 2^(ref - 11
+    // - OFF) / l, the power in two steps
+    float mine_f = 0.0f;
+    const int fw = threadIdx.x / (8 * NT), fr = threadIdx.x % (8 * NT);
+    if (fw < kTcWarps) {
+      float top = kLowest, ref = -1.0e30f, sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+      for (int w = 0; w < kTcWarps; ++w)
+        if (s_l[w][fr] > 0.0f) top = fmaxf(top, s_m[w][fr]);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        if (s_l[w][r] > 0.0f) ref = fmaxf(ref, s_m[w][r] - top + s_r[w][r]);
+      for (int w = 0; w < kTcWarps; ++w)
+        if (s_l[w][fr] > 0.0f) ref = fmaxf(ref, s_m[w][fr] - top + s_r[w][fr]);
       ref = ceilf(ref);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (!(s_l[w][r] > 0.0f)) continue;
-        const float d = s_m[w][r] - top;
-        sum = fmaf(s_l[w][r], exp2f(d), sum);
-        val = fmaf(sums[(w * 8 * NT + r) * (D + 4) + at], exp2f(d + s_r[w][r] - ref), val);
+      for (int w = 0; w < kTcWarps; ++w)
+        if (s_l[w][fr] > 0.0f) sum = fmaf(s_l[w][fr], exp2f(s_m[w][fr] - top), sum);
+      if (s_l[fw][fr] > 0.0f) mine_f = exp2f(s_m[fw][fr] - top + s_r[fw][fr] - ref);
+      if (fw == 0 && fr < heads) {
+        const float back = ref - kWeightExp - (float)T::OFF, half = truncf(back * 0.5f);
+        s_back[0][fr] = sum > 0.0f ? exp2f(half) / sum : 0.0f;
+        s_back[1][fr] = sum > 0.0f ? exp2f(back - half) : 0.0f;
+        put_weight(a, tg, fr, sum > 0.0f ? top + log2f(sum) : kLowest);
       }
-      const float back = ref - kWeightExp - (float)T::OFF, half = truncf(back * 0.5f);
-      put(a, dt, tg, r, T::channel(gr, v),
-          sum > 0.0f ? val / sum * exp2f(half) * exp2f(back - half) : 0.0f);
-      if (at == 0) put_weight(a, tg, r, sum > 0.0f ? top + log2f(sum) : kLowest);
+    }
+    __syncthreads();
+    if (fw < kTcWarps) s_r[fw][fr] = mine_f;
+    __syncthreads();
+    for (int i = threadIdx.x; i < heads * D; i += kTcThreads) {
+      const int r = i / D, ch = i - r * D;
+      float val = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kTcWarps; ++w)
+        val = fmaf(sums[(w * 8 * NT + r) * T::ROW + T::sum_at(ch)], s_r[w][r], val);
+      put(a, dt, tg, r, ch, val * s_back[0][r] * s_back[1][r]);
     }
     __syncthreads();  // the buffers are the next pair's
   });
 }
 
 template <int FMT, int D, int NB, int NT, int TERMS>
-__global__ void __launch_bounds__(kThreads, Tc<FMT, D, NB, NT, TERMS>::MIN_CTAS)
+__global__ void __launch_bounds__(kTcThreads, Tc<FMT, D, NB, NT, TERMS>::MIN_CTAS)
 attend_tc_kernel(Args a, int dt) {
   attend_tc_body<Tc<FMT, D, NB, NT, TERMS>, FMT, D, NB, NT, TERMS>(a, dt);
 }
@@ -655,7 +793,7 @@ int launch_tc(const Args& a, int dt, int64_t units, int* grid, cudaStream_t st) 
   if (allow_dynamic_smem((const void*)kernel, T::BYTES) != cudaSuccess) return MXQ_ERR_CUDA;
   const int64_t ctas = (int64_t)T::MIN_CTAS * num_sms();
   *grid = (int)(units < ctas ? units : ctas);
-  kernel<<<*grid, kThreads, T::BYTES, st>>>(a, dt);
+  kernel<<<*grid, kTcThreads, T::BYTES, st>>>(a, dt);
   return MXQ_OK;
 }
 
