@@ -290,8 +290,7 @@ uint64_t attend_cache_paged_workspace_bytes(int64_t q_heads, int64_t kv_heads, i
  *  workspace  device, 16-byte aligned, attend_cache_paged_workspace_bytes;
  *           clobbered, not shared by calls that overlap on the GPU.
  *  Logits, softmax statistics and sums are f32.  A token's value blocks whose
- *  scale is below 2^-20 of the token's largest lose bits of what lies that
- *  far below it.
+ *  scale is below 2^-18 of the token's largest one lose bits.
  *  Fast path: head_dim 64, 128 or 256, page_size a multiple of 16, block_size
  *  a power of two of at least 32 (fp8), 32 (mxfp4) or 16 (nvfp4), codes and
  *  scales 16-byte aligned; anything else valid runs a slower general kernel.

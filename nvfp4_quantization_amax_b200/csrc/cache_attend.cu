@@ -118,19 +118,31 @@ __global__ void __launch_bounds__(kThreads) attend_general_kernel(Args a, int dt
 }
 
 // Join the parts of a split pair: out = sum_i o_i 2^(l_i - L), L = log2 sum
-// 2^l_i.  One block per (block of the line, some heads of the tile); a block
-// whose line part begins no split pair has nothing to do.  `per_head` warps
-// share a head's parts (a power of two, set by how many there can be), lanes
-// hold channels; the warps' sums are added in a fixed order.
-template <int NC>
-__global__ void __launch_bounds__(kThreads) join_kernel(Args a, int dt, int n_ctas, int per_head) {
+// 2^l_i.  `per_head` warps share a head's parts (a power of two, set by how
+// many there can be), lanes hold VEC channels at a time; the warps' sums are
+// added in a fixed order.  One block per (pair, some heads of the tile), which
+// finds the pair's parts among the slots, or, where there are more pairs than
+// blocks of the line, per (block of the line, some heads): such a block joins
+// the split pair that begins there.
+template <int VEC, int NC>
+__global__ void __launch_bounds__(kThreads)
+join_kernel(Args a, int dt, int n_ctas, int per_head, bool by_pair) {
   extern __shared__ float s_part[];  // [warps][dim + 1]
-  __shared__ int s_count;
-  const int cta = blockIdx.x, D = a.c.dim;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ int s_first, s_count;
+  const int D = a.c.dim, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) s_first = -1, s_count = 0;
   sm100::griddep_wait();
-  const int32_t pair1 = a.hdr[2 * cta + 1];
+  const int pair1 = by_pair ? (int)blockIdx.x + 1 : a.hdr[2 * blockIdx.x + 1];
   if (pair1 == 0) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n_ctas; i += kThreads) {
+    const int2 h = ((const int2*)a.hdr)[i];
+    if (h.y == pair1) s_first = i;
+    if (h.x == pair1) atomicAdd(&s_count, 1);
+  }
+  __syncthreads();
+  const int cta = s_first, parts = 1 + s_count;  // the blocks from cta on
+  if (cta < 0) return;                           // not split
   const int64_t pairs = (int64_t)a.c.heads * a.head_tiles, pair = pair1 - 1;
   Target t;
   t.b = pair / pairs;
@@ -139,24 +151,16 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Args a, int dt, int n_ct
   t.tile = pl - t.head * a.head_tiles;
   t.whole = true;
   t.slot = 0;
-  // the blocks behind this one that hold the pair's further parts
-  if (threadIdx.x == 0) s_count = n_ctas - 1 - cta;
-  __syncthreads();
-  for (int i = cta + 1 + threadIdx.x; i < n_ctas; i += kThreads)
-    if (a.hdr[2 * i] != pair1) {
-      atomicMin(&s_count, i - cta - 1);
-      break;
-    }
-  __syncthreads();
-  const int parts = 1 + s_count;
   const int r = (blockIdx.y * kWarps + warp) / per_head, share = warp & (per_head - 1);
   const bool have = r < min(a.tile_heads, a.group - t.tile * a.tile_heads);
   auto place = [&](int i) {
     return (int64_t)(i == 0 ? 2 * cta + 1 : 2 * (cta + i)) * a.tile_heads + r;
   };
-  float top = kLowest, sum = 0.0f, val[NC];
+  float top = kLowest, sum = 0.0f, val[NC][VEC];
 #pragma unroll
-  for (int i = 0; i < NC; ++i) val[i] = 0.0f;
+  for (int j = 0; j < NC; ++j)
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) val[j][k] = 0.0f;
   if (have) {
     for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_l[place(i)]);
 #pragma unroll
@@ -167,14 +171,23 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Args a, int dt, int n_ct
       const float l = a.part_l[at], f = l <= kLowest ? 0.0f : exp2f(l - top);
       sum += f;
 #pragma unroll
-      for (int j = 0; j < NC; ++j)
-        if (lane + 32 * j < D) val[j] = fmaf(a.part_o[at * D + lane + 32 * j], f, val[j]);
+      for (int j = 0; j < NC; ++j) {
+        const int ch = (lane + 32 * j) * VEC;
+        if (ch >= D) continue;
+        float x[VEC];
+        if constexpr (VEC == 4) *(float4*)x = *(const float4*)(a.part_o + at * D + ch);
+        else x[0] = a.part_o[at * D + ch];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) val[j][k] = fmaf(x[k], f, val[j][k]);
+      }
     }
   }
   float* mine = s_part + warp * (D + 1);
 #pragma unroll
   for (int j = 0; j < NC; ++j)
-    if (lane + 32 * j < D) mine[lane + 32 * j] = val[j];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k)
+      if ((lane + 32 * j) * VEC < D) mine[(lane + 32 * j) * VEC + k] = val[j][k];
   if (lane == 0) mine[D] = sum;
   __syncthreads();
   if (!have || share != 0) return;
@@ -182,12 +195,19 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Args a, int dt, int n_ct
     const float* other = mine + w * (D + 1);
 #pragma unroll
     for (int j = 0; j < NC; ++j)
-      if (lane + 32 * j < D) val[j] += other[lane + 32 * j];
+#pragma unroll
+      for (int k = 0; k < VEC; ++k)
+        if ((lane + 32 * j) * VEC < D) val[j][k] += other[(lane + 32 * j) * VEC + k];
     sum += other[D];
   }
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
   for (int j = 0; j < NC; ++j)
-    if (lane + 32 * j < D) put(a, dt, t, r, lane + 32 * j, sum > 0.0f ? val[j] / sum : 0.0f);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      const int ch = (lane + 32 * j) * VEC + k;
+      if (ch < D) put(a, dt, t, r, ch, val[j][k] * inv);
+    }
   if (lane == 0) put_weight(a, t, r, sum > 0.0f ? top + log2f(sum) : kLowest);
 }
 
@@ -195,11 +215,13 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Args a, int dt, int n_ct
 // the attention kernel's last blocks run and waits for them on the device.
 int launch_join(const Args& a, int dt, int grid, cudaStream_t st) {
   const int64_t pairs = a.c.n_seqs * a.c.heads * a.head_tiles;
+  const bool by_pair = pairs <= grid;
   const int64_t parts = grid / pairs + 2;  // of an average pair
   int per_head = 1;
   while (per_head < kWarps && per_head * 4 < parts) per_head *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)((a.tile_heads * per_head + kWarps - 1) / kWarps));
+  cfg.gridDim = dim3((unsigned)(by_pair ? pairs : grid),
+                     (unsigned)((a.tile_heads * per_head + kWarps - 1) / kWarps));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kWarps * (a.c.dim + 1) * 4;
   cfg.stream = st;
@@ -208,10 +230,12 @@ int launch_join(const Args& a, int dt, int grid, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  auto go = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, a, dt, grid, per_head, by_pair); };
   cudaError_t err;
-  if (a.c.dim <= 128) err = cudaLaunchKernelEx(&cfg, join_kernel<4>, a, dt, grid, per_head);
-  else if (a.c.dim <= 256) err = cudaLaunchKernelEx(&cfg, join_kernel<8>, a, dt, grid, per_head);
-  else err = cudaLaunchKernelEx(&cfg, join_kernel<16>, a, dt, grid, per_head);
+  if (a.c.dim % 4 != 0) err = go(join_kernel<1, 16>);
+  else if (a.c.dim <= 128) err = go(join_kernel<4, 1>);
+  else if (a.c.dim <= 256) err = go(join_kernel<4, 2>);
+  else err = go(join_kernel<4, 4>);
   return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
 
@@ -287,7 +311,7 @@ int launch_attend_cache_paged(const void* q, int dt, int64_t q_heads, int64_t q_
   const int64_t slots = 2 * max_ctas;
   a.hdr = (int32_t*)workspace;
   a.part_l = (float*)((char*)workspace + (slots * 4 + 15) / 16 * 16);
-  a.part_o = a.part_l + slots * 16;
+  a.part_o = a.part_l + slots * 16;  // 16-byte aligned, as are its rows where dim % 4 == 0
   // the tensor-core kernel carries 8 heads, or 16 where that does not overfill
   // its registers (one f16 term, up to 128 channels): K and V are read once
   // for all of a tile

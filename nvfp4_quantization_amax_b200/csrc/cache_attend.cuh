@@ -149,9 +149,12 @@ __device__ __forceinline__ Part part_of(const Args& a) {
   // no part is shorter than two units: the parts of a pair lie in blocks that
   // follow one another, and are worth their join
   const int64_t most = total / 2;
-  const int64_t n = most < gridDim.x ? most : gridDim.x;
-  p.begin = min(total, total * blockIdx.x / n);
-  p.end = min(total, total * (blockIdx.x + 1) / n);
+  const uint32_t n = most < gridDim.x ? (uint32_t)most : gridDim.x;
+  const int64_t each = total < ((int64_t)1 << 32) ? (uint32_t)total / n : total / n;
+  const uint32_t rest = (uint32_t)(total - each * n);  // below n, n below 2^16
+  auto start = [&](uint32_t i) { return min(total, each * i + rest * i / n); };
+  p.begin = start(blockIdx.x);
+  p.end = start(blockIdx.x + 1);
   int64_t before = 0;
   for (int64_t b0 = 0; b0 < a.c.n_seqs; b0 += kThreads) {
     const int64_t b = b0 + threadIdx.x;

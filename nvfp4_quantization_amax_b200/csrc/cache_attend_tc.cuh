@@ -25,13 +25,15 @@
 //    and P turns from S's layout to the operand's by movmatrix.
 //
 // Scales.  E8M0 scales (fp8, mxfp4) reach 2^+-127, beyond f16.  K: the sum over
-// each scale block is multiplied by its scale in f32.  V: the token's largest
-// scale exponent r joins the weight in the exponent, 2^(s - m + r - R), with a
-// running whole reference R, so a token of huge values and no weight costs no
-// other token its bits; what is left of a block's scale is 2^(k - r) <= 1 and
-// multiplies the codes in f16 (exact down to 2^-21 (fp8), 2^-26 (mxfp4) of
-// the token's largest scale).  E4M3 scales (nvfp4) times E2M1 codes are exact
-// in f16.
+// each scale block is multiplied by its scale in f32.  V: an exponent r joins
+// the weight, 2^(s + r - E), with E the running largest of s + r: a token of
+// huge values and no weight costs no other token its bits.  With one scale a
+// row r is the token's.  With several it is the largest of the turn's tokens,
+// found by a lane looking at 1/32 of their scale bytes, and what is left of a
+// block's scale, 2^(k - r), multiplies the codes in f16 (exactly, as long as
+// k - r >= -21); where a scale byte of the turn lies more than 20 below the
+// largest, its tokens are taken in bands of nearly one r, each a pass over V.
+// E4M3 scales (nvfp4) times E2M1 codes are exact in f16.
 //
 // Rounding.  Q is scaled by a power of two into f16 and held in TERMS terms
 // (one is exact for bf16 and f16; f32: 22 bits), the weights in TERMS terms:
@@ -54,6 +56,9 @@ constexpr int kTcWarps = kTcThreads / 32;
 constexpr int kTile = 16;           // tokens
 constexpr float kLag = 4.0f;        // how far a logit may exceed the reference
 constexpr float kWeightExp = 11.0f; // weights are held times 2^11: at most 2^15
+// Scale bytes of V: how far a turn's may lie below its largest to be taken
+// together, and how far tokens' largest ones in one band.
+constexpr int kBand = 20, kSpan = 4;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -196,7 +201,10 @@ struct Tc {
   static constexpr int CPL = D / 8;   // channels of V a lane holds
   static constexpr int KS = D / 16;   // k steps of S
   static constexpr int MT = D / 16;   // channel tiles of O
-  static constexpr bool kAbsolute = FMT == MXQ_FMT_NVFP4;  // scales that f16 holds
+  // how V's scales are met: E4M3 scales that f16 holds; one E8M0 scale a row;
+  // several
+  static constexpr bool kAbsolute = FMT == MXQ_FMT_NVFP4;
+  static constexpr bool kRow = !kAbsolute && NB == 1;
   static constexpr bool kRelative = !kAbsolute && NB > 1;
   static constexpr int B = D / NB;    // channels of a scale
   static constexpr int OFF = !kRelative ? 0 : FMT == MXQ_FMT_FP8 ? 7 : 12;
@@ -313,27 +321,32 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
       fill = next(fill);
       cp_async_commit();
     };
+    // Q in the layout of the second operand of S, in shared memory: lane (g, t)
+    // of a warp holds head g's channels, four (fp8) or eight (fp4) a chunk, in
+    // the order of the codes; two k steps in 16 bytes.  One warp lays a tile,
+    // its loads under way while the first tiles are looked up.
+    const int q_head = r0 + warp * 8 + g;
+    const int64_t q_from = tg.b * a.q_stride + ((int64_t)tg.head * a.group + q_head) * D;
+    const bool q_mine = warp < NT && q_head < a.group;
+    const bool q_wide = dt != kF32 && ((uintptr_t)a.q & 7) == 0 && (a.q_stride & 3) == 0;
+    auto q_channel = [&](int k) {
+      return FMT == MXQ_FMT_FP8 ? k * 16 + t4 * 4 : (k >> 1) * 32 + t4 * 8 + (k & 1) * 4;
+    };
+    uint2 q_raw[T::KS];  // four channels in 8 bytes
+    if (q_mine && q_wide) {
+#pragma unroll
+      for (int k = 0; k < T::KS; ++k)
+        q_raw[k] = __ldg((const uint2*)((const uint16_t*)a.q + q_from + q_channel(k)));
+    }
 #pragma unroll
     for (int i = 0; i < T::STAGES - 1; ++i) issue(i);
 
-    // Q in the layout of the second operand of S, in shared memory: lane (g, t)
-    // of a warp holds head g's channels, four (fp8) or eight (fp4) a chunk, in
-    // the order of the codes; two k steps in 16 bytes.  One warp lays a tile.
     if (warp < NT) {
-      const int r = r0 + warp * 8 + g;
       float x[T::KS][4], top = 0.0f;
-      const int64_t at = tg.b * a.q_stride + ((int64_t)tg.head * a.group + r) * D;
-      auto channel = [&](int k) {
-        return FMT == MXQ_FMT_FP8 ? k * 16 + t4 * 4 : (k >> 1) * 32 + t4 * 8 + (k & 1) * 4;
-      };
-      if (r < a.group && dt != kF32 && ((uintptr_t)a.q & 7) == 0 && (a.q_stride & 3) == 0) {
-        uint2 w[T::KS];  // four channels in 8 bytes
-#pragma unroll
-        for (int k = 0; k < T::KS; ++k)
-          w[k] = __ldg((const uint2*)((const uint16_t*)a.q + at + channel(k)));
+      if (q_mine && q_wide) {
 #pragma unroll
         for (int k = 0; k < T::KS; ++k) {
-          const uint32_t h[2] = {w[k].x, w[k].y};
+          const uint32_t h[2] = {q_raw[k].x, q_raw[k].y};
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const bool bf = TERMS == 1 || dt == kBF16;  // one term: bf16 only
@@ -346,7 +359,7 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
         for (int k = 0; k < T::KS; ++k)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            x[k][j] = r < a.group ? load_q(a, dt, at + channel(k) + j) : 0.0f;
+            x[k][j] = q_mine ? load_q(a, dt, q_from + q_channel(k) + j) : 0.0f;
       }
 #pragma unroll
       for (int k = 0; k < T::KS; ++k)
@@ -380,112 +393,17 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) qf[nt][j] = s_qf[nt * 8 + 2 * t4 + j];
 
-    // R is kept as R + 2^23 + 127 - 11: a scale byte in the low bits of 2^23's
-    // pattern less that is the byte's exponent - R + 11, exactly
-    constexpr float kShift = 8388608.0f + 127.0f - kWeightExp;
-    float o[T::MT][NT][4], m[NT][2], R[NT][2], l[NT][2];
+    // sums: l times 2^m, o times 2^(E - 11 - OFF)
+    float o[T::MT][NT][4], m[NT][2], E[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) m[nt][j] = 0.0f, R[nt][j] = kShift, l[nt][j] = 0.0f;
+      for (int j = 0; j < 2; ++j) m[nt][j] = 0.0f, E[nt][j] = kLowest, l[nt][j] = 0.0f;
 #pragma unroll
       for (int i = 0; i < T::MT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
     }
-
-    // sacc = K Q^T of a tile (Q's power of two apart): rows g, g + 8, columns
-    // 2 t, 2 t + 1 of each 8 heads
-    auto scores = [&](uint32_t kb, uint32_t ks, float (*sacc)[4]) {
-      uint32_t sw0[(NB + 3) / 4], sw1[(NB + 3) / 4];  // scale bytes of tokens g, g + 8
-      lds_bytes<NB>(sw0, ks + g * NB);
-      lds_bytes<NB>(sw1, ks + (g + 8) * NB);
-      float tmp[NT][4];
-      constexpr int STEPS = Codes<FMT>::kPairs / 2;          // k steps of a chunk
-      constexpr int BLK = T::kRelative ? T::B / 16 : T::KS;  // k steps of a scale block
-      uint32_t abs0[T::CH], abs1[T::CH];  // nvfp4: this lane's scale of each chunk, twice
-      if constexpr (T::kAbsolute) {
-#pragma unroll
-        for (int q4 = 0; q4 < (T::CH + 3) / 4; ++q4) {
-          const uint32_t sel = t4 < 2 ? 0x6420 : 0x7531;  // 8 of a chunk's 32 channels
-          const uint32_t x0 = __byte_perm(sw0[2 * q4], NB > 4 ? sw0[2 * q4 + 1 < (NB + 3) / 4 ? 2 * q4 + 1 : 0] : 0u, sel);
-          const uint32_t x1 = __byte_perm(sw1[2 * q4], NB > 4 ? sw1[2 * q4 + 1 < (NB + 3) / 4 ? 2 * q4 + 1 : 0] : 0u, sel);
-          uint32_t y0[2], y1[2];
-          decode_word<MXQ_FMT_FP8>(x0, y0);
-          decode_word<MXQ_FMT_FP8>(x1, y1);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (q4 * 4 + j < T::CH) {
-              abs0[q4 * 4 + j] = __byte_perm(y0[j >> 1], 0, j & 1 ? 0x3232 : 0x1010);
-              abs1[q4 * 4 + j] = __byte_perm(y1[j >> 1], 0, j & 1 ? 0x3232 : 0x1010);
-            }
-        }
-      }
-#pragma unroll
-      for (int c2 = 0; c2 < T::CH; c2 += 2) {
-        uint32_t w[4];
-        ldmatrix4(w, kb + src_k[c2 / 2]);
-        uint32_t q[TERMS][NT][2 * STEPS][2];  // of this pair of chunks' k steps
-#pragma unroll
-        for (int tm = 0; tm < TERMS; ++tm)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k2 = 0; k2 < STEPS; ++k2)
-              lds_bytes<16>(&q[tm][nt][2 * k2][0],
-                            q_at + ((tm * NT + nt) * (T::KS / 2) + c2 * STEPS / 2 + k2) * 512);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int col = c2 + h;
-          uint32_t x0[4], x1[4];
-          decode_word<FMT>(w[2 * h], x0);
-          decode_word<FMT>(w[2 * h + 1], x1);
-#pragma unroll
-          for (int st = 0; st < STEPS; ++st) {
-            const int k = col * STEPS + st;
-            uint32_t f[4] = {x0[2 * st], x1[2 * st], x0[2 * st + 1], x1[2 * st + 1]};
-            if constexpr (T::kAbsolute) {
-              f[0] = hmul2(f[0], abs0[col]);
-              f[1] = hmul2(f[1], abs1[col]);
-              f[2] = hmul2(f[2], abs0[col]);
-              f[3] = hmul2(f[3], abs1[col]);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int tm = 0; tm < TERMS; ++tm) {
-                const uint32_t* b = q[tm][nt][h * STEPS + st];
-                if (k % BLK == 0 && tm == 0) mma16816_first(tmp[nt], f, b[0], b[1]);
-                else mma16816(tmp[nt], f, b[0], b[1]);
-              }
-            if (k % BLK == BLK - 1) {
-              const int b = k / BLK;
-              float f0 = 1.0f, f1 = 1.0f;
-              if constexpr (!T::kAbsolute) {
-                float skip;
-                const int at = (b & 3) >> 1;  // half of its word
-                if (b & 1) {
-                  e8m0x2(sw0[b >> 2] >> (16 * at), skip, f0);
-                  e8m0x2(sw1[b >> 2] >> (16 * at), skip, f1);
-                } else {
-                  e8m0x2(sw0[b >> 2] >> (16 * at), f0, skip);
-                  e8m0x2(sw1[b >> 2] >> (16 * at), f1, skip);
-                }
-              }
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const float fj = j < 2 ? f0 : f1;
-                  if constexpr (T::kAbsolute) sacc[nt][j] = tmp[nt][j];
-                  else if (b == 0) sacc[nt][j] = tmp[nt][j] * fj;
-                  else sacc[nt][j] = fmaf(tmp[nt][j], fj, sacc[nt][j]);
-                }
-            }
-          }
-        }
-      }
-    };
 
     constexpr uint32_t FULL = U == 2 ? 0x10001000u : 0x1000u;
     const float none = __int_as_float(0xFF800000);
@@ -523,66 +441,118 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
         __syncwarp();
       }
 
-      // ---- V's scale bytes: the largest r of tokens g (low half) and g + 8
-      uint32_t both[U];
-      float rf[U][2];  // 2^23 + r
-      if constexpr (!T::kAbsolute) {
+      // ---- S = K Q^T: rows are tokens g, g + 8, columns heads 2 t, 2 t + 1 of 8
+      float d[U][NT][4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          uint32_t y0[(NB + 3) / 4], y1[(NB + 3) / 4];
-          lds_bytes<NB>(y0, sb + (2 * u + 1) * T::SC + g * NB);
-          lds_bytes<NB>(y1, sb + (2 * u + 1) * T::SC + (g + 8) * NB);
-          if constexpr (NB == 1) {
-            both[u] = y0[0] | y1[0] << 16;
-          } else if constexpr (NB == 2) {
-            const uint32_t y = __byte_perm(y0[0], y1[0], 0x5410);  // two bytes of each
-            both[u] = __vmaxu2(y & 0x00FF00FFu, (y >> 8) & 0x00FF00FFu);
-          } else {
-            uint32_t z0 = 0, z1 = 0;
+      for (int u = 0; u < U; ++u) {
+        const uint32_t tb = kb + u * (32 * T::RB), ks = sb + 2 * u * T::SC;
+        uint32_t sw0[(NB + 3) / 4], sw1[(NB + 3) / 4];  // scale bytes of tokens g, g + 8
+        lds_bytes<NB>(sw0, ks + g * NB);
+        lds_bytes<NB>(sw1, ks + (g + 8) * NB);
+        float tmp[NT][4];
+        constexpr int STEPS = Codes<FMT>::kPairs / 2;          // k steps of a chunk
+        constexpr int BLK = T::kRelative ? T::B / 16 : T::KS;  // k steps of a scale block
+        uint32_t abs0[T::CH], abs1[T::CH];  // nvfp4: this lane's scale of each chunk, twice
+        if constexpr (T::kAbsolute) {
 #pragma unroll
-            for (int j = 0; j < NB / 4; ++j) {
-              const uint32_t w0 = __vmaxu2(y0[j] & 0x00FF00FFu, (y0[j] >> 8) & 0x00FF00FFu);
-              const uint32_t w1 = __vmaxu2(y1[j] & 0x00FF00FFu, (y1[j] >> 8) & 0x00FF00FFu);
-              z0 = j ? __vmaxu2(z0, w0) : w0;
-              z1 = j ? __vmaxu2(z1, w1) : w1;
-            }
-            both[u] = __vmaxu2(__byte_perm(z0, z1, 0x5410), __byte_perm(z0, z1, 0x7632));
+          for (int q4 = 0; q4 < (T::CH + 3) / 4; ++q4) {
+            const uint32_t sel = t4 < 2 ? 0x6420 : 0x7531;  // 8 of a chunk's 32 channels
+            const uint32_t x0 = __byte_perm(sw0[2 * q4], NB > 4 ? sw0[2 * q4 + 1 < (NB + 3) / 4 ? 2 * q4 + 1 : 0] : 0u, sel);
+            const uint32_t x1 = __byte_perm(sw1[2 * q4], NB > 4 ? sw1[2 * q4 + 1 < (NB + 3) / 4 ? 2 * q4 + 1 : 0] : 0u, sel);
+            uint32_t y0[2], y1[2];
+            decode_word<MXQ_FMT_FP8>(x0, y0);
+            decode_word<MXQ_FMT_FP8>(x1, y1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (q4 * 4 + j < T::CH) {
+                abs0[q4 * 4 + j] = __byte_perm(y0[j >> 1], 0, j & 1 ? 0x3232 : 0x1010);
+                abs1[q4 * 4 + j] = __byte_perm(y1[j >> 1], 0, j & 1 ? 0x3232 : 0x1010);
+              }
           }
-          rf[u][0] = __uint_as_float((both[u] & 0xFFFFu) | 0x4B000000u);
-          rf[u][1] = __uint_as_float(__byte_perm(both[u], 0x4B000000u, 0x7432));
+        }
+#pragma unroll
+        for (int c2 = 0; c2 < T::CH; c2 += 2) {
+          uint32_t w[4];
+          ldmatrix4(w, tb + src_k[c2 / 2]);
+          uint32_t q[TERMS][NT][2 * STEPS][2];  // of this pair of chunks' k steps
+#pragma unroll
+          for (int tm = 0; tm < TERMS; ++tm)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k2 = 0; k2 < STEPS; ++k2)
+                lds_bytes<16>(&q[tm][nt][2 * k2][0],
+                              q_at + ((tm * NT + nt) * (T::KS / 2) + c2 * STEPS / 2 + k2) * 512);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int col = c2 + h;
+            uint32_t x0[4], x1[4];
+            decode_word<FMT>(w[2 * h], x0);
+            decode_word<FMT>(w[2 * h + 1], x1);
+#pragma unroll
+            for (int st = 0; st < STEPS; ++st) {
+              const int k = col * STEPS + st;
+              uint32_t f[4] = {x0[2 * st], x1[2 * st], x0[2 * st + 1], x1[2 * st + 1]};
+              if constexpr (T::kAbsolute) {
+                f[0] = hmul2(f[0], abs0[col]);
+                f[1] = hmul2(f[1], abs1[col]);
+                f[2] = hmul2(f[2], abs0[col]);
+                f[3] = hmul2(f[3], abs1[col]);
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int tm = 0; tm < TERMS; ++tm) {
+                  const uint32_t* b = q[tm][nt][h * STEPS + st];
+                  if (k % BLK == 0 && tm == 0) mma16816_first(tmp[nt], f, b[0], b[1]);
+                  else mma16816(tmp[nt], f, b[0], b[1]);
+                }
+              if (k % BLK == BLK - 1) {
+                const int b = k / BLK;
+                float f0 = 1.0f, f1 = 1.0f;
+                if constexpr (!T::kAbsolute) {
+                  float skip;
+                  const int at = (b & 3) >> 1;  // half of its word
+                  if (b & 1) {
+                    e8m0x2(sw0[b >> 2] >> (16 * at), skip, f0);
+                    e8m0x2(sw1[b >> 2] >> (16 * at), skip, f1);
+                  } else {
+                    e8m0x2(sw0[b >> 2] >> (16 * at), f0, skip);
+                    e8m0x2(sw1[b >> 2] >> (16 * at), f1, skip);
+                  }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    const float fj = j < 2 ? f0 : f1;
+                    if constexpr (T::kAbsolute) d[u][nt][j] = tmp[nt][j];
+                    else if (b == 0) d[u][nt][j] = tmp[nt][j] * fj;
+                    else d[u][nt][j] = fmaf(tmp[nt][j], fj, d[u][nt][j]);
+                  }
+              }
+            }
+          }
         }
       }
 
-      // d = s - m of columns 2 t and 2 t + 1, rows g (0, 1) and g + 8 (2, 3);
-      // where one exceeds its reference, the references move and S is taken
-      // again (three times at most: the second move is exact)
-      float d[U][NT][4];
-      for (int turn = 0; turn < 4; ++turn) {
+      // ---- d = s - m; the reference moves where one exceeds it by 2^4
+      float over = -1.0f;
 #pragma unroll
-        for (int u = 0; u < U; ++u) scores(kb + u * (32 * T::RB), sb + 2 * u * T::SC, d[u]);
-        float over = -1.0f;
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
+          for (int j = 0; j < 4; ++j) d[u][nt][j] = d[u][nt][j] * qf[nt][j & 1] - m[nt][j & 1];
+          if (part) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) d[u][nt][j] = d[u][nt][j] * qf[nt][j & 1] - m[nt][j & 1];
-            if (part) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (dead(u, j < 2 ? g : g + 8)) d[u][nt][j] = none;
-            }
-            over = max3(over, d[u][nt][0], d[u][nt][1]);
-            over = max3(over, d[u][nt][2], d[u][nt][3]);
-            if constexpr (!T::kAbsolute) {
-              const float x0 = d[u][nt][0] + (rf[u][0] - R[nt][0]),
-                          x1 = d[u][nt][1] + (rf[u][0] - R[nt][1]),
-                          x2 = d[u][nt][2] + (rf[u][1] - R[nt][0]),
-                          x3 = d[u][nt][3] + (rf[u][1] - R[nt][1]);
-              over = max3(over, max3(x0, x1, x2) - kWeightExp, x3 - kWeightExp);
-            }
+            for (int j = 0; j < 4; ++j)
+              if (dead(u, j < 2 ? g : g + 8)) d[u][nt][j] = none;
           }
-        if (!__any_sync(0xffffffffu, over > kLag) && have) break;
+          over = max3(over, d[u][nt][0], d[u][nt][1]);
+          over = max3(over, d[u][nt][2], d[u][nt][3]);
+        }
+      if (__any_sync(0xffffffffu, over > kLag || !have)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -592,27 +562,137 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
             for (int u = 0; u < U; ++u) up = max3(up, d[u][nt][j], d[u][nt][j + 2]);
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, w));
-            const float mn = m[nt][j] + up, dm = have ? m[nt][j] - mn : 0.0f;
-            float Rn = R[nt][j];
-            if constexpr (!T::kAbsolute) {
-              float e = -256.0f;
+            m[nt][j] += up;
+            if (have) l[nt][j] *= ex2(-up);
+            if constexpr (T::kAbsolute) {
+              if (have) {
 #pragma unroll
-              for (int u = 0; u < U; ++u)
-                e = max3(e, ceilf(d[u][nt][j] - up) + (rf[u][0] - 8388735.0f),
-                         ceilf(d[u][nt][j + 2] - up) + (rf[u][1] - 8388735.0f));
-#pragma unroll
-              for (int w = 4; w < 32; w <<= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, w));
-              Rn = (have ? fmaxf(e, ceilf((R[nt][j] - kShift) + dm)) : e) + kShift;
+                for (int mt = 0; mt < T::MT; ++mt) o[mt][nt][j] *= ex2(-up), o[mt][nt][j + 2] *= ex2(-up);
+              }
             }
-            l[nt][j] *= ex2(dm);
-            const float fo = have ? ex2(dm + (R[nt][j] - Rn)) : 1.0f;
 #pragma unroll
-            for (int mt = 0; mt < T::MT; ++mt) o[mt][nt][j] *= fo, o[mt][nt][j + 2] *= fo;
-            m[nt][j] = mn;
-            R[nt][j] = Rn;
+            for (int u = 0; u < U; ++u) d[u][nt][j] -= up, d[u][nt][j + 2] -= up;
           }
         have = true;
       }
+
+      // ---- V's scales.  One a row: its exponent goes into the token's weight.
+      // Several: the largest exponent r of the turn's tokens does, and what is
+      // left, 2^(k - r), multiplies the codes; where the turn's scale bytes lie
+      // far apart (`wide`), its tokens are taken in bands of nearly one r.
+      float rf[U][2];                // kRow: r of tokens g and g + 8
+      int r = 0, rt[U][2];           // kRelative: the band's r (a byte); tokens' own
+      bool wide = false;
+      if constexpr (T::kRow) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          uint32_t y0, y1;
+          lds_bytes<1>(&y0, sb + (2 * u + 1) * T::SC + g);
+          lds_bytes<1>(&y1, sb + (2 * u + 1) * T::SC + g + 8);
+          rf[u][0] = __uint_as_float(y0 | 0x4B000000u) - 8388735.0f;  // 2^23 + byte, exactly
+          rf[u][1] = __uint_as_float(y1 | 0x4B000000u) - 8388735.0f;
+        }
+      }
+      if constexpr (T::kRelative) {
+        // a lane looks at its share of the turn's scale bytes of V
+        constexpr int MY = U * T::SC / 32;
+        static_assert(MY >= 1 && MY <= 8, "a lane's share of the scale bytes");
+        uint32_t w[(MY + 3) / 4];
+        const int at = lane * MY;
+        lds_bytes<MY>(w, sb + (2 * (at / T::SC) + 1) * T::SC + at % T::SC);
+        uint32_t hi2, lo2;
+        if constexpr (MY == 1) {
+          hi2 = lo2 = w[0];
+        } else if constexpr (MY == 2) {
+          hi2 = max(w[0] & 255u, w[0] >> 8);
+          lo2 = min(w[0] & 255u, w[0] >> 8);
+        } else {
+          const uint32_t even = w[0] & 0x00FF00FFu, odd = (w[0] >> 8) & 0x00FF00FFu;
+          hi2 = __vmaxu2(even, odd);
+          lo2 = __vminu2(even, odd);
+          if constexpr (MY == 8) {
+            const uint32_t even1 = w[1] & 0x00FF00FFu, odd1 = (w[1] >> 8) & 0x00FF00FFu;
+            hi2 = __vmaxu2(hi2, __vmaxu2(even1, odd1));
+            lo2 = __vminu2(lo2, __vminu2(even1, odd1));
+          }
+          hi2 = max(hi2 & 0xFFFFu, hi2 >> 16);
+          lo2 = min(lo2 & 0xFFFFu, lo2 >> 16);
+        }
+        r = (int)__reduce_max_sync(0xffffffffu, hi2);
+        wide = part || __any_sync(0xffffffffu, (int)lo2 < r - kBand);
+        if (wide) {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int row = g + 8 * h;
+              int top = -1;
+              for (int j = 0; j < NB; ++j) {
+                uint32_t y;
+                lds_bytes<1>(&y, sb + (2 * u + 1) * T::SC + row * NB + j);
+                top = max(top, (int)y);
+              }
+              rt[u][h] = part && dead(u, row) ? -1 : top;
+            }
+          int top = rt[0][0];
+#pragma unroll
+          for (int u = 0; u < U; ++u) top = max(top, max(rt[u][0], rt[u][1]));
+          r = __reduce_max_sync(0xffffffffu, top);
+        }
+      }
+
+      for (;;) {  // once, or once a band
+      // ---- weights times 2^(11 + r): x = s + r - E + 11
+      float x[U][NT][4];
+      if constexpr (!T::kAbsolute) {
+        auto relate = [&]() {
+          float most = -1.0f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float c[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              c[j] = (m[nt][j] - E[nt][j]) + (kWeightExp + (T::kRow ? 0.0f : (float)(r - 127)));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                x[u][nt][j] = d[u][nt][j] + (T::kRow ? rf[u][j >> 1] + c[j & 1] : c[j & 1]);
+                if (T::kRelative && wide && (rt[u][j >> 1] > r || rt[u][j >> 1] <= r - kSpan))
+                  x[u][nt][j] = none;
+              }
+              most = max3(most, x[u][nt][0], x[u][nt][1]);
+              most = max3(most, x[u][nt][2], x[u][nt][3]);
+            }
+          }
+          return most;
+        };
+        if (__any_sync(0xffffffffu, relate() > kWeightExp + kLag)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              // the column's largest s - m + r of this band
+              float e = kLowest;
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const bool out_of = T::kRelative && wide && (rt[u][h] > r || rt[u][h] <= r - kSpan);
+                  const float rr = T::kRow ? rf[u][h] : (float)(r - 127);
+                  if (!out_of) e = fmaxf(e, d[u][nt][j + 2 * h] + rr);
+                }
+#pragma unroll
+              for (int w = 4; w < 32; w <<= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, w));
+              const float En = fmaxf(E[nt][j], m[nt][j] + e), fo = ex2(E[nt][j] - En);
+#pragma unroll
+              for (int mt = 0; mt < T::MT; ++mt) o[mt][nt][j] *= fo, o[mt][nt][j + 2] *= fo;
+              E[nt][j] = En;
+            }
+          relate();
+        }
+      }
+      const uint32_t rr = (uint32_t)r * 0x00010001u;
 
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -620,33 +700,29 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
       uint32_t p[TERMS][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float x[4];
+        float y[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float e = ex2(d[u][nt][j]);
-          l[nt][j & 1] += e;
-          if constexpr (T::kAbsolute) x[j] = e * 2048.0f;
-          else x[j] = ex2(d[u][nt][j] + (rf[u][j >> 1] - R[nt][j & 1]));
+          if constexpr (T::kAbsolute) {
+            const float e = ex2(d[u][nt][j]);
+            l[nt][j & 1] += e;
+            y[j] = e * 2048.0f;
+          } else {
+            y[j] = ex2(x[u][nt][j]);
+          }
         }
-        const uint32_t h0 = half2_of(x[0], x[1]), h1 = half2_of(x[2], x[3]);
+        const uint32_t h0 = half2_of(y[0], y[1]), h1 = half2_of(y[2], y[3]);
         p[0][nt][0] = sm100::movmatrix_trans(h0);
         p[0][nt][1] = sm100::movmatrix_trans(h1);
         if constexpr (TERMS == 2) {
           p[1][nt][0] = sm100::movmatrix_trans(
-              half2_of(x[0] - f16lo(h0), x[1] - f16hi(h0)));
+              half2_of(y[0] - f16lo(h0), y[1] - f16hi(h0)));
           p[1][nt][1] = sm100::movmatrix_trans(
-              half2_of(x[2] - f16lo(h1), x[3] - f16hi(h1)));
+              half2_of(y[2] - f16lo(h1), y[3] - f16hi(h1)));
         }
       }
 
       // ---- O^T += V^T P^T: tokens 2 t, 2 t + 1 and 8 more; channels of group g
-      uint32_t rr[2] = {0, 0};  // r of tokens (2t, 2t + 1) and (2t + 8, 2t + 9)
-      if constexpr (T::kRelative) {
-        const uint32_t ra = __shfl_sync(0xffffffffu, both[u], 8 * t4);
-        const uint32_t rb = __shfl_sync(0xffffffffu, both[u], 8 * t4 + 4);
-        rr[0] = __byte_perm(ra, rb, 0x5410);
-        rr[1] = __byte_perm(ra, rb, 0x7632);
-      }
       constexpr int READS = T::RB / 8 / LB, W = LB / 4;
       constexpr int PER_WORD = 2 * Codes<FMT>::kPairs;  // channels
       // words of one scale
@@ -673,9 +749,10 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
                 if constexpr (T::kAbsolute) {
                   sc[k] = e4m3x2_to_f16x2(s1 * 256 + s0);
                 } else {
-                  // exponents k - r + OFF + 15 >= 0 in both halves
+                  // f16 exponents k - r + OFF + 15 in both halves, within [0, OFF + 15]
                   const uint32_t y = s1 * 65536 + s0 + (T::OFF + 15) * 0x00010001u;
-                  sc[k] = (__vmaxu2(y, rr[k]) - rr[k]) << 10;
+                  sc[k] = !wide ? (y - rr) << 10
+                                : (__vminu2(__vmaxu2(y, rr) - rr, (T::OFF + 15) * 0x00010001u)) << 10;
                 }
               }
             }
@@ -712,6 +789,28 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
         }
       }
       }
+      if constexpr (T::kRelative) {
+        if (wide) {  // the next band below this one
+          int top = -1;
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (rt[u][h] <= r - kSpan) top = max(top, rt[u][h]);
+          r = __reduce_max_sync(0xffffffffu, top);
+          if (r >= 0) continue;
+        }
+      }
+      break;
+      }
+      if constexpr (!T::kAbsolute) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) l[nt][j & 1] += ex2(d[u][nt][j]);
+      }
     }
 
     // ---- join the warps
@@ -734,31 +833,30 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
         for (int w = 4; w < 32; w <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, w);
         if (g == 0) {
           s_m[warp][head] = m[nt][j];
-          s_r[warp][head] = T::kAbsolute ? 0.0f : R[nt][j] - kShift;
+          s_r[warp][head] = T::kAbsolute ? m[nt][j] : E[nt][j];
           s_l[warp][head] = lt;
         }
       }
     __syncthreads();
     const int heads = min(8 * NT, a.group - r0);
-    // a warp's factor 2^(m - top + R - ref) goes to s_r; out = sum x 2^(ref - 11
-    // - OFF) / l, the power in two steps
+    // a warp's factor 2^(E - ref) goes to s_r; out = sum x 2^(ref - top - 11 -
+    // OFF) / l, the power in two steps
     float mine_f = 0.0f;
     const int fw = threadIdx.x / (8 * NT), fr = threadIdx.x % (8 * NT);
     if (fw < kTcWarps) {
-      float top = kLowest, ref = -1.0e30f, sum = 0.0f;
+      float top = kLowest, ref = kLowest, sum = 0.0f;
 #pragma unroll
       for (int w = 0; w < kTcWarps; ++w)
         if (s_l[w][fr] > 0.0f) top = fmaxf(top, s_m[w][fr]);
 #pragma unroll
       for (int w = 0; w < kTcWarps; ++w)
-        if (s_l[w][fr] > 0.0f) ref = fmaxf(ref, s_m[w][fr] - top + s_r[w][fr]);
-      ref = ceilf(ref);
+        if (s_l[w][fr] > 0.0f) ref = fmaxf(ref, s_r[w][fr]);
 #pragma unroll
       for (int w = 0; w < kTcWarps; ++w)
         if (s_l[w][fr] > 0.0f) sum = fmaf(s_l[w][fr], exp2f(s_m[w][fr] - top), sum);
-      if (s_l[fw][fr] > 0.0f) mine_f = exp2f(s_m[fw][fr] - top + s_r[fw][fr] - ref);
+      if (s_l[fw][fr] > 0.0f) mine_f = exp2f(s_r[fw][fr] - ref);
       if (fw == 0 && fr < heads) {
-        const float back = ref - kWeightExp - (float)T::OFF, half = truncf(back * 0.5f);
+        const float back = (ref - top) - kWeightExp - (float)T::OFF, half = truncf(back * 0.5f);
         s_back[0][fr] = sum > 0.0f ? exp2f(half) / sum : 0.0f;
         s_back[1][fr] = sum > 0.0f ? exp2f(back - half) : 0.0f;
         put_weight(a, tg, fr, sum > 0.0f ? top + log2f(sum) : kLowest);
