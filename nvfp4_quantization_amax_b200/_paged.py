@@ -11,34 +11,48 @@ import torch
 
 from ._abi import _DTYPES, _FORMATS, _check, _device_word, _out, _result, _to_device, lib
 
+_U8, _I32 = torch.uint8, torch.int32
+# The raw handle of a device's current stream, without a Stream object (a step
+# of serving makes several of these calls, and its host time is theirs).
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
+    torch._C, "_cuda_getCurrentRawStream") else (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 def _ints(t, shape, dev, name):
     """An int32 tensor of a call (page table, lengths, offs, a page list)."""
-    if t.dtype != torch.int32:
+    if t.dtype is not _I32:
         raise TypeError("%s must be int32, not %s" % (name, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, list(shape), list(t.shape)))
     if t.device != dev:
         t, _ = _to_device(t, dev)
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
 
 
-def _cache(cache, format, block_size, name, like=None):
-    """(codes, scales, (pages, kv_heads, page_size, head_dim)) of a cache."""
+def _cache(cache, format, block_size, name):
+    """(codes, scales, codes' shape) of a cache."""
     codes, scales = cache
-    for t in (codes, scales):
-        if not t.is_cuda or t.dtype != torch.uint8 or not t.is_contiguous() or t.dim() != 4:
-            raise ValueError("%s: codes and scales must be contiguous uint8 CUDA tensors of 4 "
-                             "dimensions" % name)
-    dim = codes.shape[3] * (1 if format == "fp8" else 2)
-    if scales.shape[:3] != codes.shape[:3] or scales.shape[3] * block_size != dim:
+    shape, sshape = codes.shape, scales.shape
+    if (codes.dtype is not _U8 or scales.dtype is not _U8 or len(shape) != 4 or len(sshape) != 4
+            or not codes.is_cuda or not codes.is_contiguous() or not scales.is_contiguous()):
+        raise ValueError("%s: codes and scales must be contiguous uint8 CUDA tensors of 4 "
+                         "dimensions" % name)
+    if (sshape[:3] != shape[:3]
+            or sshape[3] * block_size != (shape[3] if format == "fp8" else 2 * shape[3])):
         raise ValueError("%s: scales must have shape [pages, kv_heads, page_size, head_dim / "
                          "block_size]" % name)
     if scales.device != codes.device:
         raise ValueError("%s: codes and scales must share a device" % name)
-    if like is not None and (codes.device != like.device or codes.shape != like.shape):
+    return codes, scales, shape
+
+
+def _second(cache, format, block_size, name, first):
+    """V's (codes, scales): as K's in shape and device."""
+    codes, scales, shape = _cache(cache, format, block_size, name)
+    if shape != first.shape or codes.device != first.device:
         raise ValueError("%s must have K's shape and device" % name)
-    return codes, scales, (*codes.shape[:3], dim)
+    return codes, scales
 
 
 def _format(format, block_size, what):
@@ -46,30 +60,56 @@ def _format(format, block_size, what):
         raise ValueError("%s: format must be one of %s" % (what, sorted(_FORMATS)))
     if block_size < 1:
         raise ValueError("%s: block_size must be >= 1" % what)
+    return _FORMATS[format]
 
 
-def _rows(t, dev, what):
+def _table(page_table, what):
+    if page_table.dim() != 2:
+        raise ValueError("%s: page_table must be [sequences, max_pages]" % what)
+    return page_table.shape
+
+
+def _rows(t, dev):
     """(device tensor, elements between its rows, was on the host) of a tensor
-    whose rows must be dense, the rows themselves at any distance."""
-    t, host = (t, False) if t.device == dev else _to_device(t, dev)
-    row = t.shape[1] * t.shape[2]
-    if t.shape[0] == 1 and t[0].is_contiguous():
-        return t, row, host
-    if not (t.stride(2) == 1 and t.stride(1) == t.shape[2] and t.stride(0) >= row):
+    [rows, heads, channels] whose rows must be dense, the rows themselves at
+    any distance."""
+    host = False
+    if t.device != dev:
+        t, host = _to_device(t, dev)
+    n, heads, dim = t.shape
+    row = heads * dim
+    if not t.is_contiguous():
+        apart, head, one = t.stride()
+        if one == 1 and head == dim and apart >= row:
+            return t, apart, host
         t = t.contiguous()
-        return t, row, host
-    return t, t.stride(0), host
+    return t, row, host
 
 
 def _run(dev, what, fn, *args):
     """Call the library on dev's current stream, with dev current."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, stream)
+    index = dev.index
+    if index == torch._C._cuda_getDevice():
+        rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, stream)
-    _check(rc, what)
+            rc = fn(*args, _raw_stream(index))
+    if rc != 0:
+        _check(rc, what)
+
+
+def _word(t, dev):
+    """The optional status word."""
+    return None if t is None else _device_word(t, _I32, 1, dev, "status")
+
+
+def _scratch(t, need, dev):
+    """The optional workspace, or a new one (kept alive by the caller until the
+    call is made; the allocator hands its memory on in stream order)."""
+    if t is None:
+        return torch.empty(need, dtype=_U8, device=dev)
+    _device_word(t, _U8, need, dev, "workspace")
+    return t
 
 
 def append_cache_paged(k, v, offs, page_table, lengths, k_cache, v_cache, format, block_size,
@@ -88,41 +128,39 @@ def append_cache_paged(k, v, offs, page_table, lengths, k_cache, v_cache, format
     is reported there, and its rows are left out.
     """
     what = "append_cache_paged"
-    _format(format, block_size, what)
+    fmt = _format(format, block_size, what)
     if (v is None) != (v_cache is None):
         raise ValueError("%s: v and v_cache belong together" % what)
     kc, ks, (P, H, S, D) = _cache(k_cache, format, block_size, "k_cache")
+    D = D if fmt == 0 else 2 * D
     dev = kc.device
     vc = vs = None
     if v is not None:
-        vc, vs, _ = _cache(v_cache, format, block_size, "v_cache", kc)
+        vc, vs = _second(v_cache, format, block_size, "v_cache", kc)
         if v.dtype != k.dtype or v.shape != k.shape:
             raise ValueError("%s: k and v must have one dtype and shape" % what)
     if k.dtype not in _DTYPES:
         raise TypeError("%s: unsupported dtype %s" % (what, k.dtype))
     if k.dim() != 3 or k.shape[1] != H or k.shape[2] != D:
         raise ValueError("%s: k must be [rows, %d, %d]" % (what, H, D))
-    if page_table.dim() != 2:
-        raise ValueError("%s: page_table must be [sequences, max_pages]" % what)
-    n, M = page_table.shape
+    n, M = _table(page_table, what)
     page_table = _ints(page_table, (n, M), dev, "page_table")
     lengths = _ints(lengths, (n,), dev, "lengths")
     offs = _ints(offs, (n,), dev, "offs")
-    k, k_stride, host = _rows(k, dev, what)
+    k, k_stride, host = _rows(k, dev)
     v_stride = 0
     if v is not None:
-        v, v_stride, _ = _rows(v, dev, what)
+        v, v_stride, _ = _rows(v, dev)
     T = k.shape[0]
     k_out = v_out = None
     if values:
         k_out = torch.empty((T, H, D), dtype=k.dtype, device=dev)
-        v_out = torch.empty_like(k_out) if v is not None else None
-    ptr = [None if t is None else t.data_ptr() for t in (v, vc, vs, k_out, v_out)]
-    st = _device_word(status, torch.int32, 1, dev, "status")
+        v_out = torch.empty((T, H, D), dtype=k.dtype, device=dev) if v is not None else None
+    ptr = [None if x is None else x.data_ptr() for x in (v, vc, vs, k_out, v_out)]
     _run(dev, what, lib().append_cache_paged, k.data_ptr(), ptr[0], _DTYPES[k.dtype], T, H, D,
-         k_stride, v_stride, offs.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), n, M,
-         _FORMATS[format], block_size, P, S, kc.data_ptr(), ks.data_ptr(), ptr[1], ptr[2], ptr[3],
-         ptr[4], st)
+         k_stride, v_stride, offs.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), n, M, fmt,
+         block_size, P, S, kc.data_ptr(), ks.data_ptr(), ptr[1], ptr[2], ptr[3], ptr[4],
+         _word(status, dev))
     if not values:
         return None
     return _result(k_out, None, host), None if v is None else _result(v_out, None, host)
@@ -137,12 +175,11 @@ def bound_cache_pages(k_cache, page_table, lengths, format, block_size, bounds=N
     new_tokens tokens (None: for all of its pages), and returns it.
     """
     what = "bound_cache_pages"
-    _format(format, block_size, what)
+    fmt = _format(format, block_size, what)
     kc, ks, (P, H, S, D) = _cache(k_cache, format, block_size, "k_cache")
+    D = D if fmt == 0 else 2 * D
     dev = kc.device
-    if page_table.dim() != 2:
-        raise ValueError("%s: page_table must be [sequences, max_pages]" % what)
-    n, M = page_table.shape
+    n, M = _table(page_table, what)
     page_table = _ints(page_table, (n, M), dev, "page_table")
     lengths = _ints(lengths, (n,), dev, "lengths")
     if bounds is None:
@@ -150,10 +187,9 @@ def bound_cache_pages(k_cache, page_table, lengths, format, block_size, bounds=N
     if not bounds.is_cuda:
         raise ValueError("%s: bounds must be a CUDA tensor" % what)
     bounds, _ = _out(bounds, (P, H, 2, D), torch.bfloat16, dev, "bounds")
-    st = _device_word(status, torch.int32, 1, dev, "status")
-    _run(dev, what, lib().bound_cache_pages, kc.data_ptr(), ks.data_ptr(), H, D, _FORMATS[format],
-         block_size, P, S, page_table.data_ptr(), lengths.data_ptr(), n, M,
-         M * S if new_tokens is None else int(new_tokens), bounds.data_ptr(), st)
+    _run(dev, what, lib().bound_cache_pages, kc.data_ptr(), ks.data_ptr(), H, D, fmt, block_size,
+         P, S, page_table.data_ptr(), lengths.data_ptr(), n, M,
+         M * S if new_tokens is None else int(new_tokens), bounds.data_ptr(), _word(status, dev))
     return bounds
 
 
@@ -162,7 +198,7 @@ def _queries(q, dev, H, D, what):
         raise TypeError("%s: unsupported dtype %s" % (what, q.dtype))
     if q.dim() != 3 or q.shape[2] != D or q.shape[1] < 1 or q.shape[1] % H != 0:
         raise ValueError("%s: q must be [sequences, a multiple of %d, %d]" % (what, H, D))
-    return _rows(q, dev, what)
+    return _rows(q, dev)
 
 
 def select_cache_pages(q, bounds, page_table, lengths, page_size, top, keep_first=0, keep_last=1,
@@ -185,24 +221,22 @@ def select_cache_pages(q, bounds, page_table, lengths, page_size, top, keep_firs
     P, H, _, D = bounds.shape
     dev = bounds.device
     q, q_stride, host = _queries(q, dev, H, D, what)
-    if page_table.dim() != 2:
-        raise ValueError("%s: page_table must be [sequences, max_pages]" % what)
-    n, M = q.shape[0], page_table.shape[1]
+    n, M = q.shape[0], _table(page_table, what)[1]
     page_table = _ints(page_table, (n, M), dev, "page_table")
     lengths = _ints(lengths, (n,), dev, "lengths")
     top = int(top)
     if top < 0:
         raise ValueError("%s: top must not be negative" % what)
-    out, target = _out(out, (n, H, top), torch.int32, dev, "out")
-    need = 8 * n * H * M
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws = _device_word(workspace, torch.uint8, need, dev, "workspace")
-    st = _device_word(status, torch.int32, 1, dev, "status")
+    out, target = _out(out, (n, H, top), _I32, dev, "out")
+    ws = _scratch(workspace, 8 * n * H * M, dev)
     _run(dev, what, lib().select_cache_pages, q.data_ptr(), _DTYPES[q.dtype], n, q.shape[1], H, D,
          q_stride, bounds.data_ptr(), P, int(page_size), page_table.data_ptr(),
-         lengths.data_ptr(), M, top, int(keep_first), int(keep_last), out.data_ptr(), ws, st)
+         lengths.data_ptr(), M, top, int(keep_first), int(keep_last), out.data_ptr(),
+         ws.data_ptr(), _word(status, dev))
     return _result(out, target, host)
+
+
+_attend_need = {}  # workspace bytes by heads, head size and device
 
 
 def attend_cache_paged(q, k_cache, v_cache, page_table, lengths, format, block_size, scale=None,
@@ -223,18 +257,17 @@ def attend_cache_paged(q, k_cache, v_cache, page_table, lengths, format, block_s
     attend_cache_paged_workspace_bytes (C) bytes.
     """
     what = "attend_cache_paged"
-    _format(format, block_size, what)
+    fmt = _format(format, block_size, what)
     kc, ks, (P, H, S, D) = _cache(k_cache, format, block_size, "k_cache")
-    vc, vs, _ = _cache(v_cache, format, block_size, "v_cache", kc)
+    D = D if fmt == 0 else 2 * D
+    vc, vs = _second(v_cache, format, block_size, "v_cache", kc)
     dev = kc.device
     q, q_stride, host = _queries(q, dev, H, D, what)
-    if page_table.dim() != 2:
-        raise ValueError("%s: page_table must be [sequences, max_pages]" % what)
-    n, Hq = q.shape[0], q.shape[1]
-    M = page_table.shape[1]
+    n, Hq, _ = q.shape
+    M = _table(page_table, what)[1]
     page_table = _ints(page_table, (n, M), dev, "page_table")
     lengths = _ints(lengths, (n,), dev, "lengths")
-    top = 0
+    top, listed = 0, None
     if pages is not None:
         if pages.dim() != 3:
             raise ValueError("%s: pages must be [sequences, kv_heads, n]" % what)
@@ -242,21 +275,25 @@ def attend_cache_paged(q, k_cache, v_cache, page_table, lengths, format, block_s
         if top == 0:
             raise ValueError("%s: pages must list at least one page" % what)
         pages = _ints(pages, (n, H, top), dev, "pages")
-    if window is not None and window < 1:
+        listed = pages.data_ptr()
+    if window is None:
+        window = 0
+    elif window < 1:
         raise ValueError("%s: window must be at least 1" % what)
-    window = 0 if window is None else int(window)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    out, target = _out(out, (n, Hq, D), q.dtype, dev, "out")
+    dt = q.dtype
+    out, target = _out(out, (n, Hq, D), dt, dev, "out")
     lse = torch.empty((n, Hq), dtype=torch.float32, device=dev) if return_lse else None
-    need = lib().attend_cache_paged_workspace_bytes(Hq, H, D)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws = _device_word(workspace, torch.uint8, need, dev, "workspace")
-    st = _device_word(status, torch.int32, 1, dev, "status")
-    _run(dev, what, lib().attend_cache_paged, q.data_ptr(), _DTYPES[q.dtype], n, Hq, H, D,
-         q_stride, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), _FORMATS[format],
-         block_size, P, S, page_table.data_ptr(), lengths.data_ptr(), M,
-         None if pages is None else pages.data_ptr(), top, window, scale, out.data_ptr(),
-         None if lse is None else lse.data_ptr(), ws, st)
+    key = (Hq, H, D, dev.index)
+    need = _attend_need.get(key)
+    if need is None:
+        with torch.cuda.device(dev):
+            need = _attend_need[key] = lib().attend_cache_paged_workspace_bytes(Hq, H, D)
+    ws = _scratch(workspace, need, dev)
+    _run(dev, what, lib().attend_cache_paged, q.data_ptr(), _DTYPES[dt], n, Hq, H, D, q_stride,
+         kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), fmt, block_size, P, S,
+         page_table.data_ptr(), lengths.data_ptr(), M, listed, top, int(window), scale,
+         out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(),
+         _word(status, dev))
     out = _result(out, target, host)
     return (out, _result(lse, None, host)) if return_lse else out

@@ -25,8 +25,10 @@ namespace attend {
 
 constexpr int kUnit = 128;  // positions
 // What a pair costs beside its units (queries, the first loads' latency, the
-// join of the warps), in units: the line is laid in units plus this.
-constexpr int kPairCost = 6;
+// join of the warps), in units: the line is laid in units plus this.  Measured
+// on 32 ragged sequences of up to 8192 tokens x 8 heads in fp8: 83.6 us with 0,
+// 61.3 us with 2, 63.1 us with 6; 96 even ones in mxfp4: 122.3, 121.2, 125.3.
+constexpr int kPairCost = 2;
 // Before any token: finite, so that no difference of two of them is NaN.
 constexpr float kLowest = -3.0e38f;
 constexpr float kLn2 = 0.6931471805599453f;

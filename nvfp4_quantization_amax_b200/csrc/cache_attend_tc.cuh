@@ -185,8 +185,10 @@ struct Tc {
   static constexpr int SC = 16 * NB;  // scale bytes of a tile
   static constexpr int SCALES = U * 32 * RB;               // where a buffer's scales begin
   static constexpr int STAGE = U * 2 * (16 * RB + SC);     // [tile][K, V], then their scales
-  static constexpr int MIN_CTAS = NT == 1 && TERMS == 1 && D <= 128 ? 4 : 2;
-  static constexpr int SMEM = (MIN_CTAS == 4 ? 55 : 110) * 1024;
+  // Three blocks an SM leave 168 registers a thread: 96 x 8192 in mxfp4 take
+  // 117.0 us, with four (128 registers, some spilled) 121.0, with five 132.3.
+  static constexpr int MIN_CTAS = NT == 1 && TERMS == 1 && D <= 128 ? 3 : 2;
+  static constexpr int SMEM = (MIN_CTAS == 3 ? 74 : 110) * 1024;
   static constexpr int INFO = 32 * 16;  // bytes: a warp's ring of tile places
   static constexpr int QB = TERMS * NT * D * 16;  // bytes of Q: 8 heads of f16 in D channels
   static constexpr int FIT = ((SMEM - QB) / kTcWarps - INFO) / STAGE;
