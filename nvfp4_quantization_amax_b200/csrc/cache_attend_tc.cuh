@@ -135,29 +135,6 @@ __device__ __forceinline__ void e8m0x2(uint32_t two, float& lo, float& hi) {
   hi = __uint_as_float(b & 0xFFFF0000u);
 }
 
-// The values of a word of codes as f16 pairs in the codes' order: two of four
-// E4M3 bytes, four of eight E2M1 nibbles.  The unpacking of the word inside
-// the asm lets each conversion take its byte where it lies.
-template <int FMT>
-struct Codes {
-  static constexpr int kPairs = FMT == MXQ_FMT_FP8 ? 2 : 4;
-};
-template <int FMT>
-__device__ __forceinline__ void decode_word(uint32_t w, uint32_t* r) {
-  if constexpr (FMT == MXQ_FMT_FP8) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(r[0]), "=r"(r[1])
-        : "r"(w));
-  } else {
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-        : "r"(w));
-  }
-}
-
 // Place of 16-byte chunk `col` of row `row` in a tile of rows of CH chunks.
 // ROWS8: read 8 rows of one chunk at a time (K, ldmatrix); else four rows two
 // apart, the whole rows in 32-lane order (V).

@@ -94,6 +94,49 @@ __device__ __forceinline__ void decode8(uint2 c, float s, float* v) {
   }
 }
 
+// The values of a word of codes as f16 pairs in the codes' order: two of four
+// E4M3 bytes, four of eight E2M1 nibbles.  The unpacking of the word inside
+// the asm lets each conversion take its byte where it lies.
+template <int FMT>
+struct Codes {
+  static constexpr int kPairs = FMT == MXQ_FMT_FP8 ? 2 : 4;
+};
+template <int FMT>
+__device__ __forceinline__ void decode_word(uint32_t w, uint32_t* r) {
+  if constexpr (FMT == MXQ_FMT_FP8) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(r[0]), "=r"(r[1])
+        : "r"(w));
+  } else {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(w));
+  }
+}
+
+// Eight values (code times scale, exact in f32) of one (fp4) or two words.
+template <int FMT>
+__device__ __forceinline__ void values8(const uint32_t* w, float s, float* v) {
+  uint32_t h[4];
+  decode_word<FMT>(w[0], h);
+  if constexpr (FMT == MXQ_FMT_FP8) decode_word<FMT>(w[1], h + 2);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+    mul2_rn(v[2 * j], v[2 * j + 1], x.x, x.y, s, s);
+  }
+}
+
+// The scale of a byte that stands for a finite one.
+template <int FMT>
+__device__ __forceinline__ float finite_scale(uint32_t byte) {
+  if constexpr (FMT == MXQ_FMT_NVFP4) return f16lo(e4m3x2_to_f16x2(byte));
+  else return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
+}
+
 template <int FMT>
 __device__ __forceinline__ void store_codes(void* codes, int64_t item, uint2 c) {
   if constexpr (FMT == MXQ_FMT_FP8) {

@@ -70,60 +70,105 @@ __device__ __forceinline__ void check_offs(const AppendArgs& a) {
 
 constexpr int kMaxCtaTokens = 32;
 
+// Quotients of 31-bit numbers by a divisor known at launch: floor(x m / 2^s)
+// with m = floor(2^s / d) + 1 and s = 31 + ceil(log2 d) is exact for x < 2^31
+// (Granlund and Montgomery, "Division by invariant integers", 1994).
+struct Divisor {
+  uint32_t d, shift;
+  uint64_t m;
+  explicit Divisor(uint32_t x = 1) : d(x), shift(31), m(0) {
+    while (((uint64_t)1 << (shift - 31)) < d) ++shift;
+    m = ((uint64_t)1 << shift) / d + 1;
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t x) const { return (uint32_t)(x * m >> shift); }
+};
+
+struct AppendPlan {
+  Divisor per_tok, per_head;  // items of a token, of a head
+  uint32_t per_row;           // of a token's K
+};
+
+// Magnitude of the largest of eight elements, as f32 bits.
+template <int DT>
+__device__ __forceinline__ uint32_t amax8(const uint32_t* w) {
+  if constexpr (ElemTraits<DT>::kBytes == 2) {  // 16-bit magnitudes order as integers
+    const uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    return max(m & 0xFFFFu, m >> 16);
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, w[j] & 0x7FFFFFFFu);
+    return m;
+  }
+}
+
 // Fast path.  An item is 8 channels of one row of K or V; a block takes
 // tokens_per_cta tokens (all heads, K and V), about 4 items a thread, so that
-// each thread has several loads in flight; B/8 lanes share a group's maximum.
-// The slot of each token is looked up once per block.
+// each thread has several loads in flight; B/8 lanes share a group's maximum,
+// taken on the raw 16-bit magnitudes.  The place of each token is looked up
+// once per block.
 template <int DT, int FMT, int LPB>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
-  __shared__ int64_t s_slot[kMaxCtaTokens];
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, AppendPlan plan) {
+  __shared__ int64_t s_row[kMaxCtaTokens];  // of head 0 in the cache; heads are S rows apart
   constexpr int kUnroll = ElemTraits<DT>::kBytes == 2 ? 4 : 2;
+  constexpr int kWords = ElemTraits<DT>::kBytes == 2 ? 4 : 8;
   const PagedCache& c = a.c;
   const int64_t t0 = (int64_t)blockIdx.x * a.tokens_per_cta;
   const int n_tok = (int)min((int64_t)a.tokens_per_cta, a.rows - t0);
-  const int per_head = c.dim / 8, per_row = c.heads * per_head;
-  const int per_tok = per_row * (a.v ? 2 : 1), n_items = n_tok * per_tok;
+  const uint32_t n_items = n_tok * plan.per_tok.d, per_head = plan.per_head.d;
   check_offs(a);
-  if ((int)threadIdx.x < n_tok) s_slot[threadIdx.x] = slot_of_row(a, t0 + threadIdx.x);
+  if ((int)threadIdx.x < n_tok) {
+    const int64_t slot = slot_of_row(a, t0 + threadIdx.x);
+    const int64_t page = slot / c.page;
+    s_row[threadIdx.x] = slot < 0 ? -1 : page * c.heads * c.page + (slot - page * c.page);
+  }
   __syncthreads();
-  const int lane = threadIdx.x & 31;
-  for (int base = threadIdx.x & ~31; base < n_items; base += kThreads * kUnroll) {
-    uint32_t bits[kUnroll][8];
+  const uint32_t lane = threadIdx.x & 31;
+  for (uint32_t base = threadIdx.x & ~31; base < n_items; base += kThreads * kUnroll) {
+    uint32_t w[kUnroll][kWords];
     int64_t dst[kUnroll], src[kUnroll];
     bool is_v[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int item = base + u * kThreads + lane;
+      const uint32_t item = base + u * kThreads + lane;
       dst[u] = -1;
       if (item >= n_items) continue;
-      const int tok = item / per_tok;
-      int rem = item - tok * per_tok;
-      is_v[u] = rem >= per_row;
-      if (is_v[u]) rem -= per_row;
-      const int64_t slot = s_slot[tok];
-      if (slot < 0) continue;
-      const int head = rem / per_head, c8 = rem - head * per_head;
-      const int64_t page = slot / c.page, off = slot - page * c.page;
-      dst[u] = ((page * c.heads + head) * c.page + off) * per_head + c8;  // in items
-      src[u] = (t0 + tok) * per_row + rem;                                // dense, in items
-      const int64_t row = (t0 + tok) * ((is_v[u] ? a.v_stride : a.k_stride) / 8) + rem;
-      if (MXQ_IN_RANGE(kChkAppendIn, t0 + tok, a.rows)) load8<DT>(is_v[u] ? a.v : a.k, row, bits[u]);
+      const uint32_t tok = plan.per_tok.div(item);
+      uint32_t rem = item - tok * plan.per_tok.d;
+      is_v[u] = rem >= plan.per_row;
+      if (is_v[u]) rem -= plan.per_row;
+      const int64_t row = s_row[tok];
+      if (row < 0) continue;
+      const uint32_t head = plan.per_head.div(rem);
+      dst[u] = (row + (int64_t)head * c.page) * per_head + (rem - head * per_head);  // in items
+      src[u] = (t0 + tok) * plan.per_row + rem;                                     // dense
+      const int64_t in = (t0 + tok) * ((is_v[u] ? a.v_stride : a.k_stride) / 8) + rem;
+      const char* from = (const char*)(is_v[u] ? a.v : a.k) + in * (8 * ElemTraits<DT>::kBytes);
+      if (MXQ_IN_RANGE(kChkAppendIn, t0 + tok, a.rows)) {
+#pragma unroll
+        for (int j = 0; j < kWords; j += 4) {
+          const uint4 v = ld_stream_v4(from + 4 * j);
+          w[u][j] = v.x, w[u][j + 1] = v.y, w[u][j + 2] = v.z, w[u][j + 3] = v.w;
+        }
+      }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const bool valid = dst[u] >= 0;
-      uint32_t m = 0;
-      if (valid) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, mag_as_f32_bits<DT>(bits[u][j]));
-      }
+      uint32_t m = valid ? amax8<DT>(w[u]) : 0;
 #pragma unroll
       for (int o = 1; o < LPB; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
       if (!valid) continue;
-      const int k = group_scale_exp<FMT>(m);
+      const int k = group_scale_exp<FMT>(mag_as_f32_bits<DT>(m));
       float x[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = elem_to_f32<DT>(bits[u][j]);
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (kWords == 4)
+          x[j] = elem_to_f32<DT>((j & 1) ? w[u][j / 2] >> 16 : w[u][j / 2] & 0xFFFFu);
+        else
+          x[j] = elem_to_f32<DT>(w[u][j]);
+      }
       const uint2 code = encode8<FMT>(x, exp2i(-k));
       if (MXQ_IN_RANGE(kChkAppendOut, dst[u], c.num_pages * c.heads * c.page * per_head))
         store_codes<FMT>(is_v[u] ? c.v_codes : c.k_codes, dst[u], code);
@@ -135,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
       if (out) {
         float y[8];
         decode8<FMT>(code, exp2i(k), y);
-        if (MXQ_IN_RANGE(kChkAppendOut, src[u], a.rows * per_row)) store8<DT>(out, src[u], y);
+        if (MXQ_IN_RANGE(kChkAppendOut, src[u], a.rows * plan.per_row)) store8<DT>(out, src[u], y);
       }
     }
   }
@@ -211,13 +256,17 @@ void launch_append_fmt(AppendArgs a, bool fast, cudaStream_t st) {
   a.tokens_per_cta = (int)(per_tok >= 1024 ? 1 : 1024 / per_tok);
   if (a.tokens_per_cta > kMaxCtaTokens) a.tokens_per_cta = kMaxCtaTokens;
   const unsigned grid = (unsigned)((a.rows + a.tokens_per_cta - 1) / a.tokens_per_cta);
+  AppendPlan plan;
+  plan.per_tok = Divisor((uint32_t)per_tok);
+  plan.per_head = Divisor((uint32_t)(a.c.dim / 8));
+  plan.per_row = (uint32_t)(a.c.heads * (a.c.dim / 8));
   switch (a.c.block / 8) {
-    case 1: append_kernel<DT, FMT, 1><<<grid, kThreads, 0, st>>>(a); break;
-    case 2: append_kernel<DT, FMT, 2><<<grid, kThreads, 0, st>>>(a); break;
-    case 4: append_kernel<DT, FMT, 4><<<grid, kThreads, 0, st>>>(a); break;
-    case 8: append_kernel<DT, FMT, 8><<<grid, kThreads, 0, st>>>(a); break;
-    case 16: append_kernel<DT, FMT, 16><<<grid, kThreads, 0, st>>>(a); break;
-    default: append_kernel<DT, FMT, 32><<<grid, kThreads, 0, st>>>(a); break;
+    case 1: append_kernel<DT, FMT, 1><<<grid, kThreads, 0, st>>>(a, plan); break;
+    case 2: append_kernel<DT, FMT, 2><<<grid, kThreads, 0, st>>>(a, plan); break;
+    case 4: append_kernel<DT, FMT, 4><<<grid, kThreads, 0, st>>>(a, plan); break;
+    case 8: append_kernel<DT, FMT, 8><<<grid, kThreads, 0, st>>>(a, plan); break;
+    case 16: append_kernel<DT, FMT, 16><<<grid, kThreads, 0, st>>>(a, plan); break;
+    default: append_kernel<DT, FMT, 32><<<grid, kThreads, 0, st>>>(a, plan); break;
   }
 }
 
@@ -251,29 +300,49 @@ __device__ __forceinline__ float value_at(const uint8_t* codes, const uint8_t* s
   }
 }
 
-// One block per (page of a sequence, head); pages counted from the sequence's
-// last.  VEC = 8: a thread holds 8 channels' bounds over every (threads /
-// (D/8))-th row, and the rows' threads are joined in shared memory.  VEC = 1:
-// a thread holds one channel over all rows, for any block size and alignment.
+constexpr int kBoundThreads = 128;
+
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// One warp per (page of a sequence, head), pages counted from the sequence's
+// last; a block takes four pages that follow one another.  VEC = 8 or 16
+// channels a lane: D / VEC lanes hold a row, the other lanes further rows,
+// eight rows a lane in flight; two rows at a time go into the running bounds
+// (one three-way minimum and maximum for two values: these and the
+// conversions, not the bytes, are what the kernel issues most), and the lanes
+// of a channel are joined by shuffles.  (A block per page, its warps joined in
+// shared memory, spent more on starting 33 thousand blocks than on the rows:
+// 84 us against 45 for 136 thousand tokens x 8 heads in fp8.)  VEC = 1: a lane
+// holds one channel over all rows, for any block size and alignment.
 template <int FMT, int VEC>
-__global__ void __launch_bounds__(kThreads) bound_kernel(BoundArgs a) {
-  extern __shared__ float s_part[];  // [row threads][2][D], VEC = 8 only
+__global__ void __launch_bounds__(kBoundThreads) bound_kernel(BoundArgs a) {
   const PagedCache& c = a.c;
   const int64_t b = blockIdx.y;
-  const int head = blockIdx.z;
+  const int head = blockIdx.z, lane = threadIdx.x & 31;
   const int64_t len = c.lengths[b];
   if (len < 0 || len > c.max_pages * c.page) {
     if (c.status) *c.status = MXQ_ERR_BAD_PAGE;
     return;
   }
-  const int64_t n_pages = (len + c.page - 1) / c.page, j = n_pages - 1 - blockIdx.x;
-  if (j < 0 || (j + 1) * c.page <= len - a.new_tokens) return;
+  // lengths end at 2^30
+  const int n_pages = ((uint32_t)len + c.page - 1) / (uint32_t)c.page;
+  const int j = n_pages - 1 - (int)(blockIdx.x * (kBoundThreads / 32) + (threadIdx.x >> 5));
+  if (j < 0 || (int64_t)(j + 1) * c.page <= len - a.new_tokens) return;
   const int64_t page = c.page_table[b * c.max_pages + j];
   if (page < 0 || page >= c.num_pages) {
     if (c.status) *c.status = MXQ_ERR_BAD_PAGE;
     return;
   }
-  const int rows = (int)min((int64_t)c.page, len - j * c.page);
+  const int rows = min(c.page, (int)len - j * c.page);
   const int rb = c.row_bytes(), nb = c.row_scales();
   const int64_t row0 = (page * c.heads + head) * c.page;
   const uint8_t* codes = c.k_codes + row0 * rb;
@@ -281,39 +350,73 @@ __global__ void __launch_bounds__(kThreads) bound_kernel(BoundArgs a) {
   uint16_t* out = a.bounds + (page * c.heads + head) * 2 * c.dim;
   [[maybe_unused]] const int64_t n_rows = c.num_pages * c.heads * c.page;
   const float inf = __int_as_float(0x7F800000);
-  if constexpr (VEC == 8) {
-    const int per_row = c.dim / 8, n_thr = kThreads / per_row;  // rows at a time
-    const int r = threadIdx.x / per_row, c8 = threadIdx.x - r * per_row;
-    float lo[8], hi[8];
+  if constexpr (VEC > 1) {
+    constexpr int UNROLL = 8;
+    constexpr int WORDS = FMT == MXQ_FMT_FP8 ? VEC / 4 : VEC / 8;  // of a lane's codes of a row
+    const int per_row = c.dim / VEC;
+    for (int lane0 = 0; lane0 < per_row; lane0 += 32) {  // heads wider than a warp
+      const int width = min(32, per_row - lane0), at_once = 32 / width;
+      const int r = lane / width, cv = lane0 + lane - r * width, sb = cv * VEC / c.block;
+      float lo[VEC], hi[VEC];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) lo[i] = inf, hi[i] = -inf;
-    if (r < n_thr) {
-#pragma unroll 4
-      for (int s = r; s < rows; s += n_thr) {
-        if (!MXQ_IN_RANGE(kChkBoundIn, row0 + s, n_rows)) continue;
-        float v[8];
-        decode8<FMT>(load_codes<FMT>(codes, (int64_t)s * per_row + c8),
-                     scale_value<FMT>(__ldg(scales + s * nb + c8 * 8 / c.block)), v);
+      for (int i = 0; i < VEC; ++i) lo[i] = inf, hi[i] = -inf;
+      if (r < at_once) {
+        for (int s = r; s < rows; s += at_once * UNROLL) {
+          uint32_t w[UNROLL][WORDS], sc[UNROLL];
+          const uint8_t* p = codes + (uint32_t)(s * rb) + cv * (WORDS * 4);
+          const uint8_t* ps = scales + (uint32_t)(s * nb) + sb;
+          // past the end: the batch's first row again, which changes no bound
+          const int left = (rows - s + at_once - 1) / at_once;
+          if (!MXQ_IN_RANGE(kChkBoundIn, row0 + s + (min(left, UNROLL) - 1) * at_once, n_rows))
+            break;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) lo[i] = fminf(lo[i], v[i]), hi[i] = fmaxf(hi[i], v[i]);
-      }
+          for (int u = 0; u < UNROLL; ++u) {
+            const int step = u < left ? u * at_once : 0;
+            const uint32_t* q = (const uint32_t*)(p + step * rb);
+            if constexpr (WORDS == 2) {
+              const uint2 v = __ldg((const uint2*)q);
+              w[u][0] = v.x, w[u][1] = v.y;
+            } else {
+              w[u][0] = __ldg(q);
+            }
+            sc[u] = __ldg(ps + step * nb);
+          }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s_part[(r * 2) * c.dim + c8 * 8 + i] = lo[i];
-        s_part[(r * 2 + 1) * c.dim + c8 * 8 + i] = hi[i];
+          for (int u = 0; u < UNROLL; u += 2) {
+            float v[2][VEC];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float f = finite_scale<FMT>(sc[u + q]);
+#pragma unroll
+              for (int x = 0; x < VEC / 8; ++x)
+                values8<FMT>(w[u + q] + x * (WORDS * 8 / VEC), f, v[q] + 8 * x);
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              lo[i] = min3(lo[i], v[0][i], v[1][i]);
+              hi[i] = max3(hi[i], v[0][i], v[1][i]);
+            }
+          }
+        }
       }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * c.dim; i += kThreads) {
-      float v = s_part[i];
-      for (int q = 1; q < min(n_thr, rows); ++q) {
-        const float w = s_part[q * 2 * c.dim + i];
-        v = i < c.dim ? fminf(v, w) : fmaxf(v, w);
+      for (int q = 1; q < at_once; ++q) {
+        const int from = (lane + q * width) & 31;  // of use in the first row's lanes
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          lo[i] = fminf(lo[i], __shfl_sync(0xffffffffu, lo[i], from));
+          hi[i] = fmaxf(hi[i], __shfl_sync(0xffffffffu, hi[i], from));
+        }
       }
-      out[i] = (uint16_t)(pack2<kBF16>(v, 0.0f) & 0xFFFFu);
+      if (r == 0 && MXQ_IN_RANGE(kChkBoundOut, page, c.num_pages)) {
+#pragma unroll
+        for (int x = 0; x < VEC / 8; ++x) {
+          store8<kBF16>(out + cv * VEC + 8 * x, 0, lo + 8 * x);
+          store8<kBF16>(out + c.dim + cv * VEC + 8 * x, 0, hi + 8 * x);
+        }
+      }
     }
   } else {
-    for (int ch = threadIdx.x; ch < c.dim; ch += kThreads) {
+    for (int ch = lane; ch < c.dim; ch += 32) {
       float lo = inf, hi = -inf;
       for (int s = 0; s < rows; ++s) {
         if (!MXQ_IN_RANGE(kChkBoundIn, row0 + s, n_rows)) continue;
@@ -329,12 +432,11 @@ __global__ void __launch_bounds__(kThreads) bound_kernel(BoundArgs a) {
 
 template <int FMT>
 void launch_bound_fmt(const BoundArgs& a, bool fast, dim3 grid, cudaStream_t st) {
-  if (fast) {
-    const int n_thr = kThreads / (a.c.dim / 8);
-    bound_kernel<FMT, 8><<<grid, kThreads, (size_t)n_thr * 2 * a.c.dim * 4, st>>>(a);
-  } else {
-    bound_kernel<FMT, 1><<<grid, kThreads, 0, st>>>(a);
-  }
+  // a lane takes 8 bytes of codes where the scale blocks allow it
+  if (!fast) bound_kernel<FMT, 1><<<grid, kBoundThreads, 0, st>>>(a);
+  else if (FMT != MXQ_FMT_FP8 && a.c.block % 16 == 0)
+    bound_kernel<FMT, FMT != MXQ_FMT_FP8 ? 16 : 8><<<grid, kBoundThreads, 0, st>>>(a);
+  else bound_kernel<FMT, 8><<<grid, kBoundThreads, 0, st>>>(a);
 }
 
 }  // namespace
@@ -363,7 +465,7 @@ int launch_bound_cache_pages(const PagedCache& c, int64_t new_tokens, void* boun
     part.c.page_table += b * c.max_pages;
     part.c.lengths += b;
     part.c.n_seqs = c.n_seqs - b < 65535 ? c.n_seqs - b : 65535;
-    const dim3 grid((unsigned)pages, (unsigned)part.c.n_seqs, (unsigned)c.heads);
+    const dim3 grid((unsigned)((pages + 3) / 4), (unsigned)part.c.n_seqs, (unsigned)c.heads);
     switch (c.fmt) {
       case MXQ_FMT_FP8: launch_bound_fmt<MXQ_FMT_FP8>(part, fast, grid, st); break;
       case MXQ_FMT_MXFP4: launch_bound_fmt<MXQ_FMT_MXFP4>(part, fast, grid, st); break;
