@@ -2,10 +2,10 @@
 // kernel for any head size, block size, page size and alignment, and the join
 // of the parts of pairs that were split (see cache_attend.cuh).
 //
-// General kernel: a warp takes one token at a time, lanes hold channels; per
+// General kernel: a warp takes four tokens at a time, lanes hold channels; per
 // query head one dot product (a warp sum), the running maximum m, sum l and
-// weighted values o of the softmax in f32: with s the token's logit in base 2,
-//   m' = max(m, s), l = l 2^(m-m') + 2^(s-m'), o = o 2^(m-m') + 2^(s-m') v.
+// weighted values o of the softmax in f32: with s the tokens' logits in base 2,
+//   m' = max(m, s), l = l 2^(m-m') + sum 2^(s-m'), o = o 2^(m-m') + sum 2^(s-m') v.
 // The warps' sums are joined in shared memory in a fixed order.
 #include "cache_attend.cuh"
 #include "sm100_primitives.cuh"
@@ -16,84 +16,132 @@ namespace attend {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kGeneralHeads = 4;  // query heads a warp carries at once
+constexpr int kTokens = 4;  // a warp has under way at once
+// Query heads a warp carries, by channels per lane: their queries and sums
+// stay in registers.
+constexpr int general_heads(int dim) { return dim <= 128 ? 8 : dim <= 256 ? 4 : 2; }
+
+// Where a lane finds channel ch of a row: its byte of codes, nibble and scale.
+struct Where {
+  int byte, shift, scale;
+};
 
 template <int FMT>
-__device__ __forceinline__ float cache_value(const uint8_t* codes, const uint8_t* scales, int ch,
-                                             int B) {
-  const float s = scale_value<FMT>(scales[ch / B]);
-  if constexpr (FMT == MXQ_FMT_FP8) {
-    return f16lo(e4m3x2_to_f16x2(codes[ch])) * s;
-  } else {
-    const uint32_t byte = codes[ch / 2];
-    return fmaf(f16lo(e2m1x2_to_f16x2((ch & 1) ? byte >> 4 : byte & 15u)), s, 0.0f);
-  }
+__device__ __forceinline__ Where where(int ch, int B) {
+  if constexpr (FMT == MXQ_FMT_FP8) return Where{ch, 0, ch / B};
+  else return Where{ch / 2, (ch & 1) * 4, ch / B};
 }
 
-// NC: channels per lane (head_dim at most 32 NC).
-template <int FMT, int NC>
+template <int FMT>
+__device__ __forceinline__ float cache_value(uint32_t code, uint32_t scale, int shift) {
+  const float s = scale_value<FMT>(scale);
+  if constexpr (FMT == MXQ_FMT_FP8) return f16lo(e4m3x2_to_f16x2(code)) * s;
+  else return fmaf(f16lo(e2m1x2_to_f16x2(code >> shift & 15u)), s, 0.0f);
+}
+
+// NC: channels per lane (head_dim at most 32 NC); HEADS: query heads at once.
+template <int FMT, int NC, int HEADS>
 __global__ void __launch_bounds__(kThreads) attend_general_kernel(Args a, int dt) {
   extern __shared__ float s_part[];  // [warps][heads][dim + 2]
   const PagedCache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = c.dim;
   const int rb = c.row_bytes(), nb = c.row_scales(), stride = D + 2;
   [[maybe_unused]] const int64_t n_rows = c.num_pages * c.heads * c.page;
-  walk<kWarps>(a, [&](const Span& s, const Target& t, int v0, int v1) {
-    const int r0 = t.tile * kGeneralHeads, heads = min(kGeneralHeads, a.group - r0);
-    float q[kGeneralHeads][NC], o[kGeneralHeads][NC], m[kGeneralHeads], l[kGeneralHeads];
+  Where at[NC];
 #pragma unroll
-    for (int r = 0; r < kGeneralHeads; ++r) {
+  for (int i = 0; i < NC; ++i) at[i] = where<FMT>(min(lane + 32 * i, D - 1), c.block);
+  walk<kWarps>(a, [&](const Span& s, const Target& t, int v0, int v1) {
+    const int r0 = t.tile * HEADS, heads = min(HEADS, a.group - r0);
+    float q[HEADS][NC], o[HEADS][NC], m[HEADS], l[HEADS];
+#pragma unroll
+    for (int r = 0; r < HEADS; ++r) {
       m[r] = kLowest;
       l[r] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int ch = lane + 32 * i;
-        o[r][i] = q[r][i] = 0.0f;
+        o[r][i] = q[r][i] = 0.0f;  // a lane past the last channel adds nothing
         if (r < heads && ch < D)
           q[r][i] = a.scale_log2 *
                     load_q(a, dt, t.b * a.q_stride + ((int64_t)t.head * a.group + r0 + r) * D + ch);
       }
     }
-    for (int v = v0 + warp; v < v1; v += kWarps) {
-      const Token tok = token_at(a, s, t.b, t.head, v);
-      if (tok.row < 0 || !live(a, s, tok.pos) || !MXQ_IN_RANGE(kChkAttendIn, tok.row, n_rows))
-        continue;
-      float k[NC], x[kGeneralHeads];
+    // kTokens of a warp's tokens at a time, kWarps apart
+    for (int v = v0 + warp; v < v1; v += kWarps * kTokens) {
+      int64_t row[kTokens];
+      uint32_t kc[kTokens][NC], ks[kTokens][NC], vc[kTokens][NC], vs[kTokens][NC];
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int ch = lane + 32 * i;
-        k[i] = ch < D ? cache_value<FMT>(c.k_codes + tok.row * rb, c.k_scales + tok.row * nb, ch,
-                                         c.block)
-                      : 0.0f;
+      for (int y = 0; y < kTokens; ++y) {
+        row[y] = -1;
+        const int vy = v + y * kWarps;
+        if (vy >= v1) continue;
+        const Token tok = token_at(a, s, t.b, t.head, vy);
+        if (tok.row < 0 || !live(a, s, tok.pos) || !MXQ_IN_RANGE(kChkAttendIn, tok.row, n_rows))
+          continue;
+        row[y] = tok.row;
       }
 #pragma unroll
-      for (int r = 0; r < kGeneralHeads; ++r) {
-        x[r] = 0.0f;
+      for (int y = 0; y < kTokens; ++y) {
+        if (row[y] < 0) continue;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) x[r] = fmaf(q[r][i], k[i], x[r]);
+        for (int i = 0; i < NC; ++i) {
+          kc[y][i] = c.k_codes[row[y] * rb + at[i].byte];
+          ks[y][i] = c.k_scales[row[y] * nb + at[i].scale];
+          vc[y][i] = c.v_codes[row[y] * rb + at[i].byte];
+          vs[y][i] = c.v_scales[row[y] * nb + at[i].scale];
+        }
+      }
+      float x[kTokens][HEADS];
 #pragma unroll
-        for (int w = 16; w > 0; w >>= 1) x[r] += __shfl_xor_sync(0xffffffffu, x[r], w);
+      for (int y = 0; y < kTokens; ++y) {
+#pragma unroll
+        for (int r = 0; r < HEADS; ++r) x[y][r] = 0.0f;
+        if (row[y] < 0) continue;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const float k = cache_value<FMT>(kc[y][i], ks[y][i], at[i].shift);
+#pragma unroll
+          for (int r = 0; r < HEADS; ++r) x[y][r] = fmaf(q[r][i], k, x[y][r]);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int ch = lane + 32 * i;
-        k[i] = ch < D ? cache_value<FMT>(c.v_codes + tok.row * rb, c.v_scales + tok.row * nb, ch,
-                                         c.block)
-                      : 0.0f;
-      }
+      for (int y = 0; y < kTokens; ++y)
 #pragma unroll
-      for (int r = 0; r < kGeneralHeads; ++r) {
-        const float mn = fmaxf(m[r], x[r]), keep = exp2f(m[r] - mn), p = exp2f(x[r] - mn);
+        for (int r = 0; r < HEADS; ++r)
+#pragma unroll
+          for (int w = 16; w > 0; w >>= 1) x[y][r] += __shfl_xor_sync(0xffffffffu, x[y][r], w);
+#pragma unroll
+      for (int r = 0; r < HEADS; ++r) {
+        float mn = m[r];
+#pragma unroll
+        for (int y = 0; y < kTokens; ++y)
+          if (row[y] >= 0) mn = fmaxf(mn, x[y][r]);
+        const float keep = exp2f(m[r] - mn);
         m[r] = mn;
-        l[r] = fmaf(l[r], keep, p);
+        l[r] *= keep;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) o[r][i] = fmaf(o[r][i], keep, p * k[i]);
+        for (int i = 0; i < NC; ++i) o[r][i] *= keep;
+#pragma unroll
+        for (int y = 0; y < kTokens; ++y) {
+          x[y][r] = row[y] >= 0 ? exp2f(x[y][r] - mn) : 0.0f;
+          l[r] += x[y][r];
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < kTokens; ++y) {
+        if (row[y] < 0) continue;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const float val = cache_value<FMT>(vc[y][i], vs[y][i], at[i].shift);
+#pragma unroll
+          for (int r = 0; r < HEADS; ++r) o[r][i] = fmaf(x[y][r], val, o[r][i]);
+        }
       }
     }
     __syncthreads();  // the previous pair's sums have been read
 #pragma unroll
-    for (int r = 0; r < kGeneralHeads; ++r) {
-      float* mine = s_part + (warp * kGeneralHeads + r) * stride;
+    for (int r = 0; r < HEADS; ++r) {
+      float* mine = s_part + (warp * HEADS + r) * stride;
 #pragma unroll
       for (int i = 0; i < NC; ++i)
         if (lane + 32 * i < D) mine[lane + 32 * i] = o[r][i];
@@ -103,10 +151,9 @@ __global__ void __launch_bounds__(kThreads) attend_general_kernel(Args a, int dt
     for (int i = threadIdx.x; i < heads * D; i += kThreads) {
       const int r = i / D, ch = i - r * D;
       float top = kLowest, sum = 0.0f, val = 0.0f;
-      for (int w = 0; w < kWarps; ++w)
-        top = fmaxf(top, s_part[(w * kGeneralHeads + r) * stride + D]);
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_part[(w * HEADS + r) * stride + D]);
       for (int w = 0; w < kWarps; ++w) {
-        const float* p = s_part + (w * kGeneralHeads + r) * stride;
+        const float* p = s_part + (w * HEADS + r) * stride;
         const float f = exp2f(p[D] - top);
         sum = fmaf(p[D + 1], f, sum);
         val = fmaf(p[ch], f, val);
@@ -241,17 +288,17 @@ int launch_join(const Args& a, int dt, int grid, cudaStream_t st) {
 
 template <int FMT>
 int launch_general(const Args& a, int dt, int grid, cudaStream_t st) {
-  const int smem = kWarps * kGeneralHeads * (a.c.dim + 2) * 4;
+  const int smem = kWarps * a.tile_heads * (a.c.dim + 2) * 4;
   auto go = [&](auto kernel) {
     if (smem > 48 * 1024 && allow_dynamic_smem((const void*)kernel, smem) != cudaSuccess)
       return (int)MXQ_ERR_CUDA;
     kernel<<<grid, kThreads, smem, st>>>(a, dt);
     return (int)MXQ_OK;
   };
-  if (a.c.dim <= 64) return go(attend_general_kernel<FMT, 2>);
-  if (a.c.dim <= 128) return go(attend_general_kernel<FMT, 4>);
-  if (a.c.dim <= 256) return go(attend_general_kernel<FMT, 8>);
-  return go(attend_general_kernel<FMT, 16>);
+  if (a.c.dim <= 64) return go(attend_general_kernel<FMT, 2, general_heads(64)>);
+  if (a.c.dim <= 128) return go(attend_general_kernel<FMT, 4, general_heads(128)>);
+  if (a.c.dim <= 256) return go(attend_general_kernel<FMT, 8, general_heads(256)>);
+  return go(attend_general_kernel<FMT, 16, general_heads(512)>);
 }
 
 constexpr int kCtasPerSm = 4;  // at most, of any of the kernels
@@ -316,7 +363,7 @@ int launch_attend_cache_paged(const void* q, int dt, int64_t q_heads, int64_t q_
   // its registers (one f16 term, up to 128 channels): K and V are read once
   // for all of a tile
   const bool tc = tc_fits(a);
-  a.tile_heads = !tc ? kGeneralHeads : a.group > 8 && dt == kBF16 && c.dim <= 128 ? 16 : 8;
+  a.tile_heads = !tc ? general_heads(c.dim) : a.group > 8 && dt == kBF16 && c.dim <= 128 ? 16 : 8;
   a.head_tiles = (a.group + a.tile_heads - 1) / a.tile_heads;
   // no more blocks than units that there can be
   const int64_t span = selected ? top * c.page : (a.window > 0 ? a.window + 16 : lim);

@@ -13,6 +13,7 @@
 #include "mxq.h"
 #include "mxq_device.cuh"
 #include "mxq_launch.h"
+#include "sm100_primitives.cuh"
 
 namespace mxq {
 
@@ -56,8 +57,15 @@ __device__ __forceinline__ uint64_t ordered(double s) {
   return (u >> 63) ? ~u : u | (1ull << 63);
 }
 
+// The bf16 in the upper half of v, times 2^-896: its bits in a double's fields,
+// exactly so for every finite one (zeros and subnormals too), without the
+// conversion unit, which would bound the kernel.
+__device__ __forceinline__ double small_double(uint32_t v) {
+  return __hiloint2double((int)((v & 0x80000000u) | ((v >> 3) & 0x0FFFE000u)), 0);
+}
+
 // Keys of the pages.  A block takes 64 pages of one (sequence, head), a warp 8
-// of them; a lane holds NCH chunks of 8 entries of [Q-, Q+] in registers
+// of them at once; a lane holds NCH chunks of 8 entries of [Q-, Q+] in registers
 // against the same entries of the page's [lo, hi].  VEC: 16-byte loads.
 template <int NCH, bool VEC>
 __global__ void __launch_bounds__(kThreads) score_kernel(SelectArgs a, int dt) {
@@ -65,8 +73,8 @@ __global__ void __launch_bounds__(kThreads) score_kernel(SelectArgs a, int dt) {
   const PagedCache& c = a.c;
   const int64_t b = blockIdx.y;
   const int head = blockIdx.z, D = c.dim, n = pages_of(c, b);
-  const int p_block = blockIdx.x * kWarps * kPagesPerWarp;
-  if (p_block >= n) return;
+  constexpr int kPerBlock = kWarps * kPagesPerWarp;
+  if ((int)blockIdx.x * kPerBlock >= n) return;
   for (int ch = threadIdx.x; ch < D; ch += kThreads) {
     double neg = 0.0, pos = 0.0;
     const int64_t at = b * a.q_stride + (int64_t)head * a.group * D + ch;
@@ -86,77 +94,160 @@ __global__ void __launch_bounds__(kThreads) score_kernel(SelectArgs a, int dt) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = (lane + 32 * j) * 8 + i;
-      w[j][i] = e < 2 * D ? s_q[e] : 0.0;
+      w[j][i] = e < 2 * D ? s_q[e] * 0x1p800 : 0.0;  // against small_double's 2^-896
     }
   uint64_t* keys = a.keys + (b * c.heads + head) * c.max_pages;
   const int32_t* table = c.page_table + b * c.max_pages;
   [[maybe_unused]] const int64_t n_bounds = c.num_pages * c.heads;
-#pragma unroll 2
-  for (int i = 0; i < kPagesPerWarp; ++i) {
-    const int p = p_block + i * kWarps + warp;
-    if (p >= n) break;
-    const int64_t page = __ldg(table + p);
-    const bool ok = page >= 0 && page < c.num_pages;
-    double s = 0.0;
-    if (ok && MXQ_IN_RANGE(kChkSelectIn, page * c.heads + head, n_bounds)) {
-      const uint16_t* row = a.bounds + (page * c.heads + head) * 2 * D;
+  for (int p_block = blockIdx.x * kPerBlock; p_block < n; p_block += gridDim.x * kPerBlock) {
+    // this warp's 8 pages, their bounds' loads under way together
+    const int p0 = p_block + warp * kPagesPerWarp;
+    int row[kPagesPerWarp];  // pages, or -1
 #pragma unroll
-      for (int j = 0; j < NCH; ++j) {
-        const int e = (lane + 32 * j) * 8;
-        if (e >= 2 * D) continue;
-        uint32_t bits[8];
+    for (int i = 0; i < kPagesPerWarp; ++i) {
+      row[i] = -1;
+      if (p0 + i >= n) continue;
+      const int64_t page = __ldg(table + p0 + i);
+      if (page >= 0 && page < c.num_pages) row[i] = (int)page;
+      else if (lane == 0 && c.status) *c.status = MXQ_ERR_BAD_PAGE;
+    }
+    double s[kPagesPerWarp];
+#pragma unroll
+    for (int i = 0; i < kPagesPerWarp; ++i) s[i] = 0.0;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int e = (lane + 32 * j) * 8;
+      if (e >= 2 * D) continue;
+      uint32_t bits[kPagesPerWarp][4];
+#pragma unroll
+      for (int i = 0; i < kPagesPerWarp; ++i) {
+        const int64_t at = (int64_t)row[i] * c.heads + head;
+        const bool ok = row[i] >= 0 && MXQ_IN_RANGE(kChkSelectIn, at, n_bounds);
+        const uint16_t* from = a.bounds + at * 2 * D + e;
         if constexpr (VEC) {
-          load8<kBF16>(row + e, 0, bits);
+          const uint4 v = ok ? ld_stream_v4(from) : make_uint4(0u, 0u, 0u, 0u);
+          bits[i][0] = v.x, bits[i][1] = v.y, bits[i][2] = v.z, bits[i][3] = v.w;
         } else {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) bits[x] = e + x < 2 * D ? row[e + x] : 0u;
+          for (int x = 0; x < 4; ++x)
+            bits[i][x] = (ok && e + 2 * x < 2 * D ? from[2 * x] : 0u) |
+                         (ok && e + 2 * x + 1 < 2 * D ? (uint32_t)from[2 * x + 1] << 16 : 0u);
         }
-#pragma unroll
-        for (int x = 0; x < 8; ++x) s = fma((double)elem_to_f32<kBF16>(bits[x]), w[j][x], s);
       }
-    } else if (!ok && lane == 0 && c.status) {
-      *c.status = MXQ_ERR_BAD_PAGE;
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const bool keep = p < a.keep_first || p >= n - a.keep_last;
-    if (lane == 0 && MXQ_IN_RANGE(kChkSelectWs, p, c.max_pages))
-      keys[p] = keep ? ~0ull : ok ? ordered(s) : 0ull;
+      for (int i = 0; i < kPagesPerWarp; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          s[i] = fma(small_double(bits[i][x] << 16), w[j][2 * x], s[i]);
+          s[i] = fma(small_double(bits[i][x]), w[j][2 * x + 1], s[i]);
+        }
+    }
+    // the lanes' sums of 8 pages: three halvings leave a page to each 4 lanes
+#pragma unroll
+    for (int half = kPagesPerWarp / 2, o = 16; half > 0; half >>= 1, o >>= 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < half; ++i) {
+        const double give = up ? s[i] : s[i + half], keep = up ? s[i + half] : s[i];
+        s[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    }
+    s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
+    s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
+    const int mine = (lane & 16 ? 4 : 0) + (lane & 8 ? 2 : 0) + (lane & 4 ? 1 : 0), p = p0 + mine;
+    bool ok = false;
+#pragma unroll
+    for (int i = 0; i < kPagesPerWarp; ++i) ok |= i == mine && row[i] >= 0;
+    if ((lane & 3) == 0 && p < n && MXQ_IN_RANGE(kChkSelectWs, p, c.max_pages)) {
+      const bool keep = p < a.keep_first || p >= n - a.keep_last;
+      keys[p] = keep ? ~0ull : ok ? ordered(s[0]) : 0ull;
+    }
   }
 }
 
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kHeld = 8;  // keys a thread holds in registers: 4096 pages in all
+
 // The top largest of n keys, equal ones from the front, in ascending order of
 // their places.  The smallest chosen key is found by 8-bit digits from the
-// top: after each digit only the keys that share the chosen prefix matter, and
-// once that whole prefix is taken the lower digits do not.
-__global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
-  __shared__ int s_hist[256];
+// highest bit in which keys differ (above it all would count into one place):
+// after each digit only the keys that share the chosen prefix matter, and once
+// that whole prefix is taken the lower digits do not.  A thread holds the
+// keys of kHeld places that follow one another; where there are more, the
+// rest are read again for each digit.
+__global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
+  __shared__ int s_hist[2][256];
   __shared__ int s_digit, s_need, s_all;
-  __shared__ int s_gt[kWarps], s_eq[kWarps];
+  __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
+  __shared__ uint64_t s_differ[kSelWarps];
   const PagedCache& c = a.c;
   const int64_t b = blockIdx.y;
   const int head = blockIdx.x, n = pages_of(c, b), top = a.top;
   const uint64_t* keys = a.keys + (b * c.heads + head) * c.max_pages;
   int32_t* out = a.selected + (b * c.heads + head) * top;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x < 256) s_hist[0][threadIdx.x] = 0;
   if (n <= top) {
-    for (int i = threadIdx.x; i < top; i += kThreads) out[i] = i < n ? i : -1;
+    for (int i = threadIdx.x; i < top; i += kSelThreads) out[i] = i < n ? i : -1;
+    sm100::griddep_wait();  // the scores' kernel has its end before this one's
     return;
   }
-  uint64_t prefix = 0, mask = 0;
-  int need = top;  // of the keys that share the prefix
-  for (int shift = 56; shift >= 0; shift -= 8) {
-    s_hist[threadIdx.x] = 0;
-    __syncthreads();
-    for (int p = threadIdx.x; p < n; p += kThreads) {
-      const uint64_t k = keys[p];
-      if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & 255], 1);
+  sm100::griddep_wait();
+  const bool held = n <= kSelThreads * kHeld;
+  const int per = held ? kHeld : (n + kSelThreads - 1) / kSelThreads;
+  const int p0 = min(n, (int)threadIdx.x * per), p1 = min(n, p0 + per);
+  uint64_t k8[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) k8[i] = held && p0 + i < p1 ? keys[p0 + i] : 0ull;
+  auto each = [&](auto f) {  // f(place, key) of this thread's places in order
+    if (held) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (p0 + i < p1) f(p0 + i, k8[i]);
+    } else {
+      for (int p = p0; p < p1; ++p) f(p, keys[p]);
     }
+  };
+  // the bits in which the scored keys differ, and how many pages are kept anyway
+  const uint64_t some = keys[min(a.keep_first, n - 1)];
+  uint64_t differ = 0;
+  int kept = 0;
+  each([&](int, uint64_t k) {
+    if (k == ~0ull) ++kept;
+    else differ |= k ^ some;
+  });
+  const uint32_t dh = __reduce_or_sync(0xffffffffu, (uint32_t)(differ >> 32)),
+                 dl = __reduce_or_sync(0xffffffffu, (uint32_t)differ);
+  kept = __reduce_add_sync(0xffffffffu, kept);
+  if (lane == 0) {
+    s_differ[warp] = (uint64_t)dh << 32 | dl;
+    s_gt[warp] = kept;
+  }
+  __syncthreads();
+  differ = 0;
+  int need = top;  // of the keys that share the prefix
+  for (int i = 0; i < kSelWarps; ++i) differ |= s_differ[i], need -= s_gt[i];
+  int low = 64 - __clzll((long long)differ);  // bits still open
+  uint64_t mask = low == 64 ? 0ull : ~0ull << low, prefix = some & mask;
+  if (need <= 0) {  // only pages that are kept anyway
+    low = 0;
+    mask = prefix = ~0ull;
+    need = top;
+  }
+  for (int turn = 0; low > 0; turn ^= 1) {
+    const int width = min(8, low), shift = low - width;
+    const uint32_t digits = (1u << width) - 1;
+    int* hist = s_hist[turn];
+    each([&](int, uint64_t k) {
+      if ((k & mask) == prefix && k != ~0ull) atomicAdd(&hist[(uint32_t)(k >> shift) & digits], 1);
+    });
+    if (threadIdx.x < 256) s_hist[turn ^ 1][threadIdx.x] = 0;
     __syncthreads();
     if (warp == 0) {  // the digit where the count from above reaches need
       int local[8], sum = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) local[i] = s_hist[255 - (lane * 8 + i)], sum += local[i];
+      for (int i = 0; i < 8; ++i) local[i] = hist[255 - (lane * 8 + i)], sum += local[i];
       int before = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -178,39 +269,36 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
     }
     __syncthreads();
     prefix |= (uint64_t)s_digit << shift;
-    mask |= 255ull << shift;
+    low = shift;
+    mask = ~0ull << low;
     need = s_need;
-    const bool all = s_all != 0;
-    __syncthreads();
-    if (all) break;
+    if (s_all) break;
   }
   // every key above the prefix, and the first `need` that share it
-  const int per = (n + kThreads - 1) / kThreads, p0 = min(n, (int)threadIdx.x * per),
-            p1 = min(n, p0 + per);
   int gt = 0, eq = 0;
-  for (int p = p0; p < p1; ++p) {
-    const uint64_t k = keys[p] & mask;
-    gt += k > prefix;
-    eq += k == prefix;
-  }
+  each([&](int, uint64_t k) {
+    gt += (k & mask) > prefix;
+    eq += (k & mask) == prefix;
+  });
   int sg = gt, se = eq;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int yg = __shfl_up_sync(0xffffffffu, sg, o), ye = __shfl_up_sync(0xffffffffu, se, o);
     if (lane >= o) sg += yg, se += ye;
   }
+  __syncthreads();  // the kept pages' counts have been read
   if (lane == 31) s_gt[warp] = sg, s_eq[warp] = se;
   __syncthreads();
   int bg = sg - gt, be = se - eq;
   for (int i = 0; i < warp; ++i) bg += s_gt[i], be += s_eq[i];
-  for (int p = p0; p < p1; ++p) {
-    const uint64_t k = keys[p] & mask;
+  each([&](int p, uint64_t key) {
+    const uint64_t k = key & mask;
     const int at = bg + min(be, need);
     const bool take = k > prefix || (k == prefix && be < need);
     if (take && MXQ_IN_RANGE(kChkSelectOut, at, top)) out[at] = p;
     bg += k > prefix;
     be += k == prefix;
-  }
+  });
 }
 
 template <int NCH>
@@ -241,12 +329,30 @@ int launch_select_cache_pages(const void* q, int dt, int64_t q_heads, int64_t q_
     a.c.n_seqs = c.n_seqs - b < 65535 ? c.n_seqs - b : 65535;
     a.selected += b * c.heads * top;
     a.keys += b * c.heads * c.max_pages;
-    const dim3 grid((unsigned)((c.max_pages + per - 1) / per), (unsigned)a.c.n_seqs,
+    // enough blocks for four an SM; where there are fewer page blocks than
+    // that, one each (a block's queries cost as much as its first 64 pages)
+    const int64_t pairs = a.c.n_seqs * c.heads, page_blocks = (c.max_pages + per - 1) / per;
+    const int64_t wanted = (4 * num_sms() + pairs - 1) / pairs;
+    const dim3 grid((unsigned)(page_blocks < wanted ? page_blocks : wanted), (unsigned)a.c.n_seqs,
                     (unsigned)c.heads);
     if (c.dim <= 128) launch_score<1>(a, dt, vec, grid, st);
     else if (c.dim <= 256) launch_score<2>(a, dt, vec, grid, st);
     else launch_score<4>(a, dt, vec, grid, st);
-    select_kernel<<<dim3((unsigned)c.heads, (unsigned)a.c.n_seqs), kThreads, 0, st>>>(a);
+    // launched with programmatic stream serialization: it looks up its
+    // sequence while the scores' last blocks run
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)c.heads, (unsigned)a.c.n_seqs);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, select_kernel, a) != cudaSuccess) {
+      (void)cudaGetLastError();  // reported here
+      return MXQ_ERR_CUDA;
+    }
   }
   return cudaGetLastError() == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
