@@ -19,7 +19,7 @@ namespace mxq {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPagesPerWarp = 8;
 
@@ -64,104 +64,101 @@ __device__ __forceinline__ double small_double(uint32_t v) {
   return __hiloint2double((int)((v & 0x80000000u) | ((v >> 3) & 0x0FFFE000u)), 0);
 }
 
-// Keys of the pages.  A block takes 64 pages of one (sequence, head), a warp 8
-// of them at once; a lane holds NCH chunks of 8 entries of [Q-, Q+] in registers
-// against the same entries of the page's [lo, hi].  VEC: 16-byte loads.
+// Keys of the pages.  A block takes 32 pages of one (sequence, head), a warp 8
+// of them at once; a lane holds NCH chunks of 8 entries of [Q-, Q+] in
+// registers against the same entries of the pages' [lo, hi].  The loads of the
+// first chunk are under way while the block sums its queries: the chain of
+// length, page and bounds is what a block waits for.  VEC: 16-byte loads.
 template <int NCH, bool VEC>
 __global__ void __launch_bounds__(kThreads) score_kernel(SelectArgs a, int dt) {
   __shared__ double s_q[2 * 512];
   const PagedCache& c = a.c;
   const int64_t b = blockIdx.y;
   const int head = blockIdx.z, D = c.dim, n = pages_of(c, b);
-  constexpr int kPerBlock = kWarps * kPagesPerWarp;
-  if ((int)blockIdx.x * kPerBlock >= n) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if ((int)blockIdx.x * kWarps * kPagesPerWarp >= n) return;
+  uint64_t* keys = a.keys + (b * c.heads + head) * c.max_pages;
+  [[maybe_unused]] const int64_t n_bounds = c.num_pages * c.heads;
+  const int p0 = (blockIdx.x * kWarps + warp) * kPagesPerWarp;
+  int mine = -1;  // the page of p0 + lane, or -1
+  if (lane < kPagesPerWarp && p0 + lane < n) {
+    mine = __ldg(c.page_table + b * c.max_pages + p0 + lane);
+    if (mine < 0 || mine >= c.num_pages) {
+      mine = -1;
+      if (c.status) *c.status = MXQ_ERR_BAD_PAGE;
+    }
+  }
+  int page[kPagesPerWarp];
+#pragma unroll
+  for (int i = 0; i < kPagesPerWarp; ++i) page[i] = __shfl_sync(0xffffffffu, mine, i);
+  uint32_t bits[kPagesPerWarp][4];
+  auto load = [&](int j) {
+    const int e = (lane + 32 * j) * 8;
+#pragma unroll
+    for (int i = 0; i < kPagesPerWarp; ++i) {
+      const int64_t at = (int64_t)page[i] * c.heads + head;
+      const bool ok = page[i] >= 0 && e < 2 * D && MXQ_IN_RANGE(kChkSelectIn, at, n_bounds);
+      const uint16_t* from = a.bounds + at * 2 * D + e;
+      if constexpr (VEC) {
+        const uint4 v = ok ? ld_stream_v4(from) : make_uint4(0u, 0u, 0u, 0u);
+        bits[i][0] = v.x, bits[i][1] = v.y, bits[i][2] = v.z, bits[i][3] = v.w;
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          bits[i][x] = (ok && e + 2 * x < 2 * D ? from[2 * x] : 0u) |
+                       (ok && e + 2 * x + 1 < 2 * D ? (uint32_t)from[2 * x + 1] << 16 : 0u);
+      }
+    }
+  };
+  load(0);
   for (int ch = threadIdx.x; ch < D; ch += kThreads) {
     double neg = 0.0, pos = 0.0;
     const int64_t at = b * a.q_stride + (int64_t)head * a.group * D + ch;
+#pragma unroll 4
     for (int g = 0; g < a.group; ++g) {
       const double x = (double)q_at(a.q, dt, at + (int64_t)g * D);
-      if (x < 0.0) neg += x;
-      else pos += x;
+      neg += x < 0.0 ? x : 0.0;
+      pos += x < 0.0 ? 0.0 : x;
     }
-    s_q[ch] = neg;
-    s_q[D + ch] = pos;
+    s_q[ch] = neg * 0x1p800;  // against small_double's 2^-896
+    s_q[D + ch] = pos * 0x1p800;
   }
   __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  double w[NCH][8];
+  double s[kPagesPerWarp];
 #pragma unroll
-  for (int j = 0; j < NCH; ++j)
+  for (int i = 0; i < kPagesPerWarp; ++i) s[i] = 0.0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = (lane + 32 * j) * 8 + i;
-      w[j][i] = e < 2 * D ? s_q[e] * 0x1p800 : 0.0;  // against small_double's 2^-896
-    }
-  uint64_t* keys = a.keys + (b * c.heads + head) * c.max_pages;
-  const int32_t* table = c.page_table + b * c.max_pages;
-  [[maybe_unused]] const int64_t n_bounds = c.num_pages * c.heads;
-  for (int p_block = blockIdx.x * kPerBlock; p_block < n; p_block += gridDim.x * kPerBlock) {
-    // this warp's 8 pages, their bounds' loads under way together
-    const int p0 = p_block + warp * kPagesPerWarp;
-    int row[kPagesPerWarp];  // pages, or -1
+  for (int j = 0; j < NCH; ++j) {
+    if (j > 0) load(j);
+    const int e = (lane + 32 * j) * 8;
 #pragma unroll
-    for (int i = 0; i < kPagesPerWarp; ++i) {
-      row[i] = -1;
-      if (p0 + i >= n) continue;
-      const int64_t page = __ldg(table + p0 + i);
-      if (page >= 0 && page < c.num_pages) row[i] = (int)page;
-      else if (lane == 0 && c.status) *c.status = MXQ_ERR_BAD_PAGE;
-    }
-    double s[kPagesPerWarp];
-#pragma unroll
-    for (int i = 0; i < kPagesPerWarp; ++i) s[i] = 0.0;
-#pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      const int e = (lane + 32 * j) * 8;
-      if (e >= 2 * D) continue;
-      uint32_t bits[kPagesPerWarp][4];
+    for (int x = 0; x < 4; ++x) {
+      const double w0 = e + 2 * x < 2 * D ? s_q[e + 2 * x] : 0.0;
+      const double w1 = e + 2 * x + 1 < 2 * D ? s_q[e + 2 * x + 1] : 0.0;
 #pragma unroll
       for (int i = 0; i < kPagesPerWarp; ++i) {
-        const int64_t at = (int64_t)row[i] * c.heads + head;
-        const bool ok = row[i] >= 0 && MXQ_IN_RANGE(kChkSelectIn, at, n_bounds);
-        const uint16_t* from = a.bounds + at * 2 * D + e;
-        if constexpr (VEC) {
-          const uint4 v = ok ? ld_stream_v4(from) : make_uint4(0u, 0u, 0u, 0u);
-          bits[i][0] = v.x, bits[i][1] = v.y, bits[i][2] = v.z, bits[i][3] = v.w;
-        } else {
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            bits[i][x] = (ok && e + 2 * x < 2 * D ? from[2 * x] : 0u) |
-                         (ok && e + 2 * x + 1 < 2 * D ? (uint32_t)from[2 * x + 1] << 16 : 0u);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kPagesPerWarp; ++i)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          s[i] = fma(small_double(bits[i][x] << 16), w[j][2 * x], s[i]);
-          s[i] = fma(small_double(bits[i][x]), w[j][2 * x + 1], s[i]);
-        }
-    }
-    // the lanes' sums of 8 pages: three halvings leave a page to each 4 lanes
-#pragma unroll
-    for (int half = kPagesPerWarp / 2, o = 16; half > 0; half >>= 1, o >>= 1) {
-      const bool up = lane & o;
-#pragma unroll
-      for (int i = 0; i < half; ++i) {
-        const double give = up ? s[i] : s[i + half], keep = up ? s[i + half] : s[i];
-        s[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        s[i] = fma(small_double(bits[i][x] << 16), w0, s[i]);
+        s[i] = fma(small_double(bits[i][x]), w1, s[i]);
       }
     }
-    s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
-    s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
-    const int mine = (lane & 16 ? 4 : 0) + (lane & 8 ? 2 : 0) + (lane & 4 ? 1 : 0), p = p0 + mine;
-    bool ok = false;
+  }
+  // the lanes' sums of 8 pages: three halvings leave a page to each 4 lanes
 #pragma unroll
-    for (int i = 0; i < kPagesPerWarp; ++i) ok |= i == mine && row[i] >= 0;
-    if ((lane & 3) == 0 && p < n && MXQ_IN_RANGE(kChkSelectWs, p, c.max_pages)) {
-      const bool keep = p < a.keep_first || p >= n - a.keep_last;
-      keys[p] = keep ? ~0ull : ok ? ordered(s[0]) : 0ull;
+  for (int half = kPagesPerWarp / 2, o = 16; half > 0; half >>= 1, o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const double give = up ? s[i] : s[i + half], keep = up ? s[i + half] : s[i];
+      s[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
     }
+  }
+  s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
+  s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
+  const int of = (lane & 16 ? 4 : 0) + (lane & 8 ? 2 : 0) + (lane & 4 ? 1 : 0), p = p0 + of;
+  const bool ok = __shfl_sync(0xffffffffu, mine, of) >= 0;
+  if ((lane & 3) == 0 && p < n && MXQ_IN_RANGE(kChkSelectWs, p, c.max_pages)) {
+    const bool keep = p < a.keep_first || p >= n - a.keep_last;
+    keys[p] = keep ? ~0ull : ok ? ordered(s[0]) : 0ull;
   }
 }
 
@@ -329,11 +326,7 @@ int launch_select_cache_pages(const void* q, int dt, int64_t q_heads, int64_t q_
     a.c.n_seqs = c.n_seqs - b < 65535 ? c.n_seqs - b : 65535;
     a.selected += b * c.heads * top;
     a.keys += b * c.heads * c.max_pages;
-    // enough blocks for four an SM; where there are fewer page blocks than
-    // that, one each (a block's queries cost as much as its first 64 pages)
-    const int64_t pairs = a.c.n_seqs * c.heads, page_blocks = (c.max_pages + per - 1) / per;
-    const int64_t wanted = (4 * num_sms() + pairs - 1) / pairs;
-    const dim3 grid((unsigned)(page_blocks < wanted ? page_blocks : wanted), (unsigned)a.c.n_seqs,
+    const dim3 grid((unsigned)((c.max_pages + per - 1) / per), (unsigned)a.c.n_seqs,
                     (unsigned)c.heads);
     if (c.dim <= 128) launch_score<1>(a, dt, vec, grid, st);
     else if (c.dim <= 256) launch_score<2>(a, dt, vec, grid, st);
