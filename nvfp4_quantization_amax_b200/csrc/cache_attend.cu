@@ -2,9 +2,11 @@
 // kernel for any head size, block size, page size and alignment, and the join
 // of the parts of pairs that were split (see cache_attend.cuh).
 //
-// General kernel: a warp takes four tokens at a time, lanes hold channels; per
-// query head one dot product (a warp sum), the running maximum m, sum l and
-// weighted values o of the softmax in f32: with s the tokens' logits in base 2,
+// General kernel: a warp takes 4 tokens x 8 heads (8 x 4, 16 x 2 for wide heads)
+// at a time, lanes hold channels.  The 32 partial dot products are summed over
+// the lanes by halvings, 31 shuffles that leave each lane one (token, head): it
+// takes that exponential, and its weight is handed round for the values.  The
+// running maximum m, sum l and weighted values o of the softmax are f32:
 //   m' = max(m, s), l = l 2^(m-m') + sum 2^(s-m'), o = o 2^(m-m') + sum 2^(s-m') v.
 // The warps' sums are joined in shared memory in a fixed order.
 #include "cache_attend.cuh"
@@ -16,136 +18,187 @@ namespace attend {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTokens = 4;  // a warp has under way at once
-// Query heads a warp carries, by channels per lane: their queries and sums
-// stay in registers.
+// Query heads a warp carries, by channels per lane (their queries and sums stay
+// in registers), and tokens it has under way: a (token, head) for every lane.
 constexpr int general_heads(int dim) { return dim <= 128 ? 8 : dim <= 256 ? 4 : 2; }
 
-// Where a lane finds channel ch of a row: its byte of codes, nibble and scale.
-struct Where {
-  int byte, shift, scale;
+// NC channels of a row of codes, as the lane's bytes lie: NC (fp8) or NC / 2
+// bytes at once where the sizes allow it (WIDE), else one by one.
+template <int FMT, int NC, bool WIDE>
+struct Channels {
+  static constexpr int BYTES = FMT == MXQ_FMT_FP8 ? NC : NC / 2;
+  static constexpr int CODES = WIDE ? (BYTES + 3) / 4 : NC, SCALES = WIDE ? 1 : NC;
+  uint32_t code[CODES], scale[SCALES];
+
+  static __device__ __forceinline__ int channel(int lane, int i) {
+    return WIDE ? lane * NC + i : lane + 32 * i;
+  }
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int lane, int D,
+                                       int B) {
+    if constexpr (WIDE) {
+      if (lane * NC >= D) return;
+      const uint8_t* p = codes + lane * BYTES;
+      if constexpr (BYTES == 1) code[0] = *p;
+      else if constexpr (BYTES == 2) code[0] = *(const uint16_t*)p;
+      else if constexpr (BYTES == 4) code[0] = *(const uint32_t*)p;
+      else if constexpr (BYTES == 8) *(uint2*)code = *(const uint2*)p;
+      else *(uint4*)code = *(const uint4*)p;
+      scale[0] = scales[lane * NC / B];
+    } else {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int ch = min(lane + 32 * i, D - 1);
+        code[i] = codes[FMT == MXQ_FMT_FP8 ? ch : ch / 2] >> (FMT == MXQ_FMT_FP8 ? 0 : (ch & 1) * 4);
+        scale[i] = scales[ch / B];
+      }
+    }
+  }
+  // The values, exact in f32; 0 for a lane past the last channel.
+  __device__ __forceinline__ void values(float* v, int lane, int D) const {
+    if constexpr (WIDE) {
+      const bool in = lane * NC < D;
+      const float s = in ? scale_value<FMT>(scale[0]) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < NC; i += 2) {
+        const int bit = (FMT == MXQ_FMT_FP8 ? 8 : 4) * i;  // where the pair begins
+        const uint32_t w = in ? code[bit / 32] >> (bit % 32) : 0u;
+        const uint32_t h = FMT == MXQ_FMT_FP8 ? e4m3x2_to_f16x2(w & 0xFFFFu) : e2m1x2_to_f16x2(w & 0xFFu);
+        v[i] = f16lo(h) * s;
+        v[i + 1] = f16hi(h) * s;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const float s = scale_value<FMT>(scale[i]);
+        const uint32_t h = FMT == MXQ_FMT_FP8 ? e4m3x2_to_f16x2(code[i] & 0xFFu)
+                                              : e2m1x2_to_f16x2(code[i] & 15u);
+        v[i] = lane + 32 * i < D ? f16lo(h) * s : 0.0f;
+      }
+    }
+  }
 };
 
-template <int FMT>
-__device__ __forceinline__ Where where(int ch, int B) {
-  if constexpr (FMT == MXQ_FMT_FP8) return Where{ch, 0, ch / B};
-  else return Where{ch / 2, (ch & 1) * 4, ch / B};
-}
-
-template <int FMT>
-__device__ __forceinline__ float cache_value(uint32_t code, uint32_t scale, int shift) {
-  const float s = scale_value<FMT>(scale);
-  if constexpr (FMT == MXQ_FMT_FP8) return f16lo(e4m3x2_to_f16x2(code)) * s;
-  else return fmaf(f16lo(e2m1x2_to_f16x2(code >> shift & 15u)), s, 0.0f);
-}
-
 // NC: channels per lane (head_dim at most 32 NC); HEADS: query heads at once.
-template <int FMT, int NC, int HEADS>
+template <int FMT, int NC, int HEADS, bool WIDE>
 __global__ void __launch_bounds__(kThreads) attend_general_kernel(Args a, int dt) {
   extern __shared__ float s_part[];  // [warps][heads][dim + 2]
+  using Ch = Channels<FMT, NC, WIDE>;
+  constexpr int TOK = 32 / HEADS;
   const PagedCache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = c.dim;
   const int rb = c.row_bytes(), nb = c.row_scales(), stride = D + 2;
+  const int my_tok = lane / HEADS;  // this lane ends up with its logit of head lane % HEADS
   [[maybe_unused]] const int64_t n_rows = c.num_pages * c.heads * c.page;
-  Where at[NC];
-#pragma unroll
-  for (int i = 0; i < NC; ++i) at[i] = where<FMT>(min(lane + 32 * i, D - 1), c.block);
   walk<kWarps>(a, [&](const Span& s, const Target& t, int v0, int v1) {
     const int r0 = t.tile * HEADS, heads = min(HEADS, a.group - r0);
-    float q[HEADS][NC], o[HEADS][NC], m[HEADS], l[HEADS];
+    float q[HEADS][NC], o[HEADS][NC];
+    float m = kLowest, l = 0.0f;  // of head lane % HEADS; l over my_tok's tokens only
 #pragma unroll
-    for (int r = 0; r < HEADS; ++r) {
-      m[r] = kLowest;
-      l[r] = 0.0f;
+    for (int r = 0; r < HEADS; ++r)
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int ch = lane + 32 * i;
-        o[r][i] = q[r][i] = 0.0f;  // a lane past the last channel adds nothing
+        const int ch = Ch::channel(lane, i);
+        o[r][i] = q[r][i] = 0.0f;
         if (r < heads && ch < D)
           q[r][i] = a.scale_log2 *
                     load_q(a, dt, t.b * a.q_stride + ((int64_t)t.head * a.group + r0 + r) * D + ch);
       }
+    // TOK of a warp's tokens at a time, kWarps apart
+    for (int v = v0 + warp; v < v1; v += kWarps * TOK) {
+      // every lane looks up its own token's row; -1: none
+      int64_t row = -1;
+      if (v + my_tok * kWarps < v1) {
+        const Token tok = token_at(a, s, t.b, t.head, v + my_tok * kWarps);
+        if (tok.row >= 0 && live(a, s, tok.pos) && MXQ_IN_RANGE(kChkAttendIn, tok.row, n_rows))
+          row = tok.row;
+      }
+      float x[32];  // [token][head], this lane's channels' share
+      constexpr int AT_ONCE = NC <= 4 ? 4 : NC <= 8 ? 2 : 1;  // tokens whose bytes are under way
+      auto rows = [&](int y) { return __shfl_sync(0xffffffffu, row, y * HEADS); };
+#pragma unroll
+      for (int y0 = 0; y0 < TOK; y0 += AT_ONCE) {
+        Ch k[AT_ONCE];
+        int64_t at[AT_ONCE];
+#pragma unroll
+        for (int y = 0; y < AT_ONCE; ++y) {
+          at[y] = max((int64_t)0, rows(y0 + y));  // no token: some row, its weight is 0
+          if (v < v1) k[y].load(c.k_codes + at[y] * rb, c.k_scales + at[y] * nb, lane, D, c.block);
+        }
+#pragma unroll
+        for (int y = 0; y < AT_ONCE; ++y) {
+          float kv[NC];
+          k[y].values(kv, lane, D);
+#pragma unroll
+          for (int r = 0; r < HEADS; ++r) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) sum = fmaf(q[r][i], kv[i], sum);
+            x[(y0 + y) * HEADS + r] = sum;
+          }
+        }
+      }
+      // 32 sums over 32 lanes: halvings leave each lane the total of its own
+#pragma unroll
+      for (int half = 16; half > 0; half >>= 1) {
+        const bool up = lane & half;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+          const float give = up ? x[i] : x[i + half], keep = up ? x[i + half] : x[i];
+          x[i] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+        }
+      }
+      const float mine = row >= 0 ? x[0] : __int_as_float(0xFF800000);
+      float mn = fmaxf(m, mine);
+#pragma unroll
+      for (int w = HEADS; w < 32; w <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
+      const float keep = exp2f(m - mn), p = row >= 0 ? exp2f(mine - mn) : 0.0f;
+      m = mn;
+      l = fmaf(l, keep, p);
+      if (__any_sync(0xffffffffu, keep != 1.0f)) {
+#pragma unroll
+        for (int r = 0; r < HEADS; ++r) {
+          const float f = __shfl_sync(0xffffffffu, keep, r);
+#pragma unroll
+          for (int i = 0; i < NC; ++i) o[r][i] *= f;
+        }
+      }
+#pragma unroll
+      for (int y0 = 0; y0 < TOK; y0 += AT_ONCE) {
+        Ch val[AT_ONCE];
+        bool in[AT_ONCE];
+#pragma unroll
+        for (int y = 0; y < AT_ONCE; ++y) {
+          const int64_t at = rows(y0 + y);
+          in[y] = at >= 0;
+          const int64_t from = max((int64_t)0, at);
+          val[y].load(c.v_codes + from * rb, c.v_scales + from * nb, lane, D, c.block);
+        }
+#pragma unroll
+        for (int y = 0; y < AT_ONCE; ++y) {
+          float vv[NC];
+          val[y].values(vv, lane, D);
+#pragma unroll
+          for (int r = 0; r < HEADS; ++r) {
+            const float w = __shfl_sync(0xffffffffu, p, (y0 + y) * HEADS + r);
+            if (!in[y]) continue;  // the same for all lanes
+#pragma unroll
+            for (int i = 0; i < NC; ++i) o[r][i] = fmaf(w, vv[i], o[r][i]);
+          }
+        }
+      }
     }
-    // kTokens of a warp's tokens at a time, kWarps apart
-    for (int v = v0 + warp; v < v1; v += kWarps * kTokens) {
-      int64_t row[kTokens];
-      uint32_t kc[kTokens][NC], ks[kTokens][NC], vc[kTokens][NC], vs[kTokens][NC];
 #pragma unroll
-      for (int y = 0; y < kTokens; ++y) {
-        row[y] = -1;
-        const int vy = v + y * kWarps;
-        if (vy >= v1) continue;
-        const Token tok = token_at(a, s, t.b, t.head, vy);
-        if (tok.row < 0 || !live(a, s, tok.pos) || !MXQ_IN_RANGE(kChkAttendIn, tok.row, n_rows))
-          continue;
-        row[y] = tok.row;
-      }
-#pragma unroll
-      for (int y = 0; y < kTokens; ++y) {
-        if (row[y] < 0) continue;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          kc[y][i] = c.k_codes[row[y] * rb + at[i].byte];
-          ks[y][i] = c.k_scales[row[y] * nb + at[i].scale];
-          vc[y][i] = c.v_codes[row[y] * rb + at[i].byte];
-          vs[y][i] = c.v_scales[row[y] * nb + at[i].scale];
-        }
-      }
-      float x[kTokens][HEADS];
-#pragma unroll
-      for (int y = 0; y < kTokens; ++y) {
-#pragma unroll
-        for (int r = 0; r < HEADS; ++r) x[y][r] = 0.0f;
-        if (row[y] < 0) continue;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          const float k = cache_value<FMT>(kc[y][i], ks[y][i], at[i].shift);
-#pragma unroll
-          for (int r = 0; r < HEADS; ++r) x[y][r] = fmaf(q[r][i], k, x[y][r]);
-        }
-      }
-#pragma unroll
-      for (int y = 0; y < kTokens; ++y)
-#pragma unroll
-        for (int r = 0; r < HEADS; ++r)
-#pragma unroll
-          for (int w = 16; w > 0; w >>= 1) x[y][r] += __shfl_xor_sync(0xffffffffu, x[y][r], w);
-#pragma unroll
-      for (int r = 0; r < HEADS; ++r) {
-        float mn = m[r];
-#pragma unroll
-        for (int y = 0; y < kTokens; ++y)
-          if (row[y] >= 0) mn = fmaxf(mn, x[y][r]);
-        const float keep = exp2f(m[r] - mn);
-        m[r] = mn;
-        l[r] *= keep;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) o[r][i] *= keep;
-#pragma unroll
-        for (int y = 0; y < kTokens; ++y) {
-          x[y][r] = row[y] >= 0 ? exp2f(x[y][r] - mn) : 0.0f;
-          l[r] += x[y][r];
-        }
-      }
-#pragma unroll
-      for (int y = 0; y < kTokens; ++y) {
-        if (row[y] < 0) continue;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          const float val = cache_value<FMT>(vc[y][i], vs[y][i], at[i].shift);
-#pragma unroll
-          for (int r = 0; r < HEADS; ++r) o[r][i] = fmaf(x[y][r], val, o[r][i]);
-        }
-      }
-    }
+    for (int w = HEADS; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
     __syncthreads();  // the previous pair's sums have been read
 #pragma unroll
-    for (int r = 0; r < HEADS; ++r) {
-      float* mine = s_part + (warp * HEADS + r) * stride;
+    for (int r = 0; r < HEADS; ++r)
 #pragma unroll
       for (int i = 0; i < NC; ++i)
-        if (lane + 32 * i < D) mine[lane + 32 * i] = o[r][i];
-      if (lane == 0) mine[D] = m[r], mine[D + 1] = l[r];
+        if (Ch::channel(lane, i) < D)
+          s_part[(warp * HEADS + r) * stride + Ch::channel(lane, i)] = o[r][i];
+    if (lane < HEADS) {
+      s_part[(warp * HEADS + lane) * stride + D] = m;
+      s_part[(warp * HEADS + lane) * stride + D + 1] = l;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < heads * D; i += kThreads) {
@@ -182,6 +235,7 @@ join_kernel(Args a, int dt, int n_ctas, int per_head, bool by_pair) {
   const int pair1 = by_pair ? (int)blockIdx.x + 1 : a.hdr[2 * blockIdx.x + 1];
   if (pair1 == 0) return;
   __syncthreads();
+#pragma unroll 4
   for (int i = threadIdx.x; i < n_ctas; i += kThreads) {
     const int2 h = ((const int2*)a.hdr)[i];
     if (h.y == pair1) s_first = i;
@@ -209,24 +263,41 @@ join_kernel(Args a, int dt, int n_ctas, int per_head, bool by_pair) {
 #pragma unroll
     for (int k = 0; k < VEC; ++k) val[j][k] = 0.0f;
   if (have) {
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_l[place(i)]);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-#pragma unroll 4
-    for (int i = share; i < parts; i += per_head) {
-      const int64_t at = place(i);
-      const float l = a.part_l[at], f = l <= kLowest ? 0.0f : exp2f(l - top);
-      sum += f;
+    // the first parts' sums are under way with all parts' weights
+    constexpr int AHEAD = NC <= 2 ? 8 / NC : 2;
+    float x[AHEAD][NC][VEC];
+    auto load = [&](int i, float (*to)[VEC]) {
+      const float* from = a.part_o + place(i) * D;
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         const int ch = (lane + 32 * j) * VEC;
         if (ch >= D) continue;
-        float x[VEC];
-        if constexpr (VEC == 4) *(float4*)x = *(const float4*)(a.part_o + at * D + ch);
-        else x[0] = a.part_o[at * D + ch];
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) val[j][k] = fmaf(x[k], f, val[j][k]);
+        if constexpr (VEC == 4) *(float4*)to[j] = *(const float4*)(from + ch);
+        else to[j][0] = from[ch];
       }
+    };
+    auto add = [&](int i, float (*from)[VEC]) {
+      const float l = a.part_l[place(i)], f = l <= kLowest ? 0.0f : exp2f(l - top);
+      sum += f;
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+          if ((lane + 32 * j) * VEC < D) val[j][k] = fmaf(from[j][k], f, val[j][k]);
+    };
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_l[place(i)]);
+#pragma unroll
+    for (int y = 0; y < AHEAD; ++y)
+      if (share + y * per_head < parts) load(share + y * per_head, x[y]);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+    for (int i = share; i < parts; i += per_head * AHEAD) {
+#pragma unroll
+      for (int y = 0; y < AHEAD; ++y)
+        if (i + y * per_head < parts) add(i + y * per_head, x[y]);
+#pragma unroll
+      for (int y = 0; y < AHEAD; ++y)
+        if (i + (AHEAD + y) * per_head < parts) load(i + (AHEAD + y) * per_head, x[y]);
     }
   }
   float* mine = s_part + warp * (D + 1);
@@ -295,10 +366,24 @@ int launch_general(const Args& a, int dt, int grid, cudaStream_t st) {
     kernel<<<grid, kThreads, smem, st>>>(a, dt);
     return (int)MXQ_OK;
   };
-  if (a.c.dim <= 64) return go(attend_general_kernel<FMT, 2, general_heads(64)>);
-  if (a.c.dim <= 128) return go(attend_general_kernel<FMT, 4, general_heads(128)>);
-  if (a.c.dim <= 256) return go(attend_general_kernel<FMT, 8, general_heads(256)>);
-  return go(attend_general_kernel<FMT, 16, general_heads(512)>);
+  // a lane's channels at once: they lie in one scale block, and their bytes on
+  // their own size in every row
+  auto wide = [&](int nc) {
+    const int bytes = FMT == MXQ_FMT_FP8 ? nc : nc / 2;
+    return a.c.dim % nc == 0 && a.c.block % nc == 0 && a.c.row_bytes() % bytes == 0 &&
+           ((uintptr_t)a.c.k_codes | (uintptr_t)a.c.v_codes) % bytes == 0;
+  };
+  if (a.c.dim <= 64)
+    return wide(2) ? go(attend_general_kernel<FMT, 2, general_heads(64), true>)
+                   : go(attend_general_kernel<FMT, 2, general_heads(64), false>);
+  if (a.c.dim <= 128)
+    return wide(4) ? go(attend_general_kernel<FMT, 4, general_heads(128), true>)
+                   : go(attend_general_kernel<FMT, 4, general_heads(128), false>);
+  if (a.c.dim <= 256)
+    return wide(8) ? go(attend_general_kernel<FMT, 8, general_heads(256), true>)
+                   : go(attend_general_kernel<FMT, 8, general_heads(256), false>);
+  return wide(16) ? go(attend_general_kernel<FMT, 16, general_heads(512), true>)
+                  : go(attend_general_kernel<FMT, 16, general_heads(512), false>);
 }
 
 constexpr int kCtasPerSm = 4;  // at most, of any of the kernels
@@ -374,7 +459,8 @@ int launch_attend_cache_paged(const void* q, int dt, int64_t q_heads, int64_t q_
   else if (c.fmt == MXQ_FMT_FP8) rc = launch_general<MXQ_FMT_FP8>(a, dt, grid, st);
   else if (c.fmt == MXQ_FMT_MXFP4) rc = launch_general<MXQ_FMT_MXFP4>(a, dt, grid, st);
   else rc = launch_general<MXQ_FMT_NVFP4>(a, dt, grid, st);
-  if (rc != MXQ_OK) return rc;
+  // a span of one unit is never split
+  if (rc != MXQ_OK || span <= kUnit) return rc == MXQ_OK && cudaGetLastError() != cudaSuccess ? (int)MXQ_ERR_CUDA : rc;
   return launch_join(a, dt, grid, st);
 }
 

@@ -136,6 +136,34 @@ __device__ __forceinline__ Part part_of(const Args& a) {
   auto length = [&](int64_t b) {
     return b < a.c.n_seqs ? pairs * (span_of(a, b).units + kPairCost) : 0;
   };
+  auto cut = [&](int64_t total) {
+    // no part is shorter than two units: the parts of a pair lie in blocks that
+    // follow one another, and are worth their join
+    const int64_t most = total / 2;
+    const uint32_t n = most < gridDim.x ? (uint32_t)most : gridDim.x;
+    const int64_t each = total < ((int64_t)1 << 32) ? (uint32_t)total / n : total / n;
+    const uint32_t rest = (uint32_t)(total - each * n);  // below n, n below 2^16
+    auto start = [&](uint32_t i) { return min(total, each * i + rest * i / n); };
+    Part p;
+    p.begin = start(blockIdx.x);
+    p.end = start(blockIdx.x + 1);
+    return p;
+  };
+  if (a.c.n_seqs <= 32) {  // each warp by itself
+    const int64_t mine = length(lane);
+    int64_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    Part p = cut(__shfl_sync(0xffffffffu, sum, 31));
+    const unsigned in = __ballot_sync(0xffffffffu, sum - mine <= p.begin && p.begin < sum);
+    const int who = in ? __ffs((int)in) - 1 : 0;  // none: an empty part at the end
+    p.b = who;
+    p.b_begin = __shfl_sync(0xffffffffu, sum - mine, who);
+    return p;
+  }
   const int64_t one = length(threadIdx.x);  // all there is for up to kThreads sequences
   int64_t total = one;
   for (int64_t b = threadIdx.x + kThreads; b < a.c.n_seqs; b += kThreads) total += length(b);
@@ -147,16 +175,7 @@ __device__ __forceinline__ Part part_of(const Args& a) {
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) total += s_sum[i];
   __syncthreads();
-  Part p;
-  // no part is shorter than two units: the parts of a pair lie in blocks that
-  // follow one another, and are worth their join
-  const int64_t most = total / 2;
-  const uint32_t n = most < gridDim.x ? (uint32_t)most : gridDim.x;
-  const int64_t each = total < ((int64_t)1 << 32) ? (uint32_t)total / n : total / n;
-  const uint32_t rest = (uint32_t)(total - each * n);  // below n, n below 2^16
-  auto start = [&](uint32_t i) { return min(total, each * i + rest * i / n); };
-  p.begin = start(blockIdx.x);
-  p.end = start(blockIdx.x + 1);
+  Part p = cut(total);
   int64_t before = 0;
   for (int64_t b0 = 0; b0 < a.c.n_seqs; b0 += kThreads) {
     const int64_t b = b0 + threadIdx.x;
