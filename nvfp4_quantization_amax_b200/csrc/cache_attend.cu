@@ -2,13 +2,13 @@
 // kernel for any head size, block size, page size and alignment, and the join
 // of the parts of pairs that were split (see cache_attend.cuh).
 //
-// General kernel: a warp takes 4 tokens x 8 heads (8 x 4, 16 x 2 for wide heads)
-// at a time, lanes hold channels.  The 32 partial dot products are summed over
-// the lanes by halvings, 31 shuffles that leave each lane one (token, head): it
-// takes that exponential, and its weight is handed round for the values.  The
-// running maximum m, sum l and weighted values o of the softmax are f32:
-//   m' = max(m, s), l = l 2^(m-m') + sum 2^(s-m'), o = o 2^(m-m') + sum 2^(s-m') v.
-// The warps' sums are joined in shared memory in a fixed order.
+// General kernel: the arithmetic of the tensor-core kernel (cache_attend_tc.cuh)
+// where rows do not lie in whole tiles of it.  A warp takes 16 tokens at a time,
+// each row read by the whole warp (as wide as its alignment allows) and decoded
+// to f16 in shared memory, padded with zeros to 16 channels: K's values times
+// 2^-(the row's largest scale exponent), which returns in f32 on the sums; V's
+// likewise, its exponent in the token's weight (nvfp4: the values themselves).
+// Then S = K Q^T and O^T = V^T P^T by mma.m16n8k16 from ldmatrix.
 #include "cache_attend.cuh"
 #include "sm100_primitives.cuh"
 
@@ -18,10 +18,6 @@ namespace attend {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// Query heads a warp carries, by channels per lane (their queries and sums stay
-// in registers), and tokens it has under way: a (token, head) for every lane.
-constexpr int general_heads(int dim) { return dim <= 128 ? 8 : dim <= 256 ? 4 : 2; }
-
 // NC channels of a row of codes, as the lane's bytes lie: NC (fp8) or NC / 2
 // bytes at once where the sizes allow it (WIDE), else one by one.
 template <int FMT, int NC, bool WIDE>
@@ -30,190 +26,321 @@ struct Channels {
   static constexpr int CODES = WIDE ? (BYTES + 3) / 4 : NC, SCALES = WIDE ? 1 : NC;
   uint32_t code[CODES], scale[SCALES];
 
-  static __device__ __forceinline__ int channel(int lane, int i) {
-    return WIDE ? lane * NC + i : lane + 32 * i;
-  }
+  // at: the lane's scale in a row (WIDE)
   __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int lane, int D,
-                                       int B) {
+                                       int B, int at) {
     if constexpr (WIDE) {
       if (lane * NC >= D) return;
       const uint8_t* p = codes + lane * BYTES;
-      if constexpr (BYTES == 1) code[0] = *p;
-      else if constexpr (BYTES == 2) code[0] = *(const uint16_t*)p;
-      else if constexpr (BYTES == 4) code[0] = *(const uint32_t*)p;
-      else if constexpr (BYTES == 8) *(uint2*)code = *(const uint2*)p;
-      else *(uint4*)code = *(const uint4*)p;
-      scale[0] = scales[lane * NC / B];
+      if constexpr (BYTES == 1) code[0] = __ldg(p);
+      else if constexpr (BYTES == 2) code[0] = __ldg((const uint16_t*)p);
+      else if constexpr (BYTES == 4) code[0] = __ldg((const uint32_t*)p);
+      else if constexpr (BYTES == 8) *(uint2*)code = __ldg((const uint2*)p);
+      else *(uint4*)code = __ldg((const uint4*)p);
+      scale[0] = __ldg(scales + at);
     } else {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int ch = min(lane + 32 * i, D - 1);
-        code[i] = codes[FMT == MXQ_FMT_FP8 ? ch : ch / 2] >> (FMT == MXQ_FMT_FP8 ? 0 : (ch & 1) * 4);
-        scale[i] = scales[ch / B];
+        code[i] = __ldg(codes + (FMT == MXQ_FMT_FP8 ? ch : ch / 2)) >>
+                  (FMT == MXQ_FMT_FP8 ? 0 : (ch & 1) * 4);
+        scale[i] = __ldg(scales + ch / B);
       }
     }
   }
-  // The values, exact in f32; 0 for a lane past the last channel.
-  __device__ __forceinline__ void values(float* v, int lane, int D) const {
+  // The largest scale byte (E8M0), over all lanes.
+  __device__ __forceinline__ int top_scale(int lane, int D) const {
+    uint32_t top = 0;
     if constexpr (WIDE) {
-      const bool in = lane * NC < D;
-      const float s = in ? scale_value<FMT>(scale[0]) : 0.0f;
+      top = lane * NC < D ? scale[0] : 0;
+    } else {
 #pragma unroll
-      for (int i = 0; i < NC; i += 2) {
-        const int bit = (FMT == MXQ_FMT_FP8 ? 8 : 4) * i;  // where the pair begins
-        const uint32_t w = in ? code[bit / 32] >> (bit % 32) : 0u;
-        const uint32_t h = FMT == MXQ_FMT_FP8 ? e4m3x2_to_f16x2(w & 0xFFFFu) : e2m1x2_to_f16x2(w & 0xFFu);
-        v[i] = f16lo(h) * s;
-        v[i + 1] = f16hi(h) * s;
+      for (int i = 0; i < NC; ++i) top = max(top, scale[i]);
+    }
+    return (int)__reduce_max_sync(0xffffffffu, top);
+  }
+  // Code times 2^(OFF + scale exponent - top's) (E8M0), or times the scale
+  // (nvfp4), in f16 at their channels of a row of `pad` channels; 0 behind the
+  // last channel.  Factors below 2^-14 count as 0.
+  template <int OFF>
+  __device__ __forceinline__ void put(__half* row, int top, int lane, int D, int pad) const {
+    auto factor = [&](uint32_t byte) -> uint32_t {  // one f16
+      if constexpr (FMT == MXQ_FMT_NVFP4) return e4m3x2_to_f16x2(byte) & 0xFFFFu;
+      else return (uint32_t)max(0, OFF + 15 + (int)byte - top) << 10;
+    };
+    if constexpr (WIDE) {
+      if (lane * NC >= pad) return;
+      const bool in = lane * NC < D;
+      const uint32_t s = in ? factor(scale[0]) * 0x00010001u : 0u;
+      uint32_t h[NC / 2 < 2 ? 2 : NC / 2];
+      if constexpr (NC == 2) {
+        const uint32_t w = in ? code[0] : 0u;
+        h[0] = FMT == MXQ_FMT_FP8 ? e4m3x2_to_f16x2(w) : e2m1x2_to_f16x2(w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < CODES; ++i) {
+          uint32_t y[4];
+          decode_word<FMT>(in ? code[i] : 0u, y);
+#pragma unroll
+          for (int j = 0; j < Codes<FMT>::kPairs; ++j)
+            if (i * Codes<FMT>::kPairs + j < NC / 2) h[i * Codes<FMT>::kPairs + j] = y[j];
+        }
       }
+#pragma unroll
+      for (int i = 0; i < NC / 2; ++i) h[i] = hmul2(h[i], s);
+      __half* to = row + lane * NC;
+      if constexpr (NC == 2) *(uint32_t*)to = h[0];
+      else if constexpr (NC == 4) *(uint2*)to = make_uint2(h[0], h[1]);
+      else
+#pragma unroll
+        for (int i = 0; i < NC / 2; i += 4)
+          *(uint4*)(to + 2 * i) = make_uint4(h[i], h[i + 1], h[i + 2], h[i + 3]);
     } else {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const float s = scale_value<FMT>(scale[i]);
+        const int ch = lane + 32 * i;
+        if (ch >= pad) continue;
         const uint32_t h = FMT == MXQ_FMT_FP8 ? e4m3x2_to_f16x2(code[i] & 0xFFu)
                                               : e2m1x2_to_f16x2(code[i] & 15u);
-        v[i] = lane + 32 * i < D ? f16lo(h) * s : 0.0f;
+        row[ch] = __ushort_as_half(
+            (unsigned short)(ch < D ? hmul2(h & 0xFFFFu, factor(scale[i])) & 0xFFFFu : 0u));
       }
     }
   }
 };
 
-// NC: channels per lane (head_dim at most 32 NC); HEADS: query heads at once.
-template <int FMT, int NC, int HEADS, bool WIDE>
-__global__ void __launch_bounds__(kThreads) attend_general_kernel(Args a, int dt) {
-  extern __shared__ float s_part[];  // [warps][heads][dim + 2]
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// NC: channels per lane (head_dim at most 32 NC).  Shared memory: Q [2 terms][8
+// heads][pad + 8] f16, then per warp 16 rows of K or V, [16][pad + 8] f16 (8
+// more than the padded channels: the eight rows of an ldmatrix lie in different
+// banks), or at the end of a pair the warps' sums [8 heads][dim] f32.
+template <int FMT, int NC, bool WIDE>
+__global__ void __launch_bounds__(kTcThreads, NC <= 4 ? 4 : NC <= 8 ? 2 : 1)
+attend_general_kernel(Args a, int dt, int pad) {
+  extern __shared__ __align__(128) uint8_t s_all[];
+  __shared__ float s_qf[8], s_m[kTcWarps][8], s_e[kTcWarps][8], s_l[kTcWarps][8];
   using Ch = Channels<FMT, NC, WIDE>;
-  constexpr int TOK = 32 / HEADS;
+  constexpr int MT = NC * 2;          // tiles of 16 channels
+  constexpr int AT_ONCE = 4;  // rows whose bytes are under way (8 or 16: 15 to 60 % slower)
+  constexpr int OFF = FMT == MXQ_FMT_NVFP4 ? 0 : FMT == MXQ_FMT_FP8 ? 7 : 12;
   const PagedCache& c = a.c;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = c.dim;
-  const int rb = c.row_bytes(), nb = c.row_scales(), stride = D + 2;
-  const int my_tok = lane / HEADS;  // this lane ends up with its logit of head lane % HEADS
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = c.dim, stride = pad + 8;
+  const int g = lane >> 2, t4 = lane & 3, rb = c.row_bytes(), nb = c.row_scales();
+  const int my_scale = WIDE ? min(lane * NC, D - 1) / c.block : 0;
+  const bool two = dt != kBF16;  // terms of queries and weights
   [[maybe_unused]] const int64_t n_rows = c.num_pages * c.heads * c.page;
-  walk<kWarps>(a, [&](const Span& s, const Target& t, int v0, int v1) {
-    const int r0 = t.tile * HEADS, heads = min(HEADS, a.group - r0);
-    float q[HEADS][NC], o[HEADS][NC];
-    float m = kLowest, l = 0.0f;  // of head lane % HEADS; l over my_tok's tokens only
-#pragma unroll
-    for (int r = 0; r < HEADS; ++r)
+  __half* const s_q = (__half*)s_all;
+  __half* const tile = s_q + 16 * stride + warp * 16 * stride;
+  const uint32_t q_at = sm100::smem_addr(s_q) +
+                        ((lane >> 4) * 8 * stride + (lane & 7) * stride + (lane >> 3 & 1) * 8) * 2;
+  const uint32_t k_at = sm100::smem_addr(tile) + ((lane & 15) * stride + (lane >> 4) * 8) * 2;
+  const uint32_t v_at = sm100::smem_addr(tile) +
+                        (((lane & 7) + (lane >> 4) * 8) * stride + (lane >> 3 & 1) * 8) * 2;
+  const float none = __int_as_float(0xFF800000);
+  walk<kTcWarps>(a, [&](const Span& s, const Target& tg, int v0, int v1) {
+    const int r0 = tg.tile * 8, heads = min(8, a.group - r0);
+    // Q, scaled by a power of two to [2^13, 2^14) at its largest
+    for (int r = warp; r < 8; r += kTcWarps) {
+      float x[NC], top = 0.0f;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int ch = Ch::channel(lane, i);
-        o[r][i] = q[r][i] = 0.0f;
-        if (r < heads && ch < D)
-          q[r][i] = a.scale_log2 *
-                    load_q(a, dt, t.b * a.q_stride + ((int64_t)t.head * a.group + r0 + r) * D + ch);
+        const int ch = lane + 32 * i;
+        x[i] = r < heads && ch < D
+                   ? load_q(a, dt, tg.b * a.q_stride + ((int64_t)tg.head * a.group + r0 + r) * D + ch)
+                   : 0.0f;
+        top = fmaxf(top, fabsf(x[i]));
       }
-    // TOK of a warp's tokens at a time, kWarps apart
-    for (int v = v0 + warp; v < v1; v += kWarps * TOK) {
-      // every lane looks up its own token's row; -1: none
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+      const int e = top > 0.0f ? floor_log2_f32bits(__float_as_uint(top)) - 13 : 0;
+      const float f1 = exp2i(-(e / 2)), f2 = exp2i(-(e - e / 2));
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int ch = lane + 32 * i;
+        if (ch >= pad) continue;
+        const float y = x[i] * f1 * f2;
+        const __half h = __float2half_rn(y);
+        s_q[r * stride + ch] = h;
+        s_q[(8 + r) * stride + ch] = __float2half_rn(y - __half2float(h));
+      }
+      if (lane == 0) s_qf[r] = a.scale_log2 * exp2f((float)e);
+    }
+    __syncthreads();
+    const float qf[2] = {s_qf[2 * t4], s_qf[2 * t4 + 1]};
+    float o[MT][4], m[2] = {0.0f, 0.0f}, E[2] = {kLowest, kLowest}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+    bool have = false;
+
+    for (int v = v0 + warp * kTile; v < v1; v += kTcWarps * kTile) {
+      // lanes 0 .. 15 look up a token's row each; -1: none
       int64_t row = -1;
-      if (v + my_tok * kWarps < v1) {
-        const Token tok = token_at(a, s, t.b, t.head, v + my_tok * kWarps);
+      if (lane < kTile && v + lane < v1) {
+        const Token tok = token_at(a, s, tg.b, tg.head, v + lane);
         if (tok.row >= 0 && live(a, s, tok.pos) && MXQ_IN_RANGE(kChkAttendIn, tok.row, n_rows))
           row = tok.row;
       }
-      float x[32];  // [token][head], this lane's channels' share
-      constexpr int AT_ONCE = NC <= 4 ? 4 : NC <= 8 ? 2 : 1;  // tokens whose bytes are under way
-      auto rows = [&](int y) { return __shfl_sync(0xffffffffu, row, y * HEADS); };
+      const unsigned live_rows = __ballot_sync(0xffffffffu, row >= 0);
+      if (live_rows == 0) continue;
+      // K or V into the tile; lane y of the result holds the top scale byte of token y
+      auto fetch = [&](const uint8_t* codes, const uint8_t* scales) {
+        int tops = 127;
+        __syncwarp();  // the tile's last reads are done
 #pragma unroll
-      for (int y0 = 0; y0 < TOK; y0 += AT_ONCE) {
-        Ch k[AT_ONCE];
-        int64_t at[AT_ONCE];
+        for (int y0 = 0; y0 < kTile; y0 += AT_ONCE) {
+          Ch x[AT_ONCE];
 #pragma unroll
-        for (int y = 0; y < AT_ONCE; ++y) {
-          at[y] = max((int64_t)0, rows(y0 + y));  // no token: some row, its weight is 0
-          if (v < v1) k[y].load(c.k_codes + at[y] * rb, c.k_scales + at[y] * nb, lane, D, c.block);
-        }
+          for (int y = 0; y < AT_ONCE; ++y) {
+            const int64_t at = __shfl_sync(0xffffffffu, row, y0 + y);
+            if (at >= 0) x[y].load(codes + at * rb, scales + at * nb, lane, D, c.block, my_scale);
+          }
 #pragma unroll
-        for (int y = 0; y < AT_ONCE; ++y) {
-          float kv[NC];
-          k[y].values(kv, lane, D);
-#pragma unroll
-          for (int r = 0; r < HEADS; ++r) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NC; ++i) sum = fmaf(q[r][i], kv[i], sum);
-            x[(y0 + y) * HEADS + r] = sum;
+          for (int y = 0; y < AT_ONCE; ++y) {
+            __half* to = tile + (y0 + y) * stride;
+            if (live_rows >> (y0 + y) & 1) {
+              const int top = FMT == MXQ_FMT_NVFP4 ? 127 : x[y].top_scale(lane, D);
+              if (lane == y0 + y) tops = top;
+              x[y].template put<OFF>(to, top, lane, D, pad);
+            } else {
+              for (int ch = lane * 2; ch < pad; ch += 64) *(uint32_t*)(to + ch) = 0u;
+            }
           }
         }
+        __syncwarp();
+        return tops;
+      };
+      // ---- S = K Q^T, rows tokens g, g + 8, columns heads 2 t, 2 t + 1
+      const int k_tops = fetch(c.k_codes, c.k_scales);
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < MT; ++k) {
+        if (k * 16 >= pad) continue;
+        uint32_t f[4], q[4];
+        ldmatrix4(f, k_at + k * 32);
+        ldmatrix4(q, q_at + k * 32);
+        mma16816(d, f, q[0], q[1]);
+        if (two) mma16816(d, f, q[2], q[3]);
       }
-      // 32 sums over 32 lanes: halvings leave each lane the total of its own
+      const int v_tops = fetch(c.v_codes, c.v_scales);
+      // of tokens g and g + 8: K's factor, V's exponent
+      float kf[2], rf[2];
 #pragma unroll
-      for (int half = 16; half > 0; half >>= 1) {
-        const bool up = lane & half;
-#pragma unroll
-        for (int i = 0; i < half; ++i) {
-          const float give = up ? x[i] : x[i + half], keep = up ? x[i + half] : x[i];
-          x[i] = keep + __shfl_xor_sync(0xffffffffu, give, half);
-        }
+      for (int h = 0; h < 2; ++h) {
+        kf[h] = exp2i(__shfl_sync(0xffffffffu, k_tops, g + 8 * h) - 127 - OFF);
+        rf[h] = (float)(__shfl_sync(0xffffffffu, v_tops, g + 8 * h) - 127);
       }
-      const float mine = row >= 0 ? x[0] : __int_as_float(0xFF800000);
-      float mn = fmaxf(m, mine);
+      // ---- d = s - m, and the reference where one exceeds it by 2^4
+      float over = -1.0f;
 #pragma unroll
-      for (int w = HEADS; w < 32; w <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
-      const float keep = exp2f(m - mn), p = row >= 0 ? exp2f(mine - mn) : 0.0f;
-      m = mn;
-      l = fmaf(l, keep, p);
-      if (__any_sync(0xffffffffu, keep != 1.0f)) {
-#pragma unroll
-        for (int r = 0; r < HEADS; ++r) {
-          const float f = __shfl_sync(0xffffffffu, keep, r);
-#pragma unroll
-          for (int i = 0; i < NC; ++i) o[r][i] *= f;
-        }
+      for (int j = 0; j < 4; ++j) {
+        d[j] = d[j] * kf[j >> 1] * qf[j & 1] - m[j & 1];
+        if (!(live_rows >> (j < 2 ? g : g + 8) & 1)) d[j] = none;
+        over = fmaxf(over, d[j]);
       }
+      if (__any_sync(0xffffffffu, over > kLag || !have)) {
 #pragma unroll
-      for (int y0 = 0; y0 < TOK; y0 += AT_ONCE) {
-        Ch val[AT_ONCE];
-        bool in[AT_ONCE];
+        for (int j = 0; j < 2; ++j) {
+          float up = fmaxf(have ? 0.0f : none, fmaxf(d[j], d[j + 2]));
 #pragma unroll
-        for (int y = 0; y < AT_ONCE; ++y) {
-          const int64_t at = rows(y0 + y);
-          in[y] = at >= 0;
-          const int64_t from = max((int64_t)0, at);
-          val[y].load(c.v_codes + from * rb, c.v_scales + from * nb, lane, D, c.block);
+          for (int w = 4; w < 32; w <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, w));
+          m[j] += up;
+          if (have) l[j] *= ex2(-up);
+          d[j] -= up;
+          d[j + 2] -= up;
         }
+        have = true;
+      }
+      // ---- weights times 2^(11 + r), x = s + r - E + 11
+      float x[4];
+      auto relate = [&]() {
 #pragma unroll
-        for (int y = 0; y < AT_ONCE; ++y) {
-          float vv[NC];
-          val[y].values(vv, lane, D);
+        for (int j = 0; j < 4; ++j) x[j] = d[j] + (rf[j >> 1] + ((m[j & 1] - E[j & 1]) + kWeightExp));
+        return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      };
+      if (__any_sync(0xffffffffu, relate() > kWeightExp + kLag)) {
 #pragma unroll
-          for (int r = 0; r < HEADS; ++r) {
-            const float w = __shfl_sync(0xffffffffu, p, (y0 + y) * HEADS + r);
-            if (!in[y]) continue;  // the same for all lanes
+        for (int j = 0; j < 2; ++j) {
+          float e = fmaxf(kLowest, fmaxf(d[j] + rf[0], d[j + 2] + rf[1]));
 #pragma unroll
-            for (int i = 0; i < NC; ++i) o[r][i] = fmaf(w, vv[i], o[r][i]);
-          }
+          for (int w = 4; w < 32; w <<= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, w));
+          const float En = fmaxf(E[j], m[j] + e), fo = ex2(E[j] - En);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) o[i][j] *= fo, o[i][j + 2] *= fo;
+          E[j] = En;
         }
+        relate();
+      }
+      uint32_t p[2][2];
+      {
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          y[j] = ex2(x[j]);
+          l[j & 1] += ex2(d[j]);
+        }
+        const uint32_t h0 = half2_of(y[0], y[1]), h1 = half2_of(y[2], y[3]);
+        p[0][0] = sm100::movmatrix_trans(h0);
+        p[0][1] = sm100::movmatrix_trans(h1);
+        p[1][0] = sm100::movmatrix_trans(half2_of(y[0] - f16lo(h0), y[1] - f16hi(h0)));
+        p[1][1] = sm100::movmatrix_trans(half2_of(y[2] - f16lo(h1), y[3] - f16hi(h1)));
+      }
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        if (i * 16 >= pad) continue;
+        uint32_t f[4];
+        ldmatrix4_trans(f, v_at + i * 32);
+        mma16816(o[i], f, p[0][0], p[0][1]);
+        if (two) mma16816(o[i], f, p[1][0], p[1][1]);
       }
     }
+
+    // ---- join the warps: sums [warp][head][dim]
+    __syncthreads();
+    float* const sums = (float*)(s_all + 16 * stride * 2);
 #pragma unroll
-    for (int w = HEADS; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-    __syncthreads();  // the previous pair's sums have been read
+    for (int j = 0; j < 2; ++j) {
+      float* to = sums + (warp * 8 + 2 * t4 + j) * D;
 #pragma unroll
-    for (int r = 0; r < HEADS; ++r)
+      for (int i = 0; i < MT; ++i) {
+        if (i * 16 + g < D) to[i * 16 + g] = o[i][j];
+        if (i * 16 + g + 8 < D) to[i * 16 + g + 8] = o[i][j + 2];
+      }
+      float lt = l[j];
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
-        if (Ch::channel(lane, i) < D)
-          s_part[(warp * HEADS + r) * stride + Ch::channel(lane, i)] = o[r][i];
-    if (lane < HEADS) {
-      s_part[(warp * HEADS + lane) * stride + D] = m;
-      s_part[(warp * HEADS + lane) * stride + D + 1] = l;
+      for (int w = 4; w < 32; w <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, w);
+      if (g == 0) {
+        s_m[warp][2 * t4 + j] = m[j];
+        s_e[warp][2 * t4 + j] = E[j];
+        s_l[warp][2 * t4 + j] = lt;
+      }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < heads * D; i += kThreads) {
+    for (int i = threadIdx.x; i < heads * D; i += kTcThreads) {
       const int r = i / D, ch = i - r * D;
-      float top = kLowest, sum = 0.0f, val = 0.0f;
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_part[(w * HEADS + r) * stride + D]);
-      for (int w = 0; w < kWarps; ++w) {
-        const float* p = s_part + (w * HEADS + r) * stride;
-        const float f = exp2f(p[D] - top);
-        sum = fmaf(p[D + 1], f, sum);
-        val = fmaf(p[ch], f, val);
+      float top = kLowest, ref = kLowest, sum = 0.0f, val = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kTcWarps; ++w)
+        if (s_l[w][r] > 0.0f) top = fmaxf(top, s_m[w][r]), ref = fmaxf(ref, s_e[w][r]);
+#pragma unroll
+      for (int w = 0; w < kTcWarps; ++w) {
+        if (!(s_l[w][r] > 0.0f)) continue;
+        sum = fmaf(s_l[w][r], exp2f(s_m[w][r] - top), sum);
+        val = fmaf(sums[(w * 8 + r) * D + ch], exp2f(s_e[w][r] - ref), val);
       }
-      put(a, dt, t, r, ch, sum > 0.0f ? val / sum : 0.0f);
-      if (ch == 0) put_weight(a, t, r, sum > 0.0f ? top + log2f(sum) : kLowest);
+      const float back = (ref - top) - kWeightExp - (float)OFF, half = truncf(back * 0.5f);
+      put(a, dt, tg, r, ch, sum > 0.0f ? val / sum * exp2f(half) * exp2f(back - half) : 0.0f);
+      if (ch == 0) put_weight(a, tg, r, sum > 0.0f ? top + log2f(sum) : kLowest);
     }
+    __syncthreads();  // the buffers are the next pair's
   });
 }
 
@@ -359,11 +486,13 @@ int launch_join(const Args& a, int dt, int grid, cudaStream_t st) {
 
 template <int FMT>
 int launch_general(const Args& a, int dt, int grid, cudaStream_t st) {
-  const int smem = kWarps * a.tile_heads * (a.c.dim + 2) * 4;
+  const int pad = (a.c.dim + 15) / 16 * 16;
+  const int tiles = kTcWarps * 16 * (pad + 8) * 2, sums = kTcWarps * 8 * a.c.dim * 4;
+  const int smem = 16 * (pad + 8) * 2 + (tiles > sums ? tiles : sums);
   auto go = [&](auto kernel) {
     if (smem > 48 * 1024 && allow_dynamic_smem((const void*)kernel, smem) != cudaSuccess)
       return (int)MXQ_ERR_CUDA;
-    kernel<<<grid, kThreads, smem, st>>>(a, dt);
+    kernel<<<grid, kTcThreads, smem, st>>>(a, dt, pad);
     return (int)MXQ_OK;
   };
   // a lane's channels at once: they lie in one scale block, and their bytes on
@@ -374,16 +503,12 @@ int launch_general(const Args& a, int dt, int grid, cudaStream_t st) {
            ((uintptr_t)a.c.k_codes | (uintptr_t)a.c.v_codes) % bytes == 0;
   };
   if (a.c.dim <= 64)
-    return wide(2) ? go(attend_general_kernel<FMT, 2, general_heads(64), true>)
-                   : go(attend_general_kernel<FMT, 2, general_heads(64), false>);
+    return wide(2) ? go(attend_general_kernel<FMT, 2, true>) : go(attend_general_kernel<FMT, 2, false>);
   if (a.c.dim <= 128)
-    return wide(4) ? go(attend_general_kernel<FMT, 4, general_heads(128), true>)
-                   : go(attend_general_kernel<FMT, 4, general_heads(128), false>);
+    return wide(4) ? go(attend_general_kernel<FMT, 4, true>) : go(attend_general_kernel<FMT, 4, false>);
   if (a.c.dim <= 256)
-    return wide(8) ? go(attend_general_kernel<FMT, 8, general_heads(256), true>)
-                   : go(attend_general_kernel<FMT, 8, general_heads(256), false>);
-  return wide(16) ? go(attend_general_kernel<FMT, 16, general_heads(512), true>)
-                  : go(attend_general_kernel<FMT, 16, general_heads(512), false>);
+    return wide(8) ? go(attend_general_kernel<FMT, 8, true>) : go(attend_general_kernel<FMT, 8, false>);
+  return wide(16) ? go(attend_general_kernel<FMT, 16, true>) : go(attend_general_kernel<FMT, 16, false>);
 }
 
 constexpr int kCtasPerSm = 4;  // at most, of any of the kernels
@@ -448,8 +573,9 @@ int launch_attend_cache_paged(const void* q, int dt, int64_t q_heads, int64_t q_
   // its registers (one f16 term, up to 128 channels): K and V are read once
   // for all of a tile
   const bool tc = tc_fits(a);
-  a.tile_heads = !tc ? general_heads(c.dim) : a.group > 8 && dt == kBF16 && c.dim <= 128 ? 16 : 8;
+  a.tile_heads = tc && a.group > 8 && dt == kBF16 && c.dim <= 128 ? 16 : 8;
   a.head_tiles = (a.group + a.tile_heads - 1) / a.tile_heads;
+  a.least = tc ? 2 : 1;  // a unit of the general kernel takes several times as long
   // no more blocks than units that there can be
   const int64_t span = selected ? top * c.page : (a.window > 0 ? a.window + 16 : lim);
   const int64_t units = c.n_seqs * c.heads * a.head_tiles * ((span + kUnit - 1) / kUnit);

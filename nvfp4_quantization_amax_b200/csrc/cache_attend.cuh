@@ -33,6 +33,80 @@ constexpr int kPairCost = 2;
 constexpr float kLowest = -3.0e38f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+constexpr int kTcThreads = 128;
+constexpr int kTcWarps = kTcThreads / 32;
+constexpr int kTile = 16;           // tokens
+constexpr float kLag = 4.0f;        // how far a logit may exceed the reference
+constexpr float kWeightExp = 11.0f; // weights are held times 2^11: at most 2^15
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same with a zero addend.
+__device__ __forceinline__ void mma16816_first(float* c, const uint32_t* a, uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// 16 bytes, or zeros where `bytes` is 0 (nothing is read then).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// BYTES (a power of two) bytes of shared memory, little-endian in words.
+template <int BYTES>
+__device__ __forceinline__ void lds_bytes(uint32_t* r, uint32_t a) {
+  if constexpr (BYTES <= 2) {
+    uint16_t h;
+    if constexpr (BYTES == 1) asm volatile("ld.shared.u8 %0, [%1];" : "=h"(h) : "r"(a) : "memory");
+    else asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(a) : "memory");
+    r[0] = h;
+  } else if constexpr (BYTES == 4) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(a) : "memory");
+  } else if constexpr (BYTES == 8) {
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
+  } else {
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+  }
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) { return pack2<kF16>(lo, hi); }
+
 struct Args {
   const void* q;
   int64_t q_stride;
@@ -40,6 +114,7 @@ struct Args {
   const int32_t* selected;
   int top, window;  // window 0: none
   int q_heads, group, head_tiles, tile_heads;
+  int least;  // units of a block's part, at least
   float scale_log2;  // softmax scale times log2(e)
   void* out;
   float* lse;
@@ -137,9 +212,9 @@ __device__ __forceinline__ Part part_of(const Args& a) {
     return b < a.c.n_seqs ? pairs * (span_of(a, b).units + kPairCost) : 0;
   };
   auto cut = [&](int64_t total) {
-    // no part is shorter than two units: the parts of a pair lie in blocks that
-    // follow one another, and are worth their join
-    const int64_t most = total / 2;
+    // no part is shorter than least units: the parts of a pair lie in blocks
+    // that follow one another, and are worth their join
+    const int64_t most = total / a.least;
     const uint32_t n = most < gridDim.x ? (uint32_t)most : gridDim.x;
     const int64_t each = total < ((int64_t)1 << 32) ? (uint32_t)total / n : total / n;
     const uint32_t rest = (uint32_t)(total - each * n);  // below n, n below 2^16
