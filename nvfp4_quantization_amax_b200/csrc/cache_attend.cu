@@ -184,7 +184,7 @@ attend_general_kernel(Args a, int dt, int pad) {
       // lanes 0 .. 15 look up a token's row each; -1: none
       int64_t row = -1;
       if (lane < kTile && v + lane < v1) {
-        const Token tok = token_at(a, s, tg.b, tg.head, v + lane);
+        const Token tok = token_at(a, s, tg.b, tg.head, v + lane, 1);
         if (tok.row >= 0 && live(a, s, tok.pos) && MXQ_IN_RANGE(kChkAttendIn, tok.row, n_rows))
           row = tok.row;
       }

@@ -151,12 +151,15 @@ __device__ __forceinline__ Span span_of(const Args& a, int64_t b) {
 
 // The token of position v of a span: its place in the sequence, and its row in
 // the cache ((page * heads + head) * page_size + slot) or -1 where there is
-// none (a page list's -1, a page out of range, the end of the sequence).
+// none (a page list's -1, a page out of range, the end of the sequence).  The
+// table is read only where one of the `count` positions from v on, which share
+// a page, is attended to: entries before the window may be gone.
 struct Token {
   int64_t pos, row;
 };
 
-__device__ __forceinline__ Token token_at(const Args& a, const Span& s, int64_t b, int head, int v) {
+__device__ __forceinline__ Token token_at(const Args& a, const Span& s, int64_t b, int head, int v,
+                                          int count) {
   const PagedCache& c = a.c;
   Token t;
   int page_at, off;
@@ -173,6 +176,7 @@ __device__ __forceinline__ Token token_at(const Args& a, const Span& s, int64_t 
   }
   t.pos = (int64_t)page_at * c.page + off;
   t.row = -1;
+  if (t.pos >= s.len || (a.window > 0 && t.pos + count <= s.len - a.window)) return t;
   if (!MXQ_IN_RANGE(kChkAttendTable, page_at, c.max_pages)) return t;
   const int64_t page = __ldg(c.page_table + b * c.max_pages + page_at);
   if (page < 0 || page >= c.num_pages) {

@@ -182,7 +182,7 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
       for (int u = 0; u < U; ++u) {
         const int v = (first + (i + lane) * kTcWarps) * (kTile * U) + u * kTile;
         if (i + lane >= n || v >= v1) continue;
-        const Token tok = token_at(a, s, tg.b, tg.head, v);
+        const Token tok = token_at(a, s, tg.b, tg.head, v, kTile);
         if (tok.row < 0) continue;
         const int64_t start = a.window > 0 ? s.len - a.window : 0;
         const int lo = (int)max((int64_t)0, min((int64_t)kTile, start - tok.pos));

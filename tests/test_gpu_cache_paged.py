@@ -359,6 +359,26 @@ def test_attend_window_over_freed_pages():
     assert int(status) == 0 and torch.equal(got, want)
 
 
+@pytest.mark.parametrize("S", [16, 10])
+def test_attend_window_reads_no_table_entry_before_it(S):
+    # the entries of pages that lie before the window are out of range: they
+    # are neither read nor reported, with and without a list that names them
+    cache = ref.Cache([207], 1, 64, S, "fp8", 64)
+    q = queries(1, 2, 64, torch.bfloat16)
+    pages = torch.arange(21, dtype=torch.int32).expand(1, 1, 21).contiguous()
+    for window in (1, S, 33, 34, 64, 90):
+        table = cache.table.clone()
+        table[0, :(207 - window) // S] = -1
+        for listed in (None, pages):
+            want = check_attend(cache, q, window=window, pages=listed)[0]
+            status = torch.zeros(1, dtype=torch.int32, device=DEV)
+            got = mxq.attend_cache_paged(dev(q), dev(cache.k), dev(cache.v), dev(table),
+                                         dev(cache.lengths), "fp8", 64, window=window,
+                                         pages=None if listed is None else dev(listed),
+                                         status=status)
+            assert int(status) == 0 and torch.equal(got, want)
+
+
 @pytest.mark.parametrize("S,fmt,block", [(16, "fp8", 128), (64, "mxfp4", 32), (24, "nvfp4", 16)])
 def test_attend_listed_pages(S, fmt, block):
     H, D = 2, 128
@@ -581,3 +601,72 @@ def test_two_streams_at_once():
             got.append(mxq.attend_cache_paged(q, *args))
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_debug_variant_without_a_failed_check():
+    """The cases above on the library's debug variant, whose kernels check
+    every index (tests/conftest.py asks for its record after each)."""
+    import os
+    import subprocess
+    import sys
+
+    from nvfp4_quantization_amax_b200 import build
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    env = dict(os.environ, MXQ_LIBRARY=build.build(debug=True), MXQ_EXPECT_CLEAN_CHECKS="1")
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-p", "no:cacheprovider", "-m", "gpu",
+                        "-k", "not debug_variant", os.path.abspath(__file__)],
+                       cwd=root, env=env, capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0 and " passed" in r.stdout, r.stdout[-3000:] + r.stderr[-1000:]
+
+
+def test_odd_row_starts_of_scales_and_codes():
+    # slices of larger buffers: pages that begin off every 16-byte boundary take
+    # the general kernels, with the same results
+    cache = ref.Cache([70, 9], 2, 64, 16, "mxfp4", 32)
+    q = queries(2, 4, 64, torch.bfloat16)
+    want, _ = check_attend(cache, q)
+
+    def shifted(pair, by):
+        out = []
+        for t in pair:
+            flat = torch.full((t.numel() + by,), 0xFF, dtype=torch.uint8, device=DEV)
+            flat[by:] = t.reshape(-1).to(DEV)
+            out.append(flat[by:].view(t.shape))
+        return tuple(out)
+
+    table, lengths = dev(cache.table), dev(cache.lengths)
+    for by in (1, 2, 4, 8):
+        k, v = shifted(cache.k, by), shifted(cache.v, by)
+        got = mxq.attend_cache_paged(dev(q), k, v, table, lengths, "mxfp4", 32)
+        o, _, spread, reach = ref.attend(cache, q)
+        tol = ref.out_tolerance(q.dtype, 64, 70, o, spread, reach)
+        assert (np.abs(as_f64(got) - o) <= tol).all()
+        assert torch.equal(mxq.bound_cache_pages(k, table, lengths, "mxfp4", 32),
+                           mxq.bound_cache_pages(dev(cache.k), table, lengths, "mxfp4", 32))
+        x = torch.randn(3, 2, 64, dtype=torch.bfloat16, device=DEV)
+        offs = torch.tensor([2, 3], dtype=torch.int32, device=DEV)
+        mxq.append_cache_paged(x, None, offs, table, lengths, k, None, "mxfp4", 32)
+        whole = dev(cache.k)
+        mxq.append_cache_paged(x, None, offs, table, lengths, whole, None, "mxfp4", 32)
+        assert torch.equal(k[0], whole[0]) and torch.equal(k[1], whole[1])
+    assert want.shape == q.shape
+
+
+def test_calls_without_rows_or_sequences():
+    cache = ref.Cache([20], 2, 64, 16, "fp8", 64)
+    k, v = dev(cache.k), dev(cache.v)
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    table = torch.zeros(0, 3, dtype=torch.int32, device=DEV)
+    out, lse = mxq.attend_cache_paged(torch.zeros(0, 4, 64, dtype=torch.bfloat16, device=DEV), k, v,
+                                      table, none, "fp8", 64, return_lse=True)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    x = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device=DEV)
+    got = mxq.append_cache_paged(x, x, torch.zeros(1, dtype=torch.int32, device=DEV),
+                                 dev(cache.table), dev(cache.lengths), k, v, "fp8", 64, values=True)
+    assert got[0].shape == (0, 2, 64)
+    assert torch.equal(k[0].cpu(), cache.k[0])
+    bd = mxq.bound_cache_pages(k, table, none, "fp8", 64)
+    assert not bd.any()
+    q = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device=DEV)
+    assert mxq.select_cache_pages(q, bd, table, none, 16, 3).shape == (0, 2, 3)
