@@ -585,8 +585,9 @@ int launch_attend_cache_paged(const void* q, int dt, int64_t q_heads, int64_t q_
   else if (c.fmt == MXQ_FMT_FP8) rc = launch_general<MXQ_FMT_FP8>(a, dt, grid, st);
   else if (c.fmt == MXQ_FMT_MXFP4) rc = launch_general<MXQ_FMT_MXFP4>(a, dt, grid, st);
   else rc = launch_general<MXQ_FMT_NVFP4>(a, dt, grid, st);
+  if (rc != MXQ_OK) return rc;
   // a span of one unit is never split
-  if (rc != MXQ_OK || span <= kUnit) return rc == MXQ_OK && cudaGetLastError() != cudaSuccess ? (int)MXQ_ERR_CUDA : rc;
+  if (span <= kUnit) return cudaGetLastError() == cudaSuccess ? MXQ_OK : (int)MXQ_ERR_CUDA;
   return launch_join(a, dt, grid, st);
 }
 

@@ -221,8 +221,8 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 #pragma unroll
         for (int j = 0; j < SROUNDS; ++j) {
           const int tile = (U == 2 && (SROUNDS > 1 ? j : s_tile)) ? p.y : p.x;
-          cp_async16(fill + T::SCALES + (lane + 32 * j) * 16, s_from + (int64_t)max(tile, 0) * T::SC,
-                     tile >= 0 ? 16 : 0);
+          cp_async16(fill + T::SCALES + (lane + 32 * j) * 16,
+                     s_from + (int64_t)max(tile, 0) * T::SC, tile >= 0 ? 16 : 0);
         }
       }
       fill = next(fill);
@@ -270,7 +270,8 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
       }
 #pragma unroll
       for (int k = 0; k < T::KS; ++k)
-        top = fmaxf(top, fmaxf(max3(fabsf(x[k][0]), fabsf(x[k][1]), fabsf(x[k][2])), fabsf(x[k][3])));
+        top = max3(top, fmaxf(fabsf(x[k][0]), fabsf(x[k][1])),
+                   fmaxf(fabsf(x[k][2]), fabsf(x[k][3])));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // largest magnitude to [2^13, 2^14)
@@ -326,7 +327,8 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
       const bool part = live_rows != FULL;
       // whether a row of tile u is behind the end or before the window
       auto dead = [&](int u, int row) {
-        return row < (int)(live_rows >> (16 * u) & 255) || row >= (int)(live_rows >> (16 * u + 8) & 255);
+        return row < (int)(live_rows >> (16 * u) & 255) ||
+               row >= (int)(live_rows >> (16 * u + 8) & 255);
       };
       if (part) {  // no bytes of dead rows count
 #pragma unroll
@@ -364,8 +366,10 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 #pragma unroll
           for (int q4 = 0; q4 < (T::CH + 3) / 4; ++q4) {
             const uint32_t sel = t4 < 2 ? 0x6420 : 0x7531;  // 8 of a chunk's 32 channels
-            const uint32_t x0 = __byte_perm(sw0[2 * q4], NB > 4 ? sw0[2 * q4 + 1 < (NB + 3) / 4 ? 2 * q4 + 1 : 0] : 0u, sel);
-            const uint32_t x1 = __byte_perm(sw1[2 * q4], NB > 4 ? sw1[2 * q4 + 1 < (NB + 3) / 4 ? 2 * q4 + 1 : 0] : 0u, sel);
+            constexpr int WORDS = (NB + 3) / 4;
+            const int next = 2 * q4 + 1 < WORDS ? 2 * q4 + 1 : 0;  // 0: of no use
+            const uint32_t x0 = __byte_perm(sw0[2 * q4], NB > 4 ? sw0[next] : 0u, sel);
+            const uint32_t x1 = __byte_perm(sw1[2 * q4], NB > 4 ? sw1[next] : 0u, sel);
             uint32_t y0[2], y1[2];
             decode_word<MXQ_FMT_FP8>(x0, y0);
             decode_word<MXQ_FMT_FP8>(x1, y1);
@@ -474,7 +478,8 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
             if constexpr (T::kAbsolute) {
               if (have) {
 #pragma unroll
-                for (int mt = 0; mt < T::MT; ++mt) o[mt][nt][j] *= ex2(-up), o[mt][nt][j + 2] *= ex2(-up);
+                for (int mt = 0; mt < T::MT; ++mt)
+                  o[mt][nt][j] *= ex2(-up), o[mt][nt][j + 2] *= ex2(-up);
               }
             }
 #pragma unroll
@@ -549,166 +554,168 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
       }
 
       for (;;) {  // once, or once a band
-      // ---- weights times 2^(11 + r): x = s + r - E + 11
-      float x[U][NT][4];
-      if constexpr (!T::kAbsolute) {
-        auto relate = [&]() {
-          float most = -1.0f;
+        // ---- weights times 2^(11 + r): x = s + r - E + 11
+        float x[U][NT][4];
+        if constexpr (!T::kAbsolute) {
+          auto relate = [&]() {
+            float most = -1.0f;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float c[2];
+            for (int nt = 0; nt < NT; ++nt) {
+              float c[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              c[j] = (m[nt][j] - E[nt][j]) + (kWeightExp + (T::kRow ? 0.0f : (float)(r - 127)));
+              for (int j = 0; j < 2; ++j)
+                c[j] = (m[nt][j] - E[nt][j]) + (kWeightExp + (T::kRow ? 0.0f : (float)(r - 127)));
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+              for (int u = 0; u < U; ++u) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                x[u][nt][j] = d[u][nt][j] + (T::kRow ? rf[u][j >> 1] + c[j & 1] : c[j & 1]);
-                if (T::kRelative && wide && (rt[u][j >> 1] > r || rt[u][j >> 1] <= r - kSpan))
-                  x[u][nt][j] = none;
-              }
-              most = max3(most, x[u][nt][0], x[u][nt][1]);
-              most = max3(most, x[u][nt][2], x[u][nt][3]);
-            }
-          }
-          return most;
-        };
-        if (__any_sync(0xffffffffu, relate() > kWeightExp + kLag)) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              // the column's largest s - m + r of this band
-              float e = kLowest;
-#pragma unroll
-              for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const bool out_of = T::kRelative && wide && (rt[u][h] > r || rt[u][h] <= r - kSpan);
-                  const float rr = T::kRow ? rf[u][h] : (float)(r - 127);
-                  if (!out_of) e = fmaxf(e, d[u][nt][j + 2 * h] + rr);
+                for (int j = 0; j < 4; ++j) {
+                  x[u][nt][j] = d[u][nt][j] + (T::kRow ? rf[u][j >> 1] + c[j & 1] : c[j & 1]);
+                  if (T::kRelative && wide && (rt[u][j >> 1] > r || rt[u][j >> 1] <= r - kSpan))
+                    x[u][nt][j] = none;
                 }
-#pragma unroll
-              for (int w = 4; w < 32; w <<= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, w));
-              const float En = fmaxf(E[nt][j], m[nt][j] + e), fo = ex2(E[nt][j] - En);
-#pragma unroll
-              for (int mt = 0; mt < T::MT; ++mt) o[mt][nt][j] *= fo, o[mt][nt][j + 2] *= fo;
-              E[nt][j] = En;
-            }
-          relate();
-        }
-      }
-      const uint32_t rr = (uint32_t)r * 0x00010001u;
-
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-      const uint32_t vb = kb + u * (32 * T::RB), vs = sb + (2 * u + 1) * T::SC;
-      uint32_t p[TERMS][NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (T::kAbsolute) {
-            const float e = ex2(d[u][nt][j]);
-            l[nt][j & 1] += e;
-            y[j] = e * 2048.0f;
-          } else {
-            y[j] = ex2(x[u][nt][j]);
-          }
-        }
-        const uint32_t h0 = half2_of(y[0], y[1]), h1 = half2_of(y[2], y[3]);
-        p[0][nt][0] = sm100::movmatrix_trans(h0);
-        p[0][nt][1] = sm100::movmatrix_trans(h1);
-        if constexpr (TERMS == 2) {
-          p[1][nt][0] = sm100::movmatrix_trans(
-              half2_of(y[0] - f16lo(h0), y[1] - f16hi(h0)));
-          p[1][nt][1] = sm100::movmatrix_trans(
-              half2_of(y[2] - f16lo(h1), y[3] - f16hi(h1)));
-        }
-      }
-
-      // ---- O^T += V^T P^T: tokens 2 t, 2 t + 1 and 8 more; channels of group g
-      constexpr int READS = T::RB / 8 / LB, W = LB / 4;
-      constexpr int PER_WORD = 2 * Codes<FMT>::kPairs;  // channels
-      // words of one scale
-      constexpr int SPAN = T::B / PER_WORD < W ? T::B / PER_WORD : W;
-#pragma unroll
-      for (int rd = 0; rd < READS; ++rd) {
-        uint32_t w[4][W];  // tokens 2t, 2t+1, 2t+8, 2t+9
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          lds_bytes<LB>(w[k], vb + src_v[k & 1] + (k >> 1) * EIGHT + rd * 128);
-        uint32_t sc[2] = {0, 0};
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const int ch0 = j * PER_WORD;  // of this read
-          // the scales of this lane's block: tokens (2t, 2t+1), (2t+8, 2t+9)
-          if constexpr (T::kAbsolute || T::kRelative) {
-            if (j % SPAN == 0) {
-              const int b = T::channel(g, rd * W * PER_WORD + ch0) / T::B;
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                uint32_t s0, s1;
-                lds_bytes<1>(&s0, vs + (2 * t4 + 8 * k) * NB + b);
-                lds_bytes<1>(&s1, vs + (2 * t4 + 1 + 8 * k) * NB + b);
-                if constexpr (T::kAbsolute) {
-                  sc[k] = e4m3x2_to_f16x2(s1 * 256 + s0);
-                } else {
-                  // f16 exponents k - r + OFF + 15 in both halves, within [0, OFF + 15]
-                  const uint32_t y = s1 * 65536 + s0 + (T::OFF + 15) * 0x00010001u;
-                  sc[k] = !wide ? (y - rr) << 10
-                                : (__vminu2(__vmaxu2(y, rr) - rr, (T::OFF + 15) * 0x00010001u)) << 10;
-                }
+                most = max3(most, x[u][nt][0], x[u][nt][1]);
+                most = max3(most, x[u][nt][2], x[u][nt][3]);
               }
             }
-          }
-          uint32_t f[2][PER_WORD];  // token pairs, channels
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t A = w[2 * k][j], Bw = w[2 * k + 1][j];
-            if constexpr (FMT == MXQ_FMT_FP8) {
-              decode_word<FMT>(__byte_perm(A, Bw, 0x5140), f[k]);
-              decode_word<FMT>(__byte_perm(A, Bw, 0x7362), f[k] + 2);
-            } else {
-              uint32_t even[4], odd[4];
-              decode_word<FMT>((A & 0x0F0F0F0Fu) | ((Bw << 4) & 0xF0F0F0F0u), even);
-              decode_word<FMT>(((A >> 4) & 0x0F0F0F0Fu) | (Bw & 0xF0F0F0F0u), odd);
-#pragma unroll
-              for (int h = 0; h < 4; ++h) f[k][2 * h] = even[h], f[k][2 * h + 1] = odd[h];
-            }
-            if constexpr (T::kAbsolute || T::kRelative) {
-#pragma unroll
-              for (int h = 0; h < PER_WORD; ++h) f[k][h] = hmul2(f[k][h], sc[k]);
-            }
-          }
-#pragma unroll
-          for (int h = 0; h < PER_WORD / 2; ++h) {  // two channels: one tile of O
-            const uint32_t af[4] = {f[0][2 * h], f[0][2 * h + 1], f[1][2 * h], f[1][2 * h + 1]};
-            const int mt = (rd * W * PER_WORD + ch0) / 2 + h;
+            return most;
+          };
+          if (__any_sync(0xffffffffu, relate() > kWeightExp + kLag)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int tm = 0; tm < TERMS; ++tm)
-                mma16816(o[mt][nt], af, p[tm][nt][0], p[tm][nt][1]);
+              for (int j = 0; j < 2; ++j) {
+                // the column's largest s - m + r of this band
+                float e = kLowest;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    const bool out_of =
+                        T::kRelative && wide && (rt[u][h] > r || rt[u][h] <= r - kSpan);
+                    const float rr = T::kRow ? rf[u][h] : (float)(r - 127);
+                    if (!out_of) e = fmaxf(e, d[u][nt][j + 2 * h] + rr);
+                  }
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1)
+                  e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, w));
+                const float En = fmaxf(E[nt][j], m[nt][j] + e), fo = ex2(E[nt][j] - En);
+#pragma unroll
+                for (int mt = 0; mt < T::MT; ++mt) o[mt][nt][j] *= fo, o[mt][nt][j + 2] *= fo;
+                E[nt][j] = En;
+              }
+            relate();
           }
         }
-      }
-      }
-      if constexpr (T::kRelative) {
-        if (wide) {  // the next band below this one
-          int top = -1;
+        const uint32_t rr = (uint32_t)r * 0x00010001u;
+
 #pragma unroll
-          for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+          const uint32_t vb = kb + u * (32 * T::RB), vs = sb + (2 * u + 1) * T::SC;
+          uint32_t p[TERMS][NT][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (rt[u][h] <= r - kSpan) top = max(top, rt[u][h]);
-          r = __reduce_max_sync(0xffffffffu, top);
-          if (r >= 0) continue;
+          for (int nt = 0; nt < NT; ++nt) {
+            float y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if constexpr (T::kAbsolute) {
+                const float e = ex2(d[u][nt][j]);
+                l[nt][j & 1] += e;
+                y[j] = e * 2048.0f;
+              } else {
+                y[j] = ex2(x[u][nt][j]);
+              }
+            }
+            const uint32_t h0 = half2_of(y[0], y[1]), h1 = half2_of(y[2], y[3]);
+            p[0][nt][0] = sm100::movmatrix_trans(h0);
+            p[0][nt][1] = sm100::movmatrix_trans(h1);
+            if constexpr (TERMS == 2) {
+              p[1][nt][0] = sm100::movmatrix_trans(
+                  half2_of(y[0] - f16lo(h0), y[1] - f16hi(h0)));
+              p[1][nt][1] = sm100::movmatrix_trans(
+                  half2_of(y[2] - f16lo(h1), y[3] - f16hi(h1)));
+            }
+          }
+
+          // ---- O^T += V^T P^T: tokens 2 t, 2 t + 1 and 8 more; channels of group g
+          constexpr int READS = T::RB / 8 / LB, W = LB / 4;
+          constexpr int PER_WORD = 2 * Codes<FMT>::kPairs;  // channels
+          // words of one scale
+          constexpr int SPAN = T::B / PER_WORD < W ? T::B / PER_WORD : W;
+#pragma unroll
+          for (int rd = 0; rd < READS; ++rd) {
+            uint32_t w[4][W];  // tokens 2t, 2t+1, 2t+8, 2t+9
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              lds_bytes<LB>(w[k], vb + src_v[k & 1] + (k >> 1) * EIGHT + rd * 128);
+            uint32_t sc[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+              const int ch0 = j * PER_WORD;  // of this read
+              // the scales of this lane's block: tokens (2t, 2t+1), (2t+8, 2t+9)
+              if constexpr (T::kAbsolute || T::kRelative) {
+                if (j % SPAN == 0) {
+                  const int b = T::channel(g, rd * W * PER_WORD + ch0) / T::B;
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    uint32_t s0, s1;
+                    lds_bytes<1>(&s0, vs + (2 * t4 + 8 * k) * NB + b);
+                    lds_bytes<1>(&s1, vs + (2 * t4 + 1 + 8 * k) * NB + b);
+                    if constexpr (T::kAbsolute) {
+                      sc[k] = e4m3x2_to_f16x2(s1 * 256 + s0);
+                    } else {
+                      // f16 exponents k - r + OFF + 15 in both halves, within [0, OFF + 15]
+                      constexpr uint32_t MOST = (T::OFF + 15) * 0x00010001u;
+                      const uint32_t y = s1 * 65536 + s0 + MOST;
+                      sc[k] = (wide ? __vminu2(__vmaxu2(y, rr) - rr, MOST) : y - rr) << 10;
+                    }
+                  }
+                }
+              }
+              uint32_t f[2][PER_WORD];  // token pairs, channels
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t A = w[2 * k][j], Bw = w[2 * k + 1][j];
+                if constexpr (FMT == MXQ_FMT_FP8) {
+                  decode_word<FMT>(__byte_perm(A, Bw, 0x5140), f[k]);
+                  decode_word<FMT>(__byte_perm(A, Bw, 0x7362), f[k] + 2);
+                } else {
+                  uint32_t even[4], odd[4];
+                  decode_word<FMT>((A & 0x0F0F0F0Fu) | ((Bw << 4) & 0xF0F0F0F0u), even);
+                  decode_word<FMT>(((A >> 4) & 0x0F0F0F0Fu) | (Bw & 0xF0F0F0F0u), odd);
+#pragma unroll
+                  for (int h = 0; h < 4; ++h) f[k][2 * h] = even[h], f[k][2 * h + 1] = odd[h];
+                }
+                if constexpr (T::kAbsolute || T::kRelative) {
+#pragma unroll
+                  for (int h = 0; h < PER_WORD; ++h) f[k][h] = hmul2(f[k][h], sc[k]);
+                }
+              }
+#pragma unroll
+              for (int h = 0; h < PER_WORD / 2; ++h) {  // two channels: one tile of O
+                const uint32_t af[4] = {f[0][2 * h], f[0][2 * h + 1], f[1][2 * h], f[1][2 * h + 1]};
+                const int mt = (rd * W * PER_WORD + ch0) / 2 + h;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int tm = 0; tm < TERMS; ++tm)
+                    mma16816(o[mt][nt], af, p[tm][nt][0], p[tm][nt][1]);
+              }
+            }
+          }
         }
-      }
-      break;
+        if constexpr (T::kRelative) {
+          if (wide) {  // the next band below this one
+            int top = -1;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (rt[u][h] <= r - kSpan) top = max(top, rt[u][h]);
+            r = __reduce_max_sync(0xffffffffu, top);
+            if (r >= 0) continue;
+          }
+        }
+        break;
       }
       if constexpr (!T::kAbsolute) {
 #pragma unroll
