@@ -25,14 +25,22 @@ struct PackedFormat<MXQ_FMT_NVFP4> {
   static constexpr uint32_t kQFrac = 0x400000u;
 };
 
-// Least k with 2^k * qmax >= amax, clamped to the format's range.
+// Least k with 2^k * qmax >= amax, clamped to the format's range.  The
+// fraction's excess over qmax's carries into the exponent; zeros and
+// subnormals come out below the range's lower end, whatever their fraction.
 template <int FMT>
 __device__ __forceinline__ int group_scale_exp(uint32_t amax_f32bits) {
   using F = PackedFormat<FMT>;
-  if (amax_f32bits == 0) return F::kLo;
-  int k = floor_log2_f32bits(amax_f32bits) - F::kQExp +
-          (frac23_f32bits(amax_f32bits) > F::kQFrac ? 1 : 0);
-  return k < F::kLo ? F::kLo : (k > F::kHi ? F::kHi : k);
+  const int k = (int)((amax_f32bits + (0x7FFFFFu - F::kQFrac)) >> 23) - 127 - F::kQExp;
+  return min(max(k, F::kLo), F::kHi);
+}
+
+// 2^k and 2^-k for a group's k: 2^-127, a subnormal, is the one special case.
+__device__ __forceinline__ float group_scale(int k) {
+  return __uint_as_float((uint32_t)(k + 127) << 23);
+}
+__device__ __forceinline__ float group_inverse(int k) {
+  return __uint_as_float(max((uint32_t)(127 - k) << 23, 0x00400000u));
 }
 
 // Scale byte of 2^k.  E4M3 of 2^k, k in [-9, 8]: subnormal 2^(k+9) / 2^-9
@@ -63,34 +71,17 @@ __device__ __forceinline__ uint2 encode8(const float* x, float inv) {
   if constexpr (FMT == MXQ_FMT_FP8) {
     uint32_t b[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = e4m3x2(x[2 * j] * inv, x[2 * j + 1] * inv);
+    for (int j = 0; j < 4; ++j) {
+      float v0, v1;
+      mul2_rn(v0, v1, x[2 * j], x[2 * j + 1], inv, inv);
+      b[j] = e4m3x2(v0, v1);
+    }
     return make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
   } else {
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = fmaf(x[j], inv, 0.0f);
+    for (int j = 0; j < 8; j += 2) fma2_rn_zero(v[j], v[j + 1], x[j], x[j + 1], inv, inv);
     return make_uint2(e2m1x8(v), 0u);
-  }
-}
-
-// Eight decoded values (code times scale, exact in f32).
-template <int FMT>
-__device__ __forceinline__ void decode8(uint2 c, float s, float* v) {
-  if constexpr (FMT == MXQ_FMT_FP8) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t w = j < 2 ? c.x : c.y;
-      const uint32_t h2 = e4m3x2_to_f16x2((w >> (16 * (j & 1))) & 0xFFFFu);
-      v[2 * j] = f16lo(h2) * s;
-      v[2 * j + 1] = f16hi(h2) * s;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t h2 = e2m1x2_to_f16x2((c.x >> (8 * j)) & 0xFFu);
-      v[2 * j] = fmaf(f16lo(h2), s, 0.0f);  // zero magnitudes give +0
-      v[2 * j + 1] = fmaf(f16hi(h2), s, 0.0f);
-    }
   }
 }
 
@@ -114,6 +105,24 @@ __device__ __forceinline__ void decode_word(uint32_t w, uint32_t* r) {
         "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
         : "r"(w));
+  }
+}
+
+// Eight decoded values (code times scale, exact in f32).  The bytes are taken
+// out by shifts: a word that e2m1x8 has just packed and decode_word unpacks
+// comes out with zeros for its upper bytes (nvcc 12.9), so decode_word is for
+// words read from memory.
+template <int FMT>
+__device__ __forceinline__ void decode8(uint2 c, float s, float* v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (FMT == MXQ_FMT_FP8) {
+      const uint32_t h = e4m3x2_to_f16x2(((j < 2 ? c.x : c.y) >> (16 * (j & 1))) & 0xFFFFu);
+      mul2_rn(v[2 * j], v[2 * j + 1], f16lo(h), f16hi(h), s, s);
+    } else {  // zero magnitudes give +0
+      const uint32_t h = e2m1x2_to_f16x2((c.x >> (8 * j)) & 0xFFu);
+      fma2_rn_zero(v[2 * j], v[2 * j + 1], f16lo(h), f16hi(h), s, s);
+    }
   }
 }
 

@@ -107,59 +107,68 @@ __device__ __forceinline__ uint32_t amax8(const uint32_t* w) {
 // tokens_per_cta tokens (all heads, K and V), about 4 items a thread, so that
 // each thread has several loads in flight; B/8 lanes share a group's maximum,
 // taken on the raw 16-bit magnitudes.  The place of each token is looked up
-// once per block.
+// once per block, while the first loads (which need no place) are under way.
 template <int DT, int FMT, int LPB>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, AppendPlan plan) {
-  __shared__ int64_t s_row[kMaxCtaTokens];  // of head 0 in the cache; heads are S rows apart
+  __shared__ int64_t s_row[kMaxCtaTokens];  // head 0's in the cache, in items; S rows to the next
   constexpr int kUnroll = ElemTraits<DT>::kBytes == 2 ? 4 : 2;
+  constexpr uint32_t kItemBytes = 8 * ElemTraits<DT>::kBytes;
   constexpr int kWords = ElemTraits<DT>::kBytes == 2 ? 4 : 8;
   const PagedCache& c = a.c;
   const int64_t t0 = (int64_t)blockIdx.x * a.tokens_per_cta;
   const int n_tok = (int)min((int64_t)a.tokens_per_cta, a.rows - t0);
   const uint32_t n_items = n_tok * plan.per_tok.d, per_head = plan.per_head.d;
+  const uint32_t lane = threadIdx.x & 31;
+  const int64_t k_bytes = a.k_stride * ElemTraits<DT>::kBytes;
+  const int64_t v_bytes = a.v_stride * ElemTraits<DT>::kBytes;
+  const char* const k_from = (const char*)a.k + t0 * k_bytes;
+  const char* const v_from = (const char*)a.v + t0 * v_bytes;
+  uint32_t w[kUnroll][kWords];
+  auto load = [&](uint32_t base) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t item = base + u * kThreads + lane;
+      if (item >= n_items) continue;
+      const uint32_t tok = plan.per_tok.div(item);
+      const uint32_t rem = item - tok * plan.per_tok.d;
+      const char* from = rem < plan.per_row
+                             ? k_from + tok * k_bytes + rem * kItemBytes
+                             : v_from + tok * v_bytes + (rem - plan.per_row) * kItemBytes;
+      if (!MXQ_IN_RANGE(kChkAppendIn, t0 + tok, a.rows)) continue;
+#pragma unroll
+      for (int j = 0; j < kWords; j += 4) {
+        const uint4 v = ld_stream_v4(from + 4 * j);
+        w[u][j] = v.x, w[u][j + 1] = v.y, w[u][j + 2] = v.z, w[u][j + 3] = v.w;
+      }
+    }
+  };
+  uint32_t base = threadIdx.x & ~31;
+  load(base);  // under way while the places are looked up
   check_offs(a);
   if ((int)threadIdx.x < n_tok) {
     const int64_t slot = slot_of_row(a, t0 + threadIdx.x);
     const int64_t page = slot / c.page;
-    s_row[threadIdx.x] = slot < 0 ? -1 : page * c.heads * c.page + (slot - page * c.page);
+    s_row[threadIdx.x] =
+        slot < 0 ? -1 : (page * c.heads * c.page + (slot - page * c.page)) * per_head;
   }
   __syncthreads();
-  const uint32_t lane = threadIdx.x & 31;
-  for (uint32_t base = threadIdx.x & ~31; base < n_items; base += kThreads * kUnroll) {
-    uint32_t w[kUnroll][kWords];
-    int64_t dst[kUnroll], src[kUnroll];
-    bool is_v[kUnroll];
+  const int64_t head_items = (int64_t)(c.page - 1) * per_head;  // beyond a dense row's
+  for (;;) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const uint32_t item = base + u * kThreads + lane;
-      dst[u] = -1;
-      if (item >= n_items) continue;
-      const uint32_t tok = plan.per_tok.div(item);
+      const bool within = item < n_items;
+      const uint32_t tok = within ? plan.per_tok.div(item) : 0;
       uint32_t rem = item - tok * plan.per_tok.d;
-      is_v[u] = rem >= plan.per_row;
-      if (is_v[u]) rem -= plan.per_row;
+      const bool is_v = rem >= plan.per_row;
+      if (is_v) rem -= plan.per_row;
       const int64_t row = s_row[tok];
-      if (row < 0) continue;
-      const uint32_t head = plan.per_head.div(rem);
-      dst[u] = (row + (int64_t)head * c.page) * per_head + (rem - head * per_head);  // in items
-      src[u] = (t0 + tok) * plan.per_row + rem;                                     // dense
-      const int64_t in = (t0 + tok) * ((is_v[u] ? a.v_stride : a.k_stride) / 8) + rem;
-      const char* from = (const char*)(is_v[u] ? a.v : a.k) + in * (8 * ElemTraits<DT>::kBytes);
-      if (MXQ_IN_RANGE(kChkAppendIn, t0 + tok, a.rows)) {
-#pragma unroll
-        for (int j = 0; j < kWords; j += 4) {
-          const uint4 v = ld_stream_v4(from + 4 * j);
-          w[u][j] = v.x, w[u][j + 1] = v.y, w[u][j + 2] = v.z, w[u][j + 3] = v.w;
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const bool valid = dst[u] >= 0;
+      const bool valid = within && row >= 0;
       uint32_t m = valid ? amax8<DT>(w[u]) : 0;
 #pragma unroll
       for (int o = 1; o < LPB; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
       if (!valid) continue;
+      const int64_t dst = row + rem + plan.per_head.div(rem) * head_items;
       const int k = group_scale_exp<FMT>(mag_as_f32_bits<DT>(m));
       float x[8];
 #pragma unroll
@@ -169,20 +178,24 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, AppendPl
         else
           x[j] = elem_to_f32<DT>(w[u][j]);
       }
-      const uint2 code = encode8<FMT>(x, exp2i(-k));
-      if (MXQ_IN_RANGE(kChkAppendOut, dst[u], c.num_pages * c.heads * c.page * per_head))
-        store_codes<FMT>(is_v[u] ? c.v_codes : c.k_codes, dst[u], code);
+      const uint2 code = encode8<FMT>(x, group_inverse(k));
+      if (MXQ_IN_RANGE(kChkAppendOut, dst, c.num_pages * c.heads * c.page * per_head))
+        store_codes<FMT>(is_v ? c.v_codes : c.k_codes, dst, code);
       if ((lane & (LPB - 1)) == 0 &&
-          MXQ_IN_RANGE(kChkAppendScale, dst[u] / LPB,
+          MXQ_IN_RANGE(kChkAppendScale, dst / LPB,
                        c.num_pages * c.heads * c.page * (int64_t)c.row_scales()))
-        (is_v[u] ? c.v_scales : c.k_scales)[dst[u] / LPB] = (uint8_t)scale_byte<FMT>(k);
-      void* out = is_v[u] ? a.v_out : a.k_out;
+        (is_v ? c.v_scales : c.k_scales)[(uint64_t)dst / LPB] = (uint8_t)scale_byte<FMT>(k);
+      void* out = is_v ? a.v_out : a.k_out;
       if (out) {
+        const int64_t src = (t0 + tok) * plan.per_row + rem;  // dense
         float y[8];
-        decode8<FMT>(code, exp2i(k), y);
-        if (MXQ_IN_RANGE(kChkAppendOut, src[u], a.rows * plan.per_row)) store8<DT>(out, src[u], y);
+        decode8<FMT>(code, group_scale(k), y);
+        if (MXQ_IN_RANGE(kChkAppendOut, src, a.rows * plan.per_row)) store8<DT>(out, src, y);
       }
     }
+    base += kThreads * kUnroll;
+    if (base >= n_items) break;
+    load(base);
   }
 }
 
