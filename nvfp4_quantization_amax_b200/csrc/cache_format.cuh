@@ -64,25 +64,21 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 }
 
 // Element codes of eight values x * 2^-k.  fp8: E4M3 (sign of zero kept);
-// fp4: E2M1 with the sign bit iff x < 0 (fmaf(x, inv, +0) turns -0 into +0
-// and keeps the sign of a negative product that underflows).
+// fp4: E2M1 with the sign bit iff x < 0 (an addend +0 turns -0 into +0 and
+// keeps the sign of a negative product that underflows).
 template <int FMT>
 __device__ __forceinline__ uint2 encode8(const float* x, float inv) {
-  if constexpr (FMT == MXQ_FMT_FP8) {
-    uint32_t b[4];
+  float v[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float v0, v1;
-      mul2_rn(v0, v1, x[2 * j], x[2 * j + 1], inv, inv);
-      b[j] = e4m3x2(v0, v1);
-    }
-    return make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
-  } else {
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) fma2_rn_zero(v[j], v[j + 1], x[j], x[j + 1], inv, inv);
-    return make_uint2(e2m1x8(v), 0u);
+  for (int j = 0; j < 8; j += 2) {
+    if constexpr (FMT == MXQ_FMT_FP8) mul2_rn(v[j], v[j + 1], x[j], x[j + 1], inv, inv);
+    else fma2_rn_zero(v[j], v[j + 1], x[j], x[j + 1], inv, inv);
   }
+  if constexpr (FMT == MXQ_FMT_FP8)
+    return make_uint2(e4m3x2(v[0], v[1]) | e4m3x2(v[2], v[3]) << 16,
+                      e4m3x2(v[4], v[5]) | e4m3x2(v[6], v[7]) << 16);
+  else
+    return make_uint2(e2m1x8(v), 0u);
 }
 
 // The values of a word of codes as f16 pairs in the codes' order: two of four
@@ -108,22 +104,51 @@ __device__ __forceinline__ void decode_word(uint32_t w, uint32_t* r) {
   }
 }
 
-// Eight decoded values (code times scale, exact in f32).  The bytes are taken
-// out by shifts: a word that e2m1x8 has just packed and decode_word unpacks
-// comes out with zeros for its upper bytes (nvcc 12.9), so decode_word is for
+// The codes and their values as f16 pairs.  Each conversion back takes the
+// byte that its conversion made: decode_word on a word that e2m1x8 has just
+// packed gave zeros for the upper bytes (nvcc 12.9), so decode_word is for
 // words read from memory.
 template <int FMT>
-__device__ __forceinline__ void decode8(uint2 c, float s, float* v) {
+__device__ __forceinline__ uint2 encode8(const float* x, float inv, uint32_t* h) {
+  if constexpr (FMT == MXQ_FMT_FP8) {
+    const uint2 c = encode8<FMT>(x, inv);
+    decode_word<FMT>(c.x, h);
+    decode_word<FMT>(c.y, h + 2);
+    return c;
+  } else {
+    uint32_t b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float v0, v1;
+      fma2_rn_zero(v0, v1, x[2 * j], x[2 * j + 1], inv, inv);
+      asm("{\n\t.reg .b8 t;\n\t"
+          "cvt.rn.satfinite.e2m1x2.f32 t, %3, %2;\n\t"
+          "cvt.rn.f16x2.e2m1x2 %1, t;\n\t"
+          "cvt.u32.u8 %0, t;\n\t}"
+          : "=r"(b[j]), "=r"(h[j])
+          : "f"(v0), "f"(v1));
+    }
+    return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, 0u);
+  }
+}
+
+// Eight decoded values, f16 code values (pairs) times the scale, exact in f32.
+template <int FMT>
+__device__ __forceinline__ void scaled8(const uint32_t* h, float s, float* v) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    if constexpr (FMT == MXQ_FMT_FP8) {
-      const uint32_t h = e4m3x2_to_f16x2(((j < 2 ? c.x : c.y) >> (16 * (j & 1))) & 0xFFFFu);
-      mul2_rn(v[2 * j], v[2 * j + 1], f16lo(h), f16hi(h), s, s);
-    } else {  // zero magnitudes give +0
-      const uint32_t h = e2m1x2_to_f16x2((c.x >> (8 * j)) & 0xFFu);
-      fma2_rn_zero(v[2 * j], v[2 * j + 1], f16lo(h), f16hi(h), s, s);
-    }
+    if constexpr (FMT == MXQ_FMT_FP8)
+      mul2_rn(v[2 * j], v[2 * j + 1], f16lo(h[j]), f16hi(h[j]), s, s);
+    else  // zero magnitudes give +0
+      fma2_rn_zero(v[2 * j], v[2 * j + 1], f16lo(h[j]), f16hi(h[j]), s, s);
   }
+}
+template <int FMT>
+__device__ __forceinline__ void decode8(uint2 c, float s, float* v) {
+  uint32_t h[4];
+  decode_word<FMT>(c.x, h);
+  if constexpr (FMT == MXQ_FMT_FP8) decode_word<FMT>(c.y, h + 2);
+  scaled8<FMT>(h, s, v);
 }
 
 // Eight values (code times scale, exact in f32) of one (fp4) or two words.

@@ -33,30 +33,58 @@ struct AppendArgs {
   PagedCache c;
 };
 
-// Slot (page * S + position in the page) of row t, or -1: padding, or a row
-// whose position or page is out of range (reported).
-__device__ __forceinline__ int64_t slot_of_row(const AppendArgs& a, int64_t t) {
-  int lo = 0, hi = (int)a.c.n_seqs;  // the first b with offs[b] > t
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.offs + mid) > t) hi = mid;
-    else lo = mid + 1;
-  }
-  if (lo == a.c.n_seqs) return -1;
-  const int64_t end = __ldg(a.offs + lo), begin = lo > 0 ? __ldg(a.offs + lo - 1) : 0;
-  const int64_t len = __ldg(a.c.lengths + lo), pos = len - (end - t);
+// Row of head 0 of the cache for row t, a token of sequence b (the first whose
+// offs lies above t), or -1: padding, or a row whose position or page is out of
+// range (reported).  The rows of the other heads lie S apart.
+__device__ __forceinline__ int64_t row_of(const AppendArgs& a, int64_t t, int b) {
+  if (b == a.c.n_seqs) return -1;
+  const int64_t end = __ldg(a.offs + b), begin = b > 0 ? __ldg(a.offs + b - 1) : 0;
+  const int64_t len = __ldg(a.c.lengths + b), pos = len - (end - t);
   if (begin < 0 || begin > t || end > a.rows) {
     if (a.c.status) *a.c.status = MXQ_ERR_BAD_OFFS;
     return -1;
   }
   int64_t page = -1;
-  if (pos >= 0 && len <= a.c.max_pages * a.c.page)
-    page = __ldg(a.c.page_table + lo * a.c.max_pages + pos / a.c.page);
+  uint32_t at = 0;
+  if (pos >= 0 && len <= a.c.max_pages * a.c.page) {  // positions end at 2^30
+    const uint32_t j = (uint32_t)pos / (uint32_t)a.c.page;
+    at = (uint32_t)pos - j * (uint32_t)a.c.page;
+    page = __ldg(a.c.page_table + b * a.c.max_pages + j);
+  }
   if (page < 0 || page >= a.c.num_pages) {
     if (a.c.status) *a.c.status = MXQ_ERR_BAD_PAGE;
     return -1;
   }
-  return page * a.c.page + pos % a.c.page;
+  return page * a.c.heads * a.c.page + at;
+}
+
+// The first b >= from with offs[b] > t, n_seqs where there is none; the places
+// near `from` first.
+__device__ __forceinline__ int sequence_of(const AppendArgs& a, int64_t t, int from) {
+  const int n = (int)a.c.n_seqs;
+  int lo = from, step = 1;
+  while (step <= n - lo && __ldg(a.offs + lo + step - 1) <= t) lo += step, step *= 2;
+  int hi = lo + min(step - 1, n - lo);
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.offs + mid) > t) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+// The same from 0 by a warp, which looks at 32 places at a time: a block has
+// few tokens, and the loads that wait for one another are what a search costs.
+__device__ __forceinline__ int sequence_of_by_warp(const AppendArgs& a, int64_t t, int lane) {
+  int lo = 0, hi = (int)a.c.n_seqs;  // lo <= b <= hi
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;  // a lane: the last of its `step` sequences
+    const int mid = min(lo + lane * step + step - 1, hi - 1);
+    const uint32_t over = __ballot_sync(0xffffffffu, __ldg(a.offs + mid) > t);
+    if (over == 0) return hi;
+    lo += (__ffs(over) - 1) * step;
+    hi = min(lo + step - 1, hi - 1);
+  }
+  return lo;
 }
 
 // Block 0 looks over the whole of offs: a sequence whose end lies before its
@@ -70,22 +98,18 @@ __device__ __forceinline__ void check_offs(const AppendArgs& a) {
 
 constexpr int kMaxCtaTokens = 32;
 
-// Quotients of 31-bit numbers by a divisor known at launch: floor(x m / 2^s)
-// with m = floor(2^s / d) + 1 and s = 31 + ceil(log2 d) is exact for x < 2^31
+// Quotients of x < 2^15 by a divisor d <= 2^15 known at launch: floor(2x m /
+// 2^32) with m = ceil(2^31 / d) is exact, as x (m d - 2^31) < x d < 2^31
 // (Granlund and Montgomery, "Division by invariant integers", 1994).
+constexpr int64_t kMaxItems = 1 << 15;
 struct Divisor {
-  uint32_t d, shift;
-  uint64_t m;
-  explicit Divisor(uint32_t x = 1) : d(x), shift(31), m(0) {
-    while (((uint64_t)1 << (shift - 31)) < d) ++shift;
-    m = ((uint64_t)1 << shift) / d + 1;
-  }
-  __device__ __forceinline__ uint32_t div(uint32_t x) const { return (uint32_t)(x * m >> shift); }
+  uint32_t d, m;
+  explicit Divisor(uint32_t x = 1) : d(x), m((uint32_t)((((uint64_t)1 << 31) + x - 1) / x)) {}
+  __device__ __forceinline__ uint32_t div(uint32_t x) const { return __umulhi(2 * x, m); }
 };
 
 struct AppendPlan {
   Divisor per_tok, per_head;  // items of a token, of a head
-  uint32_t per_row;           // of a token's K
 };
 
 // Magnitude of the largest of eight elements, as f32 bits.
@@ -103,15 +127,18 @@ __device__ __forceinline__ uint32_t amax8(const uint32_t* w) {
   }
 }
 
-// Fast path.  An item is 8 channels of one row of K or V; a block takes
-// tokens_per_cta tokens (all heads, K and V), about 4 items a thread, so that
-// each thread has several loads in flight; B/8 lanes share a group's maximum,
+// Fast path.  An item is 8 channels of one row of K and of V, which share the
+// arithmetic of their place; a block takes tokens_per_cta tokens (all heads),
+// about 2 items a thread, so that each thread has several loads in flight; B/8 lanes share a group's maximum,
 // taken on the raw 16-bit magnitudes.  The place of each token is looked up
 // once per block, while the first loads (which need no place) are under way.
+// Bound by issue: 25 thousand tokens of 4 x 128 in mxfp4 with their values take
+// 23 us (28 with K and V as items of their own, 33 with the loads after the
+// lookup too), 18 at the speed of HBM.
 template <int DT, int FMT, int LPB>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, AppendPlan plan) {
   __shared__ int64_t s_row[kMaxCtaTokens];  // head 0's in the cache, in items; S rows to the next
-  constexpr int kUnroll = ElemTraits<DT>::kBytes == 2 ? 4 : 2;
+  constexpr int kUnroll = ElemTraits<DT>::kBytes == 2 ? 2 : 1;
   constexpr uint32_t kItemBytes = 8 * ElemTraits<DT>::kBytes;
   constexpr int kWords = ElemTraits<DT>::kBytes == 2 ? 4 : 8;
   const PagedCache& c = a.c;
@@ -119,37 +146,39 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, AppendPl
   const int n_tok = (int)min((int64_t)a.tokens_per_cta, a.rows - t0);
   const uint32_t n_items = n_tok * plan.per_tok.d, per_head = plan.per_head.d;
   const uint32_t lane = threadIdx.x & 31;
-  const int64_t k_bytes = a.k_stride * ElemTraits<DT>::kBytes;
-  const int64_t v_bytes = a.v_stride * ElemTraits<DT>::kBytes;
-  const char* const k_from = (const char*)a.k + t0 * k_bytes;
-  const char* const v_from = (const char*)a.v + t0 * v_bytes;
-  uint32_t w[kUnroll][kWords];
+  const int64_t in_bytes[2] = {a.k_stride * ElemTraits<DT>::kBytes,
+                               a.v_stride * ElemTraits<DT>::kBytes};
+  const char* const in[2] = {(const char*)a.k + t0 * in_bytes[0],
+                             (const char*)a.v + t0 * in_bytes[1]};
+  uint32_t w[kUnroll][2][kWords];
   auto load = [&](uint32_t base) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const uint32_t item = base + u * kThreads + lane;
       if (item >= n_items) continue;
-      const uint32_t tok = plan.per_tok.div(item);
-      const uint32_t rem = item - tok * plan.per_tok.d;
-      const char* from = rem < plan.per_row
-                             ? k_from + tok * k_bytes + rem * kItemBytes
-                             : v_from + tok * v_bytes + (rem - plan.per_row) * kItemBytes;
+      const uint32_t tok = plan.per_tok.div(item), rem = item - tok * plan.per_tok.d;
       if (!MXQ_IN_RANGE(kChkAppendIn, t0 + tok, a.rows)) continue;
 #pragma unroll
-      for (int j = 0; j < kWords; j += 4) {
-        const uint4 v = ld_stream_v4(from + 4 * j);
-        w[u][j] = v.x, w[u][j + 1] = v.y, w[u][j + 2] = v.z, w[u][j + 3] = v.w;
+      for (int s = 0; s < 2; ++s) {
+        if (s == 1 && !a.v) break;
+        const char* from = in[s] + tok * in_bytes[s] + rem * kItemBytes;
+#pragma unroll
+        for (int j = 0; j < kWords; j += 4) {
+          const uint4 v = ld_stream_v4(from + 4 * j);
+          w[u][s][j] = v.x, w[u][s][j + 1] = v.y, w[u][s][j + 2] = v.z, w[u][s][j + 3] = v.w;
+        }
       }
     }
   };
   uint32_t base = threadIdx.x & ~31;
   load(base);  // under way while the places are looked up
   check_offs(a);
-  if ((int)threadIdx.x < n_tok) {
-    const int64_t slot = slot_of_row(a, t0 + threadIdx.x);
-    const int64_t page = slot / c.page;
-    s_row[threadIdx.x] =
-        slot < 0 ? -1 : (page * c.heads * c.page + (slot - page * c.page)) * per_head;
+  if (threadIdx.x < 32) {
+    const int first = sequence_of_by_warp(a, t0, lane);
+    if ((int)lane < n_tok) {
+      const int64_t row = row_of(a, t0 + lane, sequence_of(a, t0 + lane, first));
+      s_row[lane] = row < 0 ? -1 : row * per_head;
+    }
   }
   __syncthreads();
   const int64_t head_items = (int64_t)(c.page - 1) * per_head;  // beyond a dense row's
@@ -159,38 +188,42 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, AppendPl
       const uint32_t item = base + u * kThreads + lane;
       const bool within = item < n_items;
       const uint32_t tok = within ? plan.per_tok.div(item) : 0;
-      uint32_t rem = item - tok * plan.per_tok.d;
-      const bool is_v = rem >= plan.per_row;
-      if (is_v) rem -= plan.per_row;
+      const uint32_t rem = item - tok * plan.per_tok.d;
       const int64_t row = s_row[tok];
       const bool valid = within && row >= 0;
-      uint32_t m = valid ? amax8<DT>(w[u]) : 0;
-#pragma unroll
-      for (int o = 1; o < LPB; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (!valid) continue;
       const int64_t dst = row + rem + plan.per_head.div(rem) * head_items;
-      const int k = group_scale_exp<FMT>(mag_as_f32_bits<DT>(m));
-      float x[8];
+      const int64_t src = t0 * plan.per_tok.d + item;  // dense
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if constexpr (kWords == 4)
-          x[j] = elem_to_f32<DT>((j & 1) ? w[u][j / 2] >> 16 : w[u][j / 2] & 0xFFFFu);
-        else
-          x[j] = elem_to_f32<DT>(w[u][j]);
-      }
-      const uint2 code = encode8<FMT>(x, group_inverse(k));
-      if (MXQ_IN_RANGE(kChkAppendOut, dst, c.num_pages * c.heads * c.page * per_head))
-        store_codes<FMT>(is_v ? c.v_codes : c.k_codes, dst, code);
-      if ((lane & (LPB - 1)) == 0 &&
-          MXQ_IN_RANGE(kChkAppendScale, dst / LPB,
-                       c.num_pages * c.heads * c.page * (int64_t)c.row_scales()))
-        (is_v ? c.v_scales : c.k_scales)[(uint64_t)dst / LPB] = (uint8_t)scale_byte<FMT>(k);
-      void* out = is_v ? a.v_out : a.k_out;
-      if (out) {
-        const int64_t src = (t0 + tok) * plan.per_row + rem;  // dense
-        float y[8];
-        decode8<FMT>(code, group_scale(k), y);
-        if (MXQ_IN_RANGE(kChkAppendOut, src, a.rows * plan.per_row)) store8<DT>(out, src, y);
+      for (int s = 0; s < 2; ++s) {
+        if (s == 1 && !a.v) break;
+        const uint32_t* raw = w[u][s];
+        uint32_t m = valid ? amax8<DT>(raw) : 0;
+#pragma unroll
+        for (int o = 1; o < LPB; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (!valid) continue;
+        const int k = group_scale_exp<FMT>(mag_as_f32_bits<DT>(m));
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if constexpr (kWords == 4)
+            x[j] = elem_to_f32<DT>((j & 1) ? raw[j / 2] >> 16 : raw[j / 2] & 0xFFFFu);
+          else
+            x[j] = elem_to_f32<DT>(raw[j]);
+        }
+        uint32_t h[4];  // the codes' values, as f16
+        const uint2 code = encode8<FMT>(x, group_inverse(k), h);
+        if (MXQ_IN_RANGE(kChkAppendOut, dst, c.num_pages * c.heads * c.page * per_head))
+          store_codes<FMT>(s ? c.v_codes : c.k_codes, dst, code);
+        if ((lane & (LPB - 1)) == 0 &&
+            MXQ_IN_RANGE(kChkAppendScale, dst / LPB,
+                         c.num_pages * c.heads * c.page * (int64_t)c.row_scales()))
+          (s ? c.v_scales : c.k_scales)[(uint64_t)dst / LPB] = (uint8_t)scale_byte<FMT>(k);
+        void* out = s ? a.v_out : a.k_out;
+        if (out && MXQ_IN_RANGE(kChkAppendOut, src, a.rows * plan.per_tok.d)) {
+          float y[8];
+          scaled8<FMT>(h, group_scale(k), y);
+          store8<DT>(out, src, y);
+        }
       }
     }
     base += kThreads * kUnroll;
@@ -215,9 +248,9 @@ __global__ void __launch_bounds__(kThreads) append_general_kernel(AppendArgs a) 
     const int rem = (int)(i - t * per_tok);
     const bool is_v = rem >= c.heads * nb;
     const int hg = is_v ? rem - c.heads * nb : rem, head = hg / nb, g = hg - head * nb;
-    const int64_t slot = slot_of_row(a, t);
-    if (slot < 0) continue;
-    const int64_t page = slot / c.page, row = (page * c.heads + head) * c.page + slot % c.page;
+    int64_t row = row_of(a, t, sequence_of(a, t, 0));
+    if (row < 0) continue;
+    row += (int64_t)head * c.page;
     const void* in = is_v ? a.v : a.k;
     const int64_t src = t * (is_v ? a.v_stride : a.k_stride) + head * c.dim + g * B;
     const int64_t dense = (t * c.heads + head) * c.dim + g * B;
@@ -257,22 +290,21 @@ __global__ void __launch_bounds__(kThreads) append_general_kernel(AppendArgs a) 
 
 template <int DT, int FMT>
 void launch_append_fmt(AppendArgs a, bool fast, cudaStream_t st) {
-  const int64_t per_tok = (int64_t)a.c.heads * (a.c.dim / 8) * (a.v ? 2 : 1);
-  // items are counted in 32 bits, up to 32 tokens of a block
-  if (!fast || per_tok > (1 << 24)) {
+  const int64_t per_tok = (int64_t)a.c.heads * (a.c.dim / 8);
+  // a block's items are at most 512 or one token's
+  if (!fast || per_tok > kMaxItems) {
     const int64_t n = a.rows * a.c.heads * a.c.row_scales() * (a.v ? 2 : 1);
     append_general_kernel<DT, FMT>
         <<<wave_grid((const void*)append_general_kernel<DT, FMT>, kThreads, n, kThreads), kThreads,
            0, st>>>(a);
     return;
   }
-  a.tokens_per_cta = (int)(per_tok >= 1024 ? 1 : 1024 / per_tok);
+  a.tokens_per_cta = (int)(per_tok >= 512 ? 1 : 512 / per_tok);
   if (a.tokens_per_cta > kMaxCtaTokens) a.tokens_per_cta = kMaxCtaTokens;
   const unsigned grid = (unsigned)((a.rows + a.tokens_per_cta - 1) / a.tokens_per_cta);
   AppendPlan plan;
   plan.per_tok = Divisor((uint32_t)per_tok);
   plan.per_head = Divisor((uint32_t)(a.c.dim / 8));
-  plan.per_row = (uint32_t)(a.c.heads * (a.c.dim / 8));
   switch (a.c.block / 8) {
     case 1: append_kernel<DT, FMT, 1><<<grid, kThreads, 0, st>>>(a, plan); break;
     case 2: append_kernel<DT, FMT, 2><<<grid, kThreads, 0, st>>>(a, plan); break;
