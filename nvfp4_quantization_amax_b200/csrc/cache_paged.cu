@@ -444,12 +444,15 @@ __global__ void __launch_bounds__(kBoundThreads) bound_kernel(BoundArgs a) {
           }
         }
       }
+      // the first row's lanes take the others' bounds; no other lane changes, so
+      // that what is taken is of that lane's channels alone, whatever the width
       for (int q = 1; q < at_once; ++q) {
-        const int from = (lane + q * width) & 31;  // of use in the first row's lanes
+        const int from = (lane + q * width) & 31;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          lo[i] = fminf(lo[i], __shfl_sync(0xffffffffu, lo[i], from));
-          hi[i] = fmaxf(hi[i], __shfl_sync(0xffffffffu, hi[i], from));
+          const float l = __shfl_sync(0xffffffffu, lo[i], from);
+          const float h = __shfl_sync(0xffffffffu, hi[i], from);
+          if (r == 0) lo[i] = fminf(lo[i], l), hi[i] = fmaxf(hi[i], h);
         }
       }
       if (r == 0 && MXQ_IN_RANGE(kChkBoundOut, page, c.num_pages)) {
