@@ -289,6 +289,8 @@ uint64_t attend_cache_paged_workspace_bytes(int64_t q_heads, int64_t kv_heads, i
  *           the logits; -infinity without tokens.
  *  workspace  device, 16-byte aligned, attend_cache_paged_workspace_bytes;
  *           clobbered, not shared by calls that overlap on the GPU.
+ *  A query that is not finite, or a logit beyond f32's range, makes its
+ *  head's row of out and lse NaN (not where the sequence has no tokens).
  *  Logits, softmax statistics and sums are f32.  A token's value blocks whose
  *  scale is below 2^-18 of the token's largest one lose bits.
  *  Fast path: head_dim 64, 128 or 256, page_size a multiple of 16, block_size

@@ -252,7 +252,8 @@ def attend_cache_paged(q, k_cache, v_cache, page_table, lengths, format, block_s
     over, a page listed twice counts twice).  Returns out [sequences, q_heads,
     head_dim] of q's dtype, with return_lse also the float32 [sequences,
     q_heads] natural logarithm of the sum of exponentials of the logits.  A
-    sequence without tokens gives zeros and -inf.  No gradient is defined.
+    sequence without tokens gives zeros and -inf, a query that is not finite
+    NaN in its row.  No gradient is defined.
     workspace: optional device uint8 scratch of at least
     attend_cache_paged_workspace_bytes (C) bytes.
     """

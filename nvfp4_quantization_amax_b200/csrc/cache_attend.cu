@@ -329,16 +329,16 @@ attend_general_kernel(Args a, int dt, int pad) {
       float top = kLowest, ref = kLowest, sum = 0.0f, val = 0.0f;
 #pragma unroll
       for (int w = 0; w < kTcWarps; ++w)
-        if (s_l[w][r] > 0.0f) top = fmaxf(top, s_m[w][r]), ref = fmaxf(ref, s_e[w][r]);
+        if (s_l[w][r] != 0.0f) top = fmaxf(top, s_m[w][r]), ref = fmaxf(ref, s_e[w][r]);
 #pragma unroll
       for (int w = 0; w < kTcWarps; ++w) {
-        if (!(s_l[w][r] > 0.0f)) continue;
+        if (s_l[w][r] == 0.0f) continue;  // no token
         sum = fmaf(s_l[w][r], exp2f(s_m[w][r] - top), sum);
         val = fmaf(sums[(w * 8 + r) * D + ch], exp2f(s_e[w][r] - ref), val);
       }
       const float back = (ref - top) - kWeightExp - (float)OFF, half = truncf(back * 0.5f);
-      put(a, dt, tg, r, ch, sum > 0.0f ? val / sum * exp2f(half) * exp2f(back - half) : 0.0f);
-      if (ch == 0) put_weight(a, tg, r, sum > 0.0f ? top + log2f(sum) : kLowest);
+      put(a, dt, tg, r, ch, sum != 0.0f ? val / sum * exp2f(half) * exp2f(back - half) : 0.0f);
+      if (ch == 0) put_weight(a, tg, r, sum != 0.0f ? top + log2f(sum) : kLowest);
     }
     __syncthreads();  // the buffers are the next pair's
   });
@@ -445,7 +445,7 @@ join_kernel(Args a, int dt, int n_ctas, int per_head, bool by_pair) {
         if ((lane + 32 * j) * VEC < D) val[j][k] += other[(lane + 32 * j) * VEC + k];
     sum += other[D];
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;  // a NaN stays one
 #pragma unroll
   for (int j = 0; j < NC; ++j)
 #pragma unroll
@@ -453,7 +453,7 @@ join_kernel(Args a, int dt, int n_ctas, int per_head, bool by_pair) {
       const int ch = (lane + 32 * j) * VEC + k;
       if (ch < D) put(a, dt, t, r, ch, val[j][k] * inv);
     }
-  if (lane == 0) put_weight(a, t, r, sum > 0.0f ? top + log2f(sum) : kLowest);
+  if (lane == 0) put_weight(a, t, r, sum != 0.0f ? top + log2f(sum) : kLowest);
 }
 
 // Launched with programmatic stream serialization: it takes its place while

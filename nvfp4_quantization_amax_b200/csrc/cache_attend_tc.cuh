@@ -754,25 +754,26 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
     __syncthreads();
     const int heads = min(8 * NT, a.group - r0);
     // a warp's factor 2^(E - ref); out = sum x 2^(ref - top - 11 -
-    // OFF) / l, the power in two steps
+    // OFF) / l, the power in two steps.  A sum of 0 has seen no token; one that
+    // is not a number (of a logit that is none) stays so
     const int fw = threadIdx.x / (8 * NT), fr = threadIdx.x % (8 * NT);
     if (fw < kTcWarps) {
       float top = kLowest, ref = kLowest, sum = 0.0f;
 #pragma unroll
       for (int w = 0; w < kTcWarps; ++w)
-        if (s_l[w][fr] > 0.0f) top = fmaxf(top, s_m[w][fr]);
+        if (s_l[w][fr] != 0.0f) top = fmaxf(top, s_m[w][fr]);
 #pragma unroll
       for (int w = 0; w < kTcWarps; ++w)
-        if (s_l[w][fr] > 0.0f) ref = fmaxf(ref, s_r[w][fr]);
+        if (s_l[w][fr] != 0.0f) ref = fmaxf(ref, s_r[w][fr]);
 #pragma unroll
       for (int w = 0; w < kTcWarps; ++w)
-        if (s_l[w][fr] > 0.0f) sum = fmaf(s_l[w][fr], exp2f(s_m[w][fr] - top), sum);
-      s_f[fw][fr] = s_l[fw][fr] > 0.0f ? exp2f(s_r[fw][fr] - ref) : 0.0f;
+        if (s_l[w][fr] != 0.0f) sum = fmaf(s_l[w][fr], exp2f(s_m[w][fr] - top), sum);
+      s_f[fw][fr] = s_l[fw][fr] != 0.0f ? exp2f(s_r[fw][fr] - ref) : 0.0f;
       if (fw == 0 && fr < heads) {
         const float back = (ref - top) - kWeightExp - (float)T::OFF, half = truncf(back * 0.5f);
-        s_back[0][fr] = sum > 0.0f ? exp2f(half) / sum : 0.0f;
-        s_back[1][fr] = sum > 0.0f ? exp2f(back - half) : 0.0f;
-        put_weight(a, tg, fr, sum > 0.0f ? top + log2f(sum) : kLowest);
+        s_back[0][fr] = sum != 0.0f ? exp2f(half) / sum : 0.0f;
+        s_back[1][fr] = sum != 0.0f ? exp2f(back - half) : 0.0f;
+        put_weight(a, tg, fr, sum != 0.0f ? top + log2f(sum) : kLowest);
       }
     }
     __syncthreads();
