@@ -291,7 +291,10 @@ uint64_t attend_cache_paged_workspace_bytes(int64_t q_heads, int64_t kv_heads, i
  *           clobbered, not shared by calls that overlap on the GPU.
  *  A query that is not finite, or a logit beyond f32's range, makes its
  *  head's row of out and lse NaN (not where the sequence has no tokens).
- *  Logits, softmax statistics and sums are f32.  A token's value blocks whose
+ *  Logits, softmax statistics and sums are f32.  Queries enter the products
+ *  with all bits of a bf16 or f16 element and 22 of an f32 one, but none below
+ *  2^-38 of the head's largest; every block of the keys counts, however far
+ *  its scale lies below the others.  A token's value blocks whose
  *  scale is below 2^-18 of the token's largest one lose bits.
  *  Fast path: head_dim 64, 128 or 256, page_size a multiple of 16, block_size
  *  a power of two of at least 32 (fp8), 32 (mxfp4) or 16 (nvfp4), codes and

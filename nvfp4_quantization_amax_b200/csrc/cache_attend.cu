@@ -6,9 +6,13 @@
 // where rows do not lie in whole tiles of it.  A warp takes 16 tokens at a time,
 // each row read by the whole warp (as wide as its alignment allows) and decoded
 // to f16 in shared memory, padded with zeros to 16 channels: K's values times
-// 2^-(the row's largest scale exponent), which returns in f32 on the sums; V's
-// likewise, its exponent in the token's weight (nvfp4: the values themselves).
+// 2^-(the row's largest scale exponent), which returns in f32 on the sums (blocks
+// too far below it for f16 are read again, in bands with a largest of their
+// own); V's likewise, its exponent in the token's weight (nvfp4: the values
+// themselves).
 // Then S = K Q^T and O^T = V^T P^T by mma.m16n8k16 from ldmatrix.
+#include <type_traits>
+
 #include "cache_attend.cuh"
 #include "sm100_primitives.cuh"
 
@@ -48,28 +52,41 @@ struct Channels {
       }
     }
   }
-  // The largest scale byte (E8M0), over all lanes.
-  __device__ __forceinline__ int top_scale(int lane, int D) const {
-    uint32_t top = 0;
+  // The largest scale byte (E8M0), over all lanes; BAND: of those below `lim`,
+  // -1 where there is none.
+  template <bool BAND = false>
+  __device__ __forceinline__ int top_scale(int lane, int D, int lim = 256) const {
+    int top = BAND ? -1 : 0;
+    auto count = [&](int byte) {
+      if (!BAND || byte < lim) top = max(top, byte);
+    };
     if constexpr (WIDE) {
-      top = lane * NC < D ? scale[0] : 0;
+      if (lane * NC < D) count((int)scale[0]);
     } else {
 #pragma unroll
-      for (int i = 0; i < NC; ++i) top = max(top, scale[i]);
+      for (int i = 0; i < NC; ++i) count((int)scale[i]);
     }
-    return (int)__reduce_max_sync(0xffffffffu, top);
+    return __reduce_max_sync(0xffffffffu, top);
   }
   // Code times 2^(OFF + scale exponent - top's) (E8M0), or times the scale
   // (nvfp4), in f16 at their channels of a row of `pad` channels; 0 behind the
-  // last channel.  Factors below 2^-14 count as 0.
-  template <int OFF>
-  __device__ __forceinline__ void put(__half* row, int top, int lane, int D, int pad) const {
+  // last channel.  Factors below 2^-14 count as 0, and BAND: so do blocks whose
+  // scale byte is not below `lim`.  Returns whether the lane has left out
+  // codes other than zeros because their factor was below 2^-14.
+  template <int OFF, bool BAND = false>
+  __device__ __forceinline__ bool put(__half* row, int top, int lane, int D, int pad,
+                                      int lim = 256) const {
     auto factor = [&](uint32_t byte) -> uint32_t {  // one f16
       if constexpr (FMT == MXQ_FMT_NVFP4) return e4m3x2_to_f16x2(byte) & 0xFFFFu;
+      else if (BAND && (int)byte >= lim) return 0u;
       else return (uint32_t)max(0, OFF + 15 + (int)byte - top) << 10;
     };
+    constexpr uint32_t kMagnitude = FMT == MXQ_FMT_FP8 ? 0x7F7F7F7Fu : 0x77777777u;
+    auto low = [&](uint32_t byte) {
+      return FMT != MXQ_FMT_NVFP4 && OFF + 15 + (int)byte - top <= 0;
+    };
     if constexpr (WIDE) {
-      if (lane * NC >= pad) return;
+      if (lane * NC >= pad) return false;
       const bool in = lane * NC < D;
       const uint32_t s = in ? factor(scale[0]) * 0x00010001u : 0u;
       uint32_t h[NC / 2 < 2 ? 2 : NC / 2];
@@ -95,7 +112,12 @@ struct Channels {
 #pragma unroll
         for (int i = 0; i < NC / 2; i += 4)
           *(uint4*)(to + 2 * i) = make_uint4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < CODES; ++i) any |= in ? code[i] & kMagnitude : 0u;
+      return any != 0 && low(scale[0]);
     } else {
+      bool left = false;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int ch = lane + 32 * i;
@@ -104,7 +126,9 @@ struct Channels {
                                               : e2m1x2_to_f16x2(code[i] & 15u);
         row[ch] = __ushort_as_half(
             (unsigned short)(ch < D ? hmul2(h & 0xFFFFu, factor(scale[i])) & 0xFFFFu : 0u));
+        left |= ch < D && (h & 0x7FFFu) != 0 && low(scale[i]);
       }
+      return left;
     }
   }
 };
@@ -127,7 +151,6 @@ attend_general_kernel(Args a, int dt, int pad) {
   __shared__ float s_qf[8], s_m[kTcWarps][8], s_e[kTcWarps][8], s_l[kTcWarps][8];
   using Ch = Channels<FMT, NC, WIDE>;
   constexpr int MT = NC * 2;          // tiles of 16 channels
-  constexpr int AT_ONCE = 4;  // rows whose bytes are under way (8 or 16: 15 to 60 % slower)
   constexpr int OFF = FMT == MXQ_FMT_NVFP4 ? 0 : FMT == MXQ_FMT_FP8 ? 7 : 12;
   const PagedCache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = c.dim, stride = pad + 8;
@@ -190,9 +213,17 @@ attend_general_kernel(Args a, int dt, int pad) {
       }
       const unsigned live_rows = __ballot_sync(0xffffffffu, row >= 0);
       if (live_rows == 0) continue;
-      // K or V into the tile; lane y of the result holds the top scale byte of token y
-      auto fetch = [&](const uint8_t* codes, const uint8_t* scales) {
+      // K or V into the tile; lane y's `tops` is the top scale byte of token y.
+      // BAND: only blocks that lay below what token y's f16 reached with the top
+      // byte that lane y gives.  Returns whether the lane has left out any.
+      bool left;
+      auto fetch = [&](auto band, const uint8_t* codes, const uint8_t* scales, int above) {
+        constexpr bool BAND = decltype(band)::value;
+        // rows whose bytes are under way (8 or 16: 15 to 60 % slower); bands are
+        // rare, and take few registers
+        constexpr int AT_ONCE = BAND ? 1 : 4;
         int tops = 127;
+        left = false;
         __syncwarp();  // the tile's last reads are done
 #pragma unroll
         for (int y0 = 0; y0 < kTile; y0 += AT_ONCE) {
@@ -206,9 +237,12 @@ attend_general_kernel(Args a, int dt, int pad) {
           for (int y = 0; y < AT_ONCE; ++y) {
             __half* to = tile + (y0 + y) * stride;
             if (live_rows >> (y0 + y) & 1) {
-              const int top = FMT == MXQ_FMT_NVFP4 ? 127 : x[y].top_scale(lane, D);
+              const int lim =
+                  BAND ? __shfl_sync(0xffffffffu, above, y0 + y) - OFF - 14 : 256;
+              const int top =
+                  FMT == MXQ_FMT_NVFP4 ? 127 : x[y].template top_scale<BAND>(lane, D, lim);
               if (lane == y0 + y) tops = top;
-              x[y].template put<OFF>(to, top, lane, D, pad);
+              left |= x[y].template put<OFF, BAND>(to, top, lane, D, pad, lim);
             } else {
               for (int ch = lane * 2; ch < pad; ch += 64) *(uint32_t*)(to + ch) = 0u;
             }
@@ -218,30 +252,47 @@ attend_general_kernel(Args a, int dt, int pad) {
         return tops;
       };
       // ---- S = K Q^T, rows tokens g, g + 8, columns heads 2 t, 2 t + 1
-      const int k_tops = fetch(c.k_codes, c.k_scales);
-      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float d[4];
+      auto products = [&](int k_tops, float* y) {
 #pragma unroll
-      for (int k = 0; k < MT; ++k) {
-        if (k * 16 >= pad) continue;
-        uint32_t f[4], q[4];
-        ldmatrix4(f, k_at + k * 32);
-        ldmatrix4(q, q_at + k * 32);
-        mma16816(d, f, q[0], q[1]);
-        if (two) mma16816(d, f, q[2], q[3]);
-      }
-      const int v_tops = fetch(c.v_codes, c.v_scales);
-      // of tokens g and g + 8: K's factor, V's exponent
-      float kf[2], rf[2];
+        for (int j = 0; j < 4; ++j) y[j] = 0.0f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        kf[h] = exp2i(__shfl_sync(0xffffffffu, k_tops, g + 8 * h) - 127 - OFF);
-        rf[h] = (float)(__shfl_sync(0xffffffffu, v_tops, g + 8 * h) - 127);
+        for (int k = 0; k < MT; ++k) {
+          if (k * 16 >= pad) continue;
+          uint32_t f[4], q[4];
+          ldmatrix4(f, k_at + k * 32);
+          ldmatrix4(q, q_at + k * 32);
+          mma16816(y, f, q[0], q[1]);
+          if (two) mma16816(y, f, q[2], q[3]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float kf = exp2i(max(__shfl_sync(0xffffffffu, k_tops, g + 8 * h), 0) - 127 - OFF);
+          y[2 * h] *= kf;
+          y[2 * h + 1] *= kf;
+        }
+      };
+      int k_tops = fetch(std::false_type(), c.k_codes, c.k_scales, 256);
+      products(k_tops, d);
+      // blocks too far below their row's largest for its f16: in bands of their own
+      if constexpr (FMT != MXQ_FMT_NVFP4) {
+        while (__any_sync(0xffffffffu, left)) {
+          k_tops = fetch(std::true_type(), c.k_codes, c.k_scales, k_tops);
+          float y[4];
+          products(k_tops, y);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d[j] += y[j];
+        }
       }
+      const int v_tops = fetch(std::false_type(), c.v_codes, c.v_scales, 256);
+      float rf[2];  // V's exponent of tokens g and g + 8
+#pragma unroll
+      for (int h = 0; h < 2; ++h) rf[h] = (float)(__shfl_sync(0xffffffffu, v_tops, g + 8 * h) - 127);
       // ---- d = s - m, and the reference where one exceeds it by 2^4
       float over = -1.0f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        d[j] = d[j] * kf[j >> 1] * qf[j & 1] - m[j & 1];
+        d[j] = d[j] * qf[j & 1] - m[j & 1];
         if (!(live_rows >> (j < 2 ? g : g + 8) & 1)) d[j] = none;
         over = fmaxf(over, d[j]);
       }

@@ -7,7 +7,7 @@ import torch
 
 import nvfp4_quantization_amax_b200 as mxq
 import paged_reference as ref
-from test_gpu_cache_paged import as_f64, dev, queries
+from test_gpu_cache_paged import as_f64, check_attend, dev, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +61,67 @@ def test_a_query_that_is_not_finite_gives_nan(fmt, block, D, S, dtype):
         others = [0, 2, 3, 4, 5]
         assert (np.abs(out[1:, others] - want[1:, others]) <= tol[1:, others]).all()
         assert (np.abs(lse[1:, others] - wl[1:, others]) <= ltol[1:, others]).all()
+
+
+# ------------------------------------------- keys and logits far from others
+
+def query_error(cache, q):
+    """[n, Hq]: what the rounding of queries to f16 terms adds to a logit's
+    error.  A head's elements are scaled by a power of two, the largest to
+    [2^13, 2^14).  Of an element the terms keep 22 bits (one term of a bf16 or
+    f16 element all of it), but nothing under f16's smallest step: half of 2^-24
+    beside 2^13 is 2^-38 of the largest, times the sum of the key's magnitudes."""
+    n, Hq, D = q.shape
+    top = q.double().abs().amax(-1).numpy()
+    keys = np.zeros((n, Hq))
+    for b in range(n):
+        for j in range(Hq):
+            k = np.abs(cache.values(cache.k, b, j * cache.H // Hq)).sum(1)
+            keys[b, j] = k.max() if k.size else 0.0
+    return 2.0 ** -38 * top * keys / D ** 0.5
+
+
+def check_within(cache, q, spare):
+    """check_attend's bounds with `spare` more of error for each head's logits."""
+    out, lse = mxq.attend_cache_paged(dev(q), dev(cache.k), dev(cache.v), dev(cache.table),
+                                      dev(cache.lengths), cache.fmt, cache.block, return_lse=True)
+    want, wl, spread, reach = ref.attend(cache, q)
+    N, D = max(cache.lens), cache.D
+    tol = ref.out_tolerance(q.dtype, D, N, want, spread, reach) + 2 * spare[..., None] * spread
+    assert (np.abs(as_f64(out) - want) <= tol).all(), np.max(np.abs(as_f64(out) - want) / tol)
+    tol = ref.lse_tolerance(D, N, wl, reach) + spare
+    assert (np.abs(as_f64(lse) - wl) <= tol).all(), np.max(np.abs(as_f64(lse) - wl) / tol)
+
+
+@pytest.mark.parametrize("fmt,block,D,S", [("fp8", 8, 40, 10), ("fp8", 16, 128, 16),
+                                           ("fp8", 1, 7, 3), ("mxfp4", 8, 64, 16),
+                                           ("mxfp4", 20, 80, 24), ("mxfp4", 64, 512, 16),
+                                           ("fp8", 32, 128, 16), ("mxfp4", 32, 128, 16)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_keys_with_a_block_far_above_the_others(fmt, block, D, S, dtype):
+    # the second block's keys are 2^by times the others'; the query is zero or
+    # as much smaller there, so that the logits are those of the other blocks,
+    # or of all
+    for by in (21, 22, 27, 28, 60, 120):
+        cache = ref.Cache([70, 1, 33], 2, D, S, fmt, block, seed=D)
+        live = cache.k[1][..., 1] != 0xFF
+        live[::2] = live[::2] & (torch.arange(S) % 3 != 0)  # not every token's
+        cache.k[1][..., 1] = torch.where(live, cache.k[1][..., 1] + by, cache.k[1][..., 1])
+        q = queries(3, 4, D, dtype)
+        q[..., block:2 * block] = 0
+        check_attend(cache, q)
+        if by < 30:
+            q[..., block:2 * block] = queries(3, 4, D, dtype, seed=5)[..., :block] * 2.0 ** -by
+            check_within(cache, q, query_error(cache, q))
+
+
+@pytest.mark.parametrize("fmt,block", [("fp8", 8), ("mxfp4", 8)])
+def test_keys_with_empty_blocks(fmt, block):
+    # a block of zeros has the least scale
+    cache = ref.Cache([70, 1, 33], 2, 64, 10, fmt, block, seed=2)
+    codes, scales = cache.k
+    width = block if fmt == "fp8" else block // 2
+    live = scales[..., 3] != 0xFF
+    codes[..., 3 * width:4 * width][live] = 0
+    scales[..., 3] = torch.where(live, torch.tensor(1, dtype=torch.uint8), scales[..., 3])
+    check_attend(cache, queries(3, 4, 64, torch.float32))
