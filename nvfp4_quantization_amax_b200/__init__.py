@@ -9,7 +9,10 @@ device raises.
 
 Inputs that live in host memory are accepted too: they are copied to the
 current CUDA device (asynchronously when pinned), processed there, and the
-results are copied back to host memory before the call returns.
+results are copied back to host memory before the call returns.  A call whose
+results stay on the device waits for the copies of its host arguments, so
+that these may be written again as soon as it has returned (captured into a
+graph, pinned ones are read at every replay).
 """
 from ._abi import (  # noqa: F401
     CacheQuantization,

@@ -128,10 +128,13 @@ def _stream(dev):
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _to_device(t, dev=None):
+def _to_device(t, dev=None, waits=True):
     """(device tensor, was_on_host) for an input.  A host tensor is moved to
     `dev` (default: the current CUDA device), a pinned one without blocking
-    the host; a CUDA tensor must already be on `dev`."""
+    the host where the call `waits` for its results before it returns: else
+    its owner could write into it before the copy has read it.  (A call that
+    is captured can wait for nothing; its graph reads the tensor at every
+    replay.)  A CUDA tensor must already be on `dev`."""
     if t.is_cuda:
         if dev is not None and t.device != dev:
             raise ValueError("input on %s, the call runs on %s" % (t.device, dev))
@@ -140,7 +143,11 @@ def _to_device(t, dev=None):
         raise RuntimeError("no CUDA device: libmxq runs only on the GPU")
     if dev is None:
         dev = torch.device("cuda", torch.cuda.current_device())
-    return t.to(dev, non_blocking=t.is_pinned()), True
+    later = t.is_pinned()
+    if later and not waits:
+        with torch.cuda.device(dev):
+            later = torch.cuda.is_current_stream_capturing()
+    return t.to(dev, non_blocking=later), True
 
 
 def _to_host(t):
@@ -349,7 +356,7 @@ def mx_dequantize(packed, scales, dtype=torch.bfloat16, out=None):
                         "mx_dequantize"):
             return ho
     packed, host = _to_device(packed)
-    scales, _ = _to_device(scales, packed.device)
+    scales, _ = _to_device(scales, packed.device, host)
     packed = packed.contiguous()
     scales = scales.contiguous()
     Kh = packed.shape[-1]
@@ -452,7 +459,7 @@ def dequantize_cache_packed(codes, scales, format, block_size, dtype=torch.bfloa
                             "dequantize_cache_packed"):
                 return ho
     codes, host = _to_device(codes)
-    scales, _ = _to_device(scales, codes.device)
+    scales, _ = _to_device(scales, codes.device, host)
     codes, scales = codes.contiguous(), scales.contiguous()
     C = scales.shape[-1] * B
     rows = scales.numel() // scales.shape[-1] if scales.shape[-1] else 0
@@ -491,9 +498,9 @@ def mxfp4_grouped_mm(a, packed, scales, offs, transpose_w=False, out=None, statu
     if a.dtype != torch.bfloat16:
         raise TypeError("mxfp4_grouped_mm: activations must be bf16")
     a, host = _to_device(a)
-    packed, _ = _to_device(packed, a.device)
-    scales, _ = _to_device(scales, a.device)
-    offs, _ = _to_device(offs, a.device)
+    packed, _ = _to_device(packed, a.device, host)
+    scales, _ = _to_device(scales, a.device, host)
+    offs, _ = _to_device(offs, a.device, host)
     a, packed, scales = a.contiguous(), packed.contiguous(), scales.contiguous()
     offs = offs.to(torch.int32).contiguous()
     E, N, Kh = packed.shape
@@ -544,9 +551,9 @@ def w4a4_grouped_mm(x, packed, scales, offs, out=None, status=None, x_packed=Non
         dev = x_quantized[0].device if isinstance(x_quantized[0], torch.Tensor) else None
         if dev is None or dev.type != "cuda":
             raise ValueError("w4a4_grouped_mm: x_quantized must hold CUDA tensors")
-    packed, _ = _to_device(packed, dev)
-    scales, _ = _to_device(scales, dev)
-    offs, _ = _to_device(offs, dev)
+    packed, _ = _to_device(packed, dev, host)
+    scales, _ = _to_device(scales, dev, host)
+    offs, _ = _to_device(offs, dev, host)
     packed, scales = packed.contiguous(), scales.contiguous()
     offs = offs.to(torch.int32).contiguous()
     E, N, Kh = packed.shape
@@ -599,10 +606,10 @@ def nvfp4_w4a4_grouped_mm(x, packed, block_scales, w_global_scales, offs, out=No
         dev = x_quantized[0].device if isinstance(x_quantized[0], torch.Tensor) else None
         if dev is None or dev.type != "cuda":
             raise ValueError("nvfp4_w4a4_grouped_mm: x_quantized must hold CUDA tensors")
-    packed, _ = _to_device(packed, dev)
-    block_scales, _ = _to_device(block_scales, dev)
-    w_global_scales, _ = _to_device(w_global_scales, dev)
-    offs, _ = _to_device(offs, dev)
+    packed, _ = _to_device(packed, dev, host)
+    block_scales, _ = _to_device(block_scales, dev, host)
+    w_global_scales, _ = _to_device(w_global_scales, dev, host)
+    offs, _ = _to_device(offs, dev, host)
     packed, block_scales = packed.contiguous(), block_scales.contiguous()
     w_global_scales = w_global_scales.to(torch.float32).contiguous()
     offs = offs.to(torch.int32).contiguous()
@@ -693,8 +700,8 @@ def nvfp4_dequantize(packed, block_scales, global_scale, dtype=torch.bfloat16, o
                         "nvfp4_dequantize"):
             return ho
     packed, host = _to_device(packed)
-    block_scales, _ = _to_device(block_scales, packed.device)
-    global_scale, _ = _to_device(global_scale, packed.device)
+    block_scales, _ = _to_device(block_scales, packed.device, host)
+    global_scale, _ = _to_device(global_scale, packed.device, host)
     packed, block_scales = packed.contiguous(), block_scales.contiguous()
     global_scale = global_scale.to(torch.float32).contiguous()
     Kh = packed.shape[-1]

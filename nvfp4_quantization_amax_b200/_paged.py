@@ -26,7 +26,7 @@ def _ints(t, shape, dev, name):
     if t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, list(shape), list(t.shape)))
     if t.device != dev:
-        t, _ = _to_device(t, dev)
+        t, _ = _to_device(t, dev, False)
     return t if t.is_contiguous() else t.contiguous()
 
 
@@ -69,13 +69,14 @@ def _table(page_table, what):
     return page_table.shape
 
 
-def _rows(t, dev):
+def _rows(t, dev, waits=True):
     """(device tensor, elements between its rows, was on the host) of a tensor
     [rows, heads, channels] whose rows must be dense, the rows themselves at
-    any distance."""
+    any distance.  waits: whether the call waits for its results where this
+    one is on the host."""
     host = False
     if t.device != dev:
-        t, host = _to_device(t, dev)
+        t, host = _to_device(t, dev, waits)
     n, heads, dim = t.shape
     row = heads * dim
     if not t.is_contiguous():
@@ -147,10 +148,10 @@ def append_cache_paged(k, v, offs, page_table, lengths, k_cache, v_cache, format
     page_table = _ints(page_table, (n, M), dev, "page_table")
     lengths = _ints(lengths, (n,), dev, "lengths")
     offs = _ints(offs, (n,), dev, "offs")
-    k, k_stride, host = _rows(k, dev)
+    k, k_stride, host = _rows(k, dev, values)
     v_stride = 0
     if v is not None:
-        v, v_stride, _ = _rows(v, dev)
+        v, v_stride, _ = _rows(v, dev, values and host)
     T = k.shape[0]
     k_out = v_out = None
     if values:

@@ -11,6 +11,8 @@ from test_gpu_cache_paged import as_f64, check_attend, dev, queries
 
 pytestmark = pytest.mark.gpu
 
+DEV = "cuda"
+
 
 # ------------------------------------------------------------------ bounds
 
@@ -125,3 +127,98 @@ def test_keys_with_empty_blocks(fmt, block):
     codes[..., 3 * width:4 * width][live] = 0
     scales[..., 3] = torch.where(live, torch.tensor(1, dtype=torch.uint8), scales[..., 3])
     check_attend(cache, queries(3, 4, 64, torch.float32))
+
+
+# ---------------------------------------------------------- host arguments
+
+def busy():
+    """Work on the current stream that lasts about a tenth of a second."""
+    torch.cuda._sleep(200_000_000)
+
+
+def pinned(t):
+    return t.cpu().clone().pin_memory()
+
+
+def test_pinned_arguments_may_change_when_a_call_has_returned():
+    """What a call reads of pinned host tensors it has read when it returns,
+    or its results are on the host: the caller may write the next step's
+    values into them."""
+    cache = ref.Cache([40, 33], 2, 64, 16, "fp8", 64)
+    table, lengths = cache.table, cache.lengths
+    offs = torch.tensor([2, 3], dtype=torch.int32)
+    x = torch.randn(3, 2, 64).to(torch.bfloat16)
+    q, pages = queries(2, 4, 64, torch.bfloat16), torch.tensor([[[0, 2]] * 2, [[1, 2]] * 2]).int()
+    bd = torch.randn(cache.P, 2, 2, 64).to(torch.bfloat16)
+
+    def calls(k, v, host, x):
+        """One call of each kind with new copies of its arguments by `host`;
+        these are overwritten (with valid values) as soon as it returns."""
+        def args():
+            return host(table), host(lengths)
+
+        def gone(*ts):
+            for t in ts:
+                if not t.is_cuda:
+                    t.copy_(torch.where(t > 1, t - 1, t) if t.dtype == torch.int32 else t * 0 + 1)
+
+        out = []
+        t, n, o, new = *args(), host(offs), x(x0)
+        busy()
+        mxq.append_cache_paged(new, new, o, t, n, k, v, "fp8", 64)
+        gone(t, n, o, new)
+        out += [*k, *v]
+        t, n = args()
+        busy()
+        out.append(mxq.bound_cache_pages(k, t, n, "fp8", 64))
+        gone(t, n)
+        t, n = args()
+        busy()
+        out.append(mxq.select_cache_pages(dev(q), dev(bd), t, n, 16, 2))
+        gone(t, n)
+        t, n, p = *args(), host(pages)
+        busy()
+        out.append(mxq.attend_cache_paged(dev(q), k, v, t, n, "fp8", 64, pages=p))
+        gone(t, n, p)
+        torch.cuda.synchronize()
+        return [y.cpu() for y in out]
+
+    x0 = x
+    want = calls(dev(cache.k), dev(cache.v), dev, dev)
+    for move in (dev, pinned):  # the rows on the device, or pinned too
+        got = calls(dev(cache.k), dev(cache.v), pinned, move)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_pinned_offs_of_a_grouped_product_may_change_when_the_call_has_returned():
+    x = torch.randn(40, 512, device=DEV).to(torch.bfloat16)
+    packed, scales = mxq.mx_quantize(torch.randn(2, 256, 512, device=DEV).to(torch.bfloat16))
+    offs = torch.tensor([16, 40], dtype=torch.int32)
+    for product in (mxq.mxfp4_grouped_mm, mxq.w4a4_grouped_mm):
+        want = product(x, packed, scales, dev(offs))
+        host = pinned(offs)
+        busy()
+        got = product(x, packed, scales, host)
+        host.copy_(torch.tensor([1, 40]))
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
+def test_a_captured_call_reads_pinned_lengths_at_every_replay():
+    cache = ref.Cache([40, 33], 2, 64, 16, "fp8", 64)
+    k, v, q = dev(cache.k), dev(cache.v), dev(queries(2, 4, 64, torch.bfloat16))
+    host, table = pinned(cache.lengths), dev(cache.table)
+
+    def attend(lengths):
+        return mxq.attend_cache_paged(q, k, v, table, lengths, "fp8", 64)
+
+    attend(host)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = attend(host)
+    for lens in ([40, 33], [20, 10]):
+        host.copy_(torch.tensor(lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, attend(dev(host)))
