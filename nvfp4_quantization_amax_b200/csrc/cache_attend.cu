@@ -532,7 +532,8 @@ int launch_join(const Args& a, int dt, int grid, cudaStream_t st) {
   else if (a.c.dim <= 128) err = go(join_kernel<4, 1>);
   else if (a.c.dim <= 256) err = go(join_kernel<4, 2>);
   else err = go(join_kernel<4, 4>);
-  return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
+  const cudaError_t last = cudaGetLastError();  // reported here, whichever it is
+  return err == cudaSuccess && last == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
 
 template <int FMT>
@@ -637,9 +638,9 @@ int launch_attend_cache_paged(const void* q, int dt, int64_t q_heads, int64_t q_
   else if (c.fmt == MXQ_FMT_MXFP4) rc = launch_general<MXQ_FMT_MXFP4>(a, dt, grid, st);
   else rc = launch_general<MXQ_FMT_NVFP4>(a, dt, grid, st);
   if (rc != MXQ_OK) return rc;
+  if (cudaGetLastError() != cudaSuccess) return MXQ_ERR_CUDA;  // there are no parts to join
   // a span of one unit is never split
-  if (span <= kUnit) return cudaGetLastError() == cudaSuccess ? MXQ_OK : (int)MXQ_ERR_CUDA;
-  return launch_join(a, dt, grid, st);
+  return span <= kUnit ? (int)MXQ_OK : launch_join(a, dt, grid, st);
 }
 
 MXQ_DEFINE_CHECK_READER(check_record_cache_attend)

@@ -331,6 +331,7 @@ int launch_select_cache_pages(const void* q, int dt, int64_t q_heads, int64_t q_
     if (c.dim <= 128) launch_score<1>(a, dt, vec, grid, st);
     else if (c.dim <= 256) launch_score<2>(a, dt, vec, grid, st);
     else launch_score<4>(a, dt, vec, grid, st);
+    if (cudaGetLastError() != cudaSuccess) return MXQ_ERR_CUDA;  // there are no scores to choose by
     // launched with programmatic stream serialization: it looks up its
     // sequence while the scores' last blocks run
     cudaLaunchConfig_t cfg = {};

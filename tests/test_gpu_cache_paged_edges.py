@@ -1,6 +1,10 @@
 """The paged cache calls at their edges, against the plain 64-bit
 implementation, as test_gpu_cache_paged.py.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -12,6 +16,7 @@ from test_gpu_cache_paged import as_f64, check_attend, dev, queries
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 # ------------------------------------------------------------------ bounds
@@ -222,3 +227,53 @@ def test_a_captured_call_reads_pinned_lengths_at_every_replay():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, attend(dev(host)))
+
+
+# ------------------------------------------------------------ failed launches
+
+FAILED_LAUNCH = """
+import ctypes
+import torch
+import nvfp4_quantization_amax_b200 as mxq
+
+dev, n, H, D, S, P = "cuda", 1, 1, {dim}, {page}, 4
+cache = [torch.zeros(P, H, S, w, dtype=torch.uint8, device=dev) for w in (D, 1)]
+table = torch.arange(P, dtype=torch.int32, device=dev).view(n, P)
+lengths = torch.tensor([P * S], dtype=torch.int32, device=dev)
+q = torch.zeros(n, 2, D, dtype=torch.bfloat16, device=dev)
+out, ws = torch.empty_like(q), torch.empty(16 << 20, dtype=torch.uint8, device=dev)
+x = torch.randn(4, 64, device=dev).to(torch.bfloat16)
+
+def attend():
+    return mxq.attend_cache_paged(q, cache, cache, table, lengths, "fp8", D, out=out, workspace=ws)
+
+attend()
+want = mxq.quantize_cache(x, "fp8", 32)
+torch.cuda.synchronize()
+# while a stream that the legacy stream waits for is being captured, the
+# runtime refuses launches on the legacy stream: nothing of the call runs
+rt = ctypes.CDLL("libcudart.so.12")
+stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+assert rt.cudaStreamCreate(ctypes.byref(stream)) == 0
+assert rt.cudaStreamBeginCapture(stream, 0) == 0
+try:
+    attend()
+    failed = False
+except mxq.MxqError as e:
+    failed = e.status == -5
+rt.cudaStreamEndCapture(stream, ctypes.byref(graph))
+rt.cudaGetLastError()
+assert failed
+got = mxq.quantize_cache(x, "fp8", 32)  # the next call is not told of it
+attend()
+torch.cuda.synchronize()
+assert torch.equal(got, want) and not out.any()
+print("next call ok")
+"""
+
+
+@pytest.mark.parametrize("dim,page", [(128, 64), (40, 100)])
+def test_a_refused_launch_is_reported_once(dim, page):
+    r = subprocess.run([sys.executable, "-c", FAILED_LAUNCH.format(dim=dim, page=page)], cwd=ROOT,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "next call ok" in r.stdout, r.stdout + r.stderr
