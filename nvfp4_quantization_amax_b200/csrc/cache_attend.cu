@@ -288,24 +288,28 @@ attend_general_kernel(Args a, int dt, int pad) {
       float rf[2];  // V's exponent of tokens g and g + 8
 #pragma unroll
       for (int h = 0; h < 2; ++h) rf[h] = (float)(__shfl_sync(0xffffffffu, v_tops, g + 8 * h) - 127);
-      // ---- d = s - m, and the reference where one exceeds it by 2^4
-      float over = -1.0f;
+      // ---- d = s - m, and the reference where one exceeds it by 2^4: then the
+      // largest logit itself
+      float over = -1.0f, raw[4];  // s is raw times qf
+      auto dead = [&](int j) { return !(live_rows >> (j < 2 ? g : g + 8) & 1); };
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        d[j] = d[j] * qf[j & 1] - m[j & 1];
-        if (!(live_rows >> (j < 2 ? g : g + 8) & 1)) d[j] = none;
+        raw[j] = d[j];
+        d[j] = dead(j) ? none : fmaf(raw[j], qf[j & 1], -m[j & 1]);
         over = fmaxf(over, d[j]);
       }
       if (__any_sync(0xffffffffu, over > kLag || !have)) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float up = fmaxf(have ? 0.0f : none, fmaxf(d[j], d[j + 2]));
+          float top = have ? m[j] : none;
+          if (!dead(j)) top = fmaxf(top, raw[j] * qf[j]);
+          if (!dead(j + 2)) top = fmaxf(top, raw[j + 2] * qf[j]);
 #pragma unroll
-          for (int w = 4; w < 32; w <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, w));
-          m[j] += up;
-          if (have) l[j] *= ex2(-up);
-          d[j] -= up;
-          d[j + 2] -= up;
+          for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+          if (have) l[j] *= ex2(m[j] - top);
+          m[j] = top;
+          if (!dead(j)) d[j] = fmaf(raw[j], qf[j], -top);
+          if (!dead(j + 2)) d[j + 2] = fmaf(raw[j + 2], qf[j], -top);
         }
         have = true;
       }

@@ -447,14 +447,19 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
         }
       }
 
-      // ---- d = s - m; the reference moves where one exceeds it by 2^4
-      float over = -1.0f;
+      // ---- d = s - m; the reference moves where one exceeds it by 2^4, to the
+      // largest logit itself: m plus a difference would have lost the logits'
+      // bits where they lie far above m
+      float over = -1.0f, raw[U][NT][4];  // s is raw times qf
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) d[u][nt][j] = d[u][nt][j] * qf[nt][j & 1] - m[nt][j & 1];
+          for (int j = 0; j < 4; ++j) {
+            raw[u][nt][j] = d[u][nt][j];
+            d[u][nt][j] = fmaf(raw[u][nt][j], qf[nt][j & 1], -m[nt][j & 1]);
+          }
           if (part) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -468,22 +473,32 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float up = have ? 0.0f : none;
+            float top = have ? m[nt][j] : none;
 #pragma unroll
-            for (int u = 0; u < U; ++u) up = max3(up, d[u][nt][j], d[u][nt][j + 2]);
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int w = 4; w < 32; w <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, w));
-            m[nt][j] += up;
-            if (have) l[nt][j] *= ex2(-up);
-            if constexpr (T::kAbsolute) {
-              if (have) {
+              for (int h = 0; h < 2; ++h)
+                top = fmaxf(top, d[u][nt][j + 2 * h] == none ? none
+                                                             : raw[u][nt][j + 2 * h] * qf[nt][j]);
 #pragma unroll
-                for (int mt = 0; mt < T::MT; ++mt)
-                  o[mt][nt][j] *= ex2(-up), o[mt][nt][j + 2] *= ex2(-up);
+            for (int w = 4; w < 32; w <<= 1)
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+            if (have) {
+              const float f = ex2(m[nt][j] - top);
+              l[nt][j] *= f;
+              if constexpr (T::kAbsolute) {
+#pragma unroll
+                for (int mt = 0; mt < T::MT; ++mt) o[mt][nt][j] *= f, o[mt][nt][j + 2] *= f;
               }
             }
+            m[nt][j] = top;
 #pragma unroll
-            for (int u = 0; u < U; ++u) d[u][nt][j] -= up, d[u][nt][j + 2] -= up;
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                d[u][nt][j + 2 * h] = d[u][nt][j + 2 * h] == none
+                                          ? none - top  // NaN where there is nothing else
+                                          : fmaf(raw[u][nt][j + 2 * h], qf[nt][j], -top);
           }
         have = true;
       }

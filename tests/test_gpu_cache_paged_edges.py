@@ -134,6 +134,34 @@ def test_keys_with_empty_blocks(fmt, block):
     check_attend(cache, queries(3, 4, 64, torch.float32))
 
 
+@pytest.mark.parametrize("fmt,block,D,S", KERNELS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_first_logits_far_below_the_others(fmt, block, D, S, dtype):
+    """The first tokens' logits are lower than the others' by so much that a
+    difference from one of them has none of the others' bits.  Errors are
+    those of the tokens with weight: a logit's is relative to its own terms."""
+    far, n = 200, 700
+    cache = ref.Cache([n], 1, D, S, fmt, block, seed=3)
+    q = queries(1, 2, D, dtype)
+    q[0, 1] = q[0, 0] * 0.5
+    row = (q[0, 0].double() * (-400.0 if fmt == "nvfp4" else -2.0 ** 20)).to(torch.bfloat16)
+    codes, scales = ref.pack(row.view(1, D), fmt, block)
+    for t in range(far):
+        page = int(cache.table[0, t // S])
+        cache.k[0][page, 0, t % S], cache.k[1][page, 0, t % S] = codes[0], scales[0]
+    z = (cache.values(cache.k, 0, 0) @ q[0].double().numpy().T) / D ** 0.5
+    assert (z[:far].max(0) < z[far:].max(0) - (1000 if fmt == "nvfp4" else 10 ** 6)).all()
+    out, lse = mxq.attend_cache_paged(dev(q), dev(cache.k), dev(cache.v), dev(cache.table),
+                                      dev(cache.lengths), fmt, block, return_lse=True)
+    want, wl, spread, _ = ref.attend(cache, q)
+    k = np.abs(cache.values(cache.k, 0, 0)[far:])
+    reach = (k @ np.abs(q[0].double().numpy()).T).max(0)[None] / D ** 0.5
+    tol = ref.out_tolerance(dtype, D, n, want, spread, reach)
+    assert (np.abs(as_f64(out) - want) <= tol).all(), np.max(np.abs(as_f64(out) - want) / tol)
+    tol = ref.lse_tolerance(D, n, wl, reach)
+    assert (np.abs(as_f64(lse) - wl) <= tol).all(), np.max(np.abs(as_f64(lse) - wl) / tol)
+
+
 # ---------------------------------------------------------- host arguments
 
 def busy():
