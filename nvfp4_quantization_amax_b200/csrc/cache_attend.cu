@@ -196,7 +196,7 @@ attend_general_kernel(Args a, int dt, int pad) {
     }
     __syncthreads();
     const float qf[2] = {s_qf[2 * t4], s_qf[2 * t4 + 1]};
-    float o[MT][4], m[2] = {0.0f, 0.0f}, E[2] = {kLowest, kLowest}, l[2] = {0.0f, 0.0f};
+    float o[MT][4], minus[2] = {0.0f, 0.0f}, E[2] = {kLowest, kLowest}, l[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -289,35 +289,45 @@ attend_general_kernel(Args a, int dt, int pad) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) rf[h] = (float)(__shfl_sync(0xffffffffu, v_tops, g + 8 * h) - 127);
       // ---- d = s - m, and the reference where one exceeds it by 2^4: then the
-      // largest logit itself
+      // sum of the largest logit
       float over = -1.0f, raw[4];  // s is raw times qf
-      auto dead = [&](int j) { return !(live_rows >> (j < 2 ? g : g + 8) & 1); };
+#pragma unroll
+      for (int j = 0; j < 4; ++j) raw[j] = d[j];
+      minus_times2(d, raw, minus, qf);
+      minus_times2(d + 2, raw + 2, minus, qf);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        raw[j] = d[j];
-        d[j] = dead(j) ? none : fmaf(raw[j], qf[j & 1], -m[j & 1]);
+        if (!(live_rows >> (j < 2 ? g : g + 8) & 1)) d[j] = none;
         over = fmaxf(over, d[j]);
       }
       if (__any_sync(0xffffffffu, over > kLag || !have)) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float top = have ? m[j] : none;
-          if (!dead(j)) top = fmaxf(top, raw[j] * qf[j]);
-          if (!dead(j + 2)) top = fmaxf(top, raw[j + 2] * qf[j]);
+          const float sign = qf[j] < 0.0f ? -1.0f : 1.0f;
+          float top = have ? -sign * minus[j] : none;
+#pragma unroll
+          for (int h = 0; h < 4; h += 2)
+            top = fmaxf(top, d[j + h] == none ? none : sign * raw[j + h]);
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-          if (have) l[j] *= ex2(m[j] - top);
-          m[j] = top;
-          if (!dead(j)) d[j] = fmaf(raw[j], qf[j], -top);
-          if (!dead(j + 2)) d[j + 2] = fmaf(raw[j + 2], qf[j], -top);
+          const float to = -sign * top;
+          if (have) {
+            const float down = (to - minus[j]) * qf[j];
+            l[j] *= ex2(down);
+            E[j] = fmaxf(kLowest, E[j] + down);
+          }
+          minus[j] = to;
+#pragma unroll
+          for (int h = 0; h < 4; h += 2)
+            d[j + h] = d[j + h] == none ? none - top : (raw[j + h] + to) * qf[j];
         }
         have = true;
       }
-      // ---- weights times 2^(11 + r), x = s + r - E + 11
+      // ---- weights times 2^(11 + r), x = s - m + r - E + 11
       float x[4];
       auto relate = [&]() {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = d[j] + (rf[j >> 1] + ((m[j & 1] - E[j & 1]) + kWeightExp));
+        for (int j = 0; j < 4; ++j) x[j] = d[j] + (rf[j >> 1] + (kWeightExp - E[j & 1]));
         return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       };
       if (__any_sync(0xffffffffu, relate() > kWeightExp + kLag)) {
@@ -326,7 +336,7 @@ attend_general_kernel(Args a, int dt, int pad) {
           float e = fmaxf(kLowest, fmaxf(d[j] + rf[0], d[j + 2] + rf[1]));
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, w));
-          const float En = fmaxf(E[j], m[j] + e), fo = ex2(E[j] - En);
+          const float En = fmaxf(E[j], e), fo = ex2(E[j] - En);
 #pragma unroll
           for (int i = 0; i < MT; ++i) o[i][j] *= fo, o[i][j + 2] *= fo;
           E[j] = En;
@@ -373,7 +383,7 @@ attend_general_kernel(Args a, int dt, int pad) {
 #pragma unroll
       for (int w = 4; w < 32; w <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, w);
       if (g == 0) {
-        s_m[warp][2 * t4 + j] = m[j];
+        s_m[warp][2 * t4 + j] = -minus[j] * qf[j];
         s_e[warp][2 * t4 + j] = E[j];
         s_l[warp][2 * t4 + j] = lt;
       }
@@ -384,23 +394,27 @@ attend_general_kernel(Args a, int dt, int pad) {
       float top = kLowest, ref = kLowest, sum = 0.0f, val = 0.0f;
 #pragma unroll
       for (int w = 0; w < kTcWarps; ++w)
-        if (s_l[w][r] != 0.0f) top = fmaxf(top, s_m[w][r]), ref = fmaxf(ref, s_e[w][r]);
+        if (s_l[w][r] != 0.0f) top = fmaxf(top, s_m[w][r]);
+#pragma unroll
+      for (int w = 0; w < kTcWarps; ++w)
+        if (s_l[w][r] != 0.0f) ref = fmaxf(ref, s_e[w][r] + (s_m[w][r] - top));
 #pragma unroll
       for (int w = 0; w < kTcWarps; ++w) {
         if (s_l[w][r] == 0.0f) continue;  // no token
-        sum = fmaf(s_l[w][r], exp2f(s_m[w][r] - top), sum);
-        val = fmaf(sums[(w * 8 + r) * D + ch], exp2f(s_e[w][r] - ref), val);
+        const float m = s_m[w][r] - top;
+        sum = fmaf(s_l[w][r], exp2f(m), sum);
+        val = fmaf(sums[(w * 8 + r) * D + ch], exp2f(s_e[w][r] + m - ref), val);
       }
-      const float back = (ref - top) - kWeightExp - (float)OFF, half = truncf(back * 0.5f);
+      const float back = ref - kWeightExp - (float)OFF, half = truncf(back * 0.5f);
       put(a, dt, tg, r, ch, sum != 0.0f ? val / sum * exp2f(half) * exp2f(back - half) : 0.0f);
-      if (ch == 0) put_weight(a, tg, r, sum != 0.0f ? top + log2f(sum) : kLowest);
+      if (ch == 0) put_weight(a, tg, r, top, sum);
     }
     __syncthreads();  // the buffers are the next pair's
   });
 }
 
-// Join the parts of a split pair: out = sum_i o_i 2^(l_i - L), L = log2 sum
-// 2^l_i.  `per_head` warps share a head's parts (a power of two, set by how
+// Join the parts of a split pair: out = sum_i o_i w_i / sum_i w_i, w_i = l_i
+// 2^(m_i - the largest m).  `per_head` warps share a head's parts (a power of two, set by how
 // many there can be), lanes hold VEC channels at a time; the warps' sums are
 // added in a fixed order.  One block per (pair, some heads of the tile), which
 // finds the pair's parts among the slots, or, where there are more pairs than
@@ -459,7 +473,8 @@ join_kernel(Args a, int dt, int n_ctas, int per_head, bool by_pair) {
       }
     };
     auto add = [&](int i, float (*from)[VEC]) {
-      const float l = a.part_l[place(i)], f = l <= kLowest ? 0.0f : exp2f(l - top);
+      const float2 w = a.part_w[place(i)];
+      const float f = w.y != 0.0f ? w.y * exp2f(w.x - top) : 0.0f;
       sum += f;
 #pragma unroll
       for (int j = 0; j < NC; ++j)
@@ -467,7 +482,10 @@ join_kernel(Args a, int dt, int n_ctas, int per_head, bool by_pair) {
         for (int k = 0; k < VEC; ++k)
           if ((lane + 32 * j) * VEC < D) val[j][k] = fmaf(from[j][k], f, val[j][k]);
     };
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_l[place(i)]);
+    for (int i = lane; i < parts; i += 32) {
+      const float2 w = a.part_w[place(i)];
+      if (w.y != 0.0f) top = fmaxf(top, w.x);
+    }
 #pragma unroll
     for (int y = 0; y < AHEAD; ++y)
       if (share + y * per_head < parts) load(share + y * per_head, x[y]);
@@ -508,7 +526,7 @@ join_kernel(Args a, int dt, int n_ctas, int per_head, bool by_pair) {
       const int ch = (lane + 32 * j) * VEC + k;
       if (ch < D) put(a, dt, t, r, ch, val[j][k] * inv);
     }
-  if (lane == 0) put_weight(a, t, r, sum != 0.0f ? top + log2f(sum) : kLowest);
+  if (lane == 0) put_weight(a, t, r, top, sum);
 }
 
 // Launched with programmatic stream serialization: it takes its place while
@@ -599,7 +617,7 @@ int launch_tc_any(const Args& a, int dt, int64_t units, int* grid, cudaStream_t 
 uint64_t attend_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
   (void)q_heads, (void)kv_heads;
   const uint64_t slots = 2ull * attend::kCtasPerSm * (uint64_t)num_sms();
-  return (slots * 4 + 15) / 16 * 16 + slots * 16 * (uint64_t)(head_dim + 1) * 4;
+  return (slots * 4 + 15) / 16 * 16 + slots * 16 * (uint64_t)(head_dim + 2) * 4;
 }
 
 int launch_attend_cache_paged(const void* q, int dt, int64_t q_heads, int64_t q_stride,
@@ -623,8 +641,8 @@ int launch_attend_cache_paged(const void* q, int dt, int64_t q_heads, int64_t q_
   const int max_ctas = kCtasPerSm * num_sms();
   const int64_t slots = 2 * max_ctas;
   a.hdr = (int32_t*)workspace;
-  a.part_l = (float*)((char*)workspace + (slots * 4 + 15) / 16 * 16);
-  a.part_o = a.part_l + slots * 16;  // 16-byte aligned, as are its rows where dim % 4 == 0
+  a.part_w = (float2*)((char*)workspace + (slots * 4 + 15) / 16 * 16);
+  a.part_o = (float*)(a.part_w + slots * 16);  // 16-byte aligned, as are its rows where dim % 4 == 0
   // the tensor-core kernel carries 8 heads, or 16 where that does not overfill
   // its registers (one f16 term, up to 128 channels): K and V are read once
   // for all of a tile

@@ -7,8 +7,8 @@
 // the i-th n-th of the line: sequences of any lengths keep all SMs busy for
 // the same time, without a plan made on the host.  A block that holds all
 // units of a pair writes its output; where a pair's units fall to several
-// blocks, each writes a partial (the normalised sum in f32 and the logarithm
-// of its weight) to one of its two workspace slots: slot 2i for a pair that
+// blocks, each writes a partial (the normalised sum in f32 and its weight) to
+// one of its two workspace slots: slot 2i for a pair that
 // began in an earlier block, slot 2i + 1 for one that begins here.  A second,
 // small kernel joins them: the block after which a pair's first part lies
 // looks through the slots of the blocks behind it.
@@ -105,6 +105,19 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// y = (a - b) q of two columns, b negated; each operation rounded.
+__device__ __forceinline__ void minus_times2(float* y, const float* a, const float* minus_b,
+                                             const float* q) {
+  asm("{\n\t.reg .b64 a, b, q;\n\t"
+      "mov.b64 a, {%2, %3};\n\t"
+      "mov.b64 b, {%4, %5};\n\t"
+      "mov.b64 q, {%6, %7};\n\t"
+      "add.rn.f32x2 a, a, b;\n\t"
+      "mul.rn.f32x2 a, a, q;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(y[0]), "=f"(y[1])
+      : "f"(a[0]), "f"(a[1]), "f"(minus_b[0]), "f"(minus_b[1]), "f"(q[0]), "f"(q[1]));
+}
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) { return pack2<kF16>(lo, hi); }
 
 struct Args {
@@ -119,7 +132,7 @@ struct Args {
   void* out;
   float* lse;
   int32_t* hdr;   // [2 n_ctas] pair + 1, or 0
-  float* part_l;  // [2 n_ctas][tile_heads] log2 of the weight
+  float2* part_w;  // [2 n_ctas][tile_heads] weight: y times 2^x
   float* part_o;  // [2 n_ctas][tile_heads][dim]
 };
 
@@ -308,12 +321,17 @@ __device__ __forceinline__ void put(const Args& a, int dt, const Target& t, int 
     a.part_o[((int64_t)t.slot * a.tile_heads + r) * a.c.dim + ch] = v;
   }
 }
-__device__ __forceinline__ void put_weight(const Args& a, const Target& t, int r, float l2) {
+// sum times 2^top; a partial keeps the two apart, as their sum would lose the
+// first beside large logits.
+__device__ __forceinline__ void put_weight(const Args& a, const Target& t, int r, float top,
+                                           float sum) {
   if (t.whole) {
     const int64_t qh = (int64_t)t.head * a.group + t.tile * a.tile_heads + r;
-    if (a.lse) a.lse[t.b * a.q_heads + qh] = l2 <= kLowest ? __int_as_float(0xFF800000) : l2 * kLn2;
+    if (a.lse)
+      a.lse[t.b * a.q_heads + qh] =
+          sum == 0.0f ? __int_as_float(0xFF800000) : (top + log2f(sum)) * kLn2;
   } else {
-    a.part_l[(int64_t)t.slot * a.tile_heads + r] = l2;
+    a.part_w[(int64_t)t.slot * a.tile_heads + r] = make_float2(top, sum);
   }
 }
 

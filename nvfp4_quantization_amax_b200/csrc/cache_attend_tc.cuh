@@ -26,7 +26,8 @@
 //
 // Scales.  E8M0 scales (fp8, mxfp4) reach 2^+-127, beyond f16.  K: the sum over
 // each scale block is multiplied by its scale in f32.  V: an exponent r joins
-// the weight, 2^(s + r - E), with E the running largest of s + r: a token of
+// the weight, 2^(s - m + r - E), with E the running largest of s - m + r (held
+// from m on: beside logits of 2^28 the exponents would be lost): a token of
 // huge values and no weight costs no other token its bits.  With one scale a
 // row r is the token's.  With several it is the largest of the turn's tokens,
 // found by a lane looking at 1/32 of their scale bytes, and what is left of a
@@ -301,12 +302,12 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) qf[nt][j] = s_qf[nt * 8 + 2 * t4 + j];
 
-    // sums: l times 2^m, o times 2^(E - 11 - OFF)
-    float o[T::MT][NT][4], m[NT][2], E[NT][2], l[NT][2];
+    // sums: l times 2^m, o times 2^(m + E - 11 - OFF); m is -minus times qf
+    float o[T::MT][NT][4], minus[NT][2], E[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) m[nt][j] = 0.0f, E[nt][j] = kLowest, l[nt][j] = 0.0f;
+      for (int j = 0; j < 2; ++j) minus[nt][j] = 0.0f, E[nt][j] = kLowest, l[nt][j] = 0.0f;
 #pragma unroll
       for (int i = 0; i < T::MT; ++i)
 #pragma unroll
@@ -315,7 +316,7 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 
     constexpr uint32_t FULL = U == 2 ? 0x10001000u : 0x1000u;
     const float none = __int_as_float(0xFF800000);
-    bool have = false;  // whether a token has been seen: m and R are set
+    bool have = false;  // whether a token has been seen: m and E are set
     for (int i = 0; i < n; ++i) {
       cp_async_wait<T::STAGES - 2>();
       __syncwarp();
@@ -447,19 +448,18 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
         }
       }
 
-      // ---- d = s - m; the reference moves where one exceeds it by 2^4, to the
-      // largest logit itself: m plus a difference would have lost the logits'
-      // bits where they lie far above m
+      // ---- d = s - m, taken as the difference of the sums times qf: equal sums
+      // are 0 apart however large their logits.  The reference moves where one
+      // exceeds it by 2^4, to the sum of the largest
       float over = -1.0f, raw[U][NT][4];  // s is raw times qf
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            raw[u][nt][j] = d[u][nt][j];
-            d[u][nt][j] = fmaf(raw[u][nt][j], qf[nt][j & 1], -m[nt][j & 1]);
-          }
+          for (int j = 0; j < 4; ++j) raw[u][nt][j] = d[u][nt][j];
+          minus_times2(d[u][nt], raw[u][nt], minus[nt], qf[nt]);
+          minus_times2(d[u][nt] + 2, raw[u][nt] + 2, minus[nt], qf[nt]);
           if (part) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -473,32 +473,35 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float top = have ? m[nt][j] : none;
+            const float sign = qf[nt][j] < 0.0f ? -1.0f : 1.0f;
+            float top = have ? -sign * minus[nt][j] : none;
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                top = fmaxf(top, d[u][nt][j + 2 * h] == none ? none
-                                                             : raw[u][nt][j + 2 * h] * qf[nt][j]);
+                top = fmaxf(top,
+                            d[u][nt][j + 2 * h] == none ? none : sign * raw[u][nt][j + 2 * h]);
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1)
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+            const float to = -sign * top;
             if (have) {
-              const float f = ex2(m[nt][j] - top);
+              const float down = (to - minus[nt][j]) * qf[nt][j], f = ex2(down);
               l[nt][j] *= f;
+              E[nt][j] = fmaxf(kLowest, E[nt][j] + down);
               if constexpr (T::kAbsolute) {
 #pragma unroll
                 for (int mt = 0; mt < T::MT; ++mt) o[mt][nt][j] *= f, o[mt][nt][j + 2] *= f;
               }
             }
-            m[nt][j] = top;
+            minus[nt][j] = to;
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
                 d[u][nt][j + 2 * h] = d[u][nt][j + 2 * h] == none
                                           ? none - top  // NaN where there is nothing else
-                                          : fmaf(raw[u][nt][j + 2 * h], qf[nt][j], -top);
+                                          : (raw[u][nt][j + 2 * h] + to) * qf[nt][j];
           }
         have = true;
       }
@@ -569,7 +572,7 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
       }
 
       for (;;) {  // once, or once a band
-        // ---- weights times 2^(11 + r): x = s + r - E + 11
+        // ---- weights times 2^(11 + r): x = s - m + r - E + 11
         float x[U][NT][4];
         if constexpr (!T::kAbsolute) {
           auto relate = [&]() {
@@ -579,7 +582,7 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
               float c[2];
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                c[j] = (m[nt][j] - E[nt][j]) + (kWeightExp + (T::kRow ? 0.0f : (float)(r - 127)));
+                c[j] = (kWeightExp + (T::kRow ? 0.0f : (float)(r - 127))) - E[nt][j];
 #pragma unroll
               for (int u = 0; u < U; ++u) {
 #pragma unroll
@@ -613,7 +616,7 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 #pragma unroll
                 for (int w = 4; w < 32; w <<= 1)
                   e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, w));
-                const float En = fmaxf(E[nt][j], m[nt][j] + e), fo = ex2(E[nt][j] - En);
+                const float En = fmaxf(E[nt][j], e), fo = ex2(E[nt][j] - En);
 #pragma unroll
                 for (int mt = 0; mt < T::MT; ++mt) o[mt][nt][j] *= fo, o[mt][nt][j + 2] *= fo;
                 E[nt][j] = En;
@@ -761,16 +764,16 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, w);
         if (g == 0) {
-          s_m[warp][head] = m[nt][j];
-          s_r[warp][head] = T::kAbsolute ? m[nt][j] : E[nt][j];
+          s_m[warp][head] = -minus[nt][j] * qf[nt][j];
+          s_r[warp][head] = T::kAbsolute ? 0.0f : E[nt][j];
           s_l[warp][head] = lt;
         }
       }
     __syncthreads();
     const int heads = min(8 * NT, a.group - r0);
-    // a warp's factor 2^(E - ref); out = sum x 2^(ref - top - 11 -
-    // OFF) / l, the power in two steps.  A sum of 0 has seen no token; one that
-    // is not a number (of a logit that is none) stays so
+    // a warp's factor 2^(m - top + E - ref); out = sum x 2^(ref - 11 - OFF) / l,
+    // the power in two steps.  A sum of 0 has seen no token; one that is not a
+    // number (of a logit that is none) stays so
     const int fw = threadIdx.x / (8 * NT), fr = threadIdx.x % (8 * NT);
     if (fw < kTcWarps) {
       float top = kLowest, ref = kLowest, sum = 0.0f;
@@ -779,16 +782,17 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
         if (s_l[w][fr] != 0.0f) top = fmaxf(top, s_m[w][fr]);
 #pragma unroll
       for (int w = 0; w < kTcWarps; ++w)
-        if (s_l[w][fr] != 0.0f) ref = fmaxf(ref, s_r[w][fr]);
+        if (s_l[w][fr] != 0.0f) ref = fmaxf(ref, s_r[w][fr] + (s_m[w][fr] - top));
 #pragma unroll
       for (int w = 0; w < kTcWarps; ++w)
         if (s_l[w][fr] != 0.0f) sum = fmaf(s_l[w][fr], exp2f(s_m[w][fr] - top), sum);
-      s_f[fw][fr] = s_l[fw][fr] != 0.0f ? exp2f(s_r[fw][fr] - ref) : 0.0f;
+      s_f[fw][fr] =
+          s_l[fw][fr] != 0.0f ? exp2f(s_r[fw][fr] + (s_m[fw][fr] - top) - ref) : 0.0f;
       if (fw == 0 && fr < heads) {
-        const float back = (ref - top) - kWeightExp - (float)T::OFF, half = truncf(back * 0.5f);
+        const float back = ref - kWeightExp - (float)T::OFF, half = truncf(back * 0.5f);
         s_back[0][fr] = sum != 0.0f ? exp2f(half) / sum : 0.0f;
         s_back[1][fr] = sum != 0.0f ? exp2f(back - half) : 0.0f;
-        put_weight(a, tg, fr, sum != 0.0f ? top + log2f(sum) : kLowest);
+        put_weight(a, tg, fr, top, sum);
       }
     }
     __syncthreads();

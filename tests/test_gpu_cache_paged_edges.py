@@ -162,6 +162,31 @@ def test_first_logits_far_below_the_others(fmt, block, D, S, dtype):
     assert (np.abs(as_f64(lse) - wl) <= tol).all(), np.max(np.abs(as_f64(lse) - wl) / tol)
 
 
+@pytest.mark.parametrize("fmt,block,D,S", [x for x in KERNELS if x[0] != "nvfp4"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_logits_so_large_that_a_scale_is_lost_beside_them(fmt, block, D, S, dtype):
+    """Logits of up to 2^100, exact ones (a query that is one channel): the
+    weights are those of the tokens with the largest, each 1, whatever the
+    values' scales; no error of a logit counts."""
+    for by, by_v in ((20, 8), (30, 8), (30, -20), (100, 8),
+                     (100, 10 if dtype == torch.float16 else 40)):
+        lens = [0, 300, 21]
+        cache = ref.Cache(lens, 1, D, S, fmt, block, seed=by + D)
+        for which, add in ((cache.k, by), (cache.v, by_v)):
+            which[1][:] = torch.where(which[1] == 0xFF, which[1], (which[1] + add).to(torch.uint8))
+        q = torch.zeros(3, 2, D, dtype=dtype)
+        q[:, 0, 3], q[:, 1, 2] = 1.0, -2.0
+        out, lse = mxq.attend_cache_paged(dev(q), dev(cache.k), dev(cache.v), dev(cache.table),
+                                          dev(cache.lengths), fmt, block, scale=1.0,
+                                          return_lse=True)
+        want, wl, spread, reach = ref.attend(cache, q, scale=1.0)
+        tol = ref.out_tolerance(dtype, D, 300, want, spread, 0 * reach)
+        assert (np.abs(as_f64(out) - want) <= tol).all(), (by, by_v)
+        tol = ref.lse_tolerance(D, 300, wl, 0 * reach)
+        assert (np.abs(as_f64(lse)[1:] - wl[1:]) <= tol[1:]).all(), (by, by_v)
+        assert not out[0].any() and torch.isneginf(lse[0]).all()
+
+
 # ---------------------------------------------------------- host arguments
 
 def busy():
