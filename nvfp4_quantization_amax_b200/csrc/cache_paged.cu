@@ -66,7 +66,7 @@ __device__ __forceinline__ int sequence_of(const AppendArgs& a, int64_t t, int f
   while (step <= n - lo && __ldg(a.offs + lo + step - 1) <= t) lo += step, step *= 2;
   int hi = lo + min(step - 1, n - lo);
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
+    const int mid = lo + ((hi - lo) >> 1);  // there may be 2^31 - 2 sequences
     if (__ldg(a.offs + mid) > t) hi = mid;
     else lo = mid + 1;
   }
@@ -75,16 +75,16 @@ __device__ __forceinline__ int sequence_of(const AppendArgs& a, int64_t t, int f
 // The same from 0 by a warp, which looks at 32 places at a time: a block has
 // few tokens, and the loads that wait for one another are what a search costs.
 __device__ __forceinline__ int sequence_of_by_warp(const AppendArgs& a, int64_t t, int lane) {
-  int lo = 0, hi = (int)a.c.n_seqs;  // lo <= b <= hi
+  uint32_t lo = 0, hi = (uint32_t)a.c.n_seqs;  // lo <= b <= hi; places up to hi + 30 are formed
   while (lo < hi) {
-    const int step = (hi - lo + 31) / 32;  // a lane: the last of its `step` sequences
-    const int mid = min(lo + lane * step + step - 1, hi - 1);
+    const uint32_t step = (hi - lo + 31) / 32;  // a lane: the last of its `step` sequences
+    const uint32_t mid = min(lo + lane * step + step - 1, hi - 1);
     const uint32_t over = __ballot_sync(0xffffffffu, __ldg(a.offs + mid) > t);
-    if (over == 0) return hi;
+    if (over == 0) return (int)hi;
     lo += (__ffs(over) - 1) * step;
     hi = min(lo + step - 1, hi - 1);
   }
-  return lo;
+  return (int)lo;
 }
 
 // Block 0 looks over the whole of offs: a sequence whose end lies before its

@@ -330,3 +330,31 @@ def test_a_refused_launch_is_reported_once(dim, page):
     r = subprocess.run([sys.executable, "-c", FAILED_LAUNCH.format(dim=dim, page=page)], cwd=ROOT,
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "next call ok" in r.stdout, r.stdout + r.stderr
+
+
+# ------------------------------------------------------ very many sequences
+
+@pytest.mark.parametrize("block", [64, 4])  # the fast and the general kernel
+def test_append_to_as_many_sequences_as_are_counted(block):
+    # 2^31 - 2 sequences, three of which own a row: places of the searches pass
+    # 31 bits
+    n, D, S = 2 ** 31 - 2, 64, 16
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of free device memory")
+    owners = [0, 2 ** 30 + 5, n - 1]
+    offs, lengths = [torch.zeros(n, dtype=torch.int32, device=DEV) for _ in range(2)]
+    table = torch.zeros(n, 1, dtype=torch.int32, device=DEV)
+    for i, b in enumerate(owners):
+        offs[b:] = i + 1
+        lengths[b], table[b, 0] = i + 1, i + 1
+    cache = tuple(torch.full((5, 1, S, w), 0xAA, dtype=torch.uint8, device=DEV)
+                  for w in (D, D // block))
+    x = torch.randn(4, 1, D, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    mxq.append_cache_paged(dev(x), None, offs, table, lengths, cache, None, "fp8", block)
+    want = [torch.full_like(t, 0xAA, device="cpu") for t in cache]
+    for w, rows in zip(want, ref.pack(x, "fp8", block)):
+        for i in range(3):  # the fourth row is padding
+            w[i + 1, :, i] = rows[i]
+    for got, w in zip(cache, want):
+        assert torch.equal(got.cpu(), w)
