@@ -332,6 +332,30 @@ def test_a_refused_launch_is_reported_once(dim, page):
     assert r.returncode == 0 and "next call ok" in r.stdout, r.stdout + r.stderr
 
 
+# ------------------------------------------------------------ bad offs
+
+def test_bad_offs_touch_no_slot_outside_the_sequences():
+    rng = np.random.default_rng(4)
+    few = [[2, 1, 6], [5, 3, 6], [6, 0, 2], [-1, 2, 6], [2, 4, 100], [3, 3, -2],
+           [2 ** 31 - 1, 2, 4], [-2 ** 31, -2 ** 31, 6]]
+    for lens, all_offs in (([20, 30, 8], few),
+                           ([1 + i % 40 for i in range(90)],
+                            [rng.integers(-3, 10, 90).tolist() for _ in range(4)])):
+        for block in (32, 4):  # the fast and the general kernel
+            for offs in all_offs:
+                cache = ref.Cache(lens, 2, 64, 16, "fp8", block, empty=True)
+                kc = dev(cache.k)
+                status = torch.zeros(1, dtype=torch.int32, device=DEV)
+                x = torch.randn(6, 2, 64).to(torch.bfloat16)
+                mxq.append_cache_paged(dev(x), None, dev(torch.tensor(offs, dtype=torch.int32)),
+                                       dev(cache.table), dev(cache.lengths), kc, None, "fp8", block,
+                                       status=status)
+                assert int(status) in (-6, -8)
+                for got, was in zip(kc, cache.k):
+                    free = ~cache.held[:, None].expand(-1, 2, -1)
+                    assert torch.equal(got.cpu()[free], was[free])
+
+
 # ------------------------------------------------------ very many sequences
 
 @pytest.mark.parametrize("block", [64, 4])  # the fast and the general kernel
