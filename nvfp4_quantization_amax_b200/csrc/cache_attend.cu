@@ -231,7 +231,8 @@ attend_general_kernel(Args a, int dt, int pad) {
 #pragma unroll
           for (int y = 0; y < AT_ONCE; ++y) {
             const int64_t at = __shfl_sync(0xffffffffu, row, y0 + y);
-            if (at >= 0) x[y].load(codes + at * rb, scales + at * nb, lane, D, c.block, my_scale);
+            if (at >= 0 && MXQ_IN_RANGE(kChkAttendScale, at * nb + my_scale, n_rows * nb))
+              x[y].load(codes + at * rb, scales + at * nb, lane, D, c.block, my_scale);
           }
 #pragma unroll
           for (int y = 0; y < AT_ONCE; ++y) {
@@ -450,8 +451,10 @@ join_kernel(Args a, int dt, int n_ctas, int per_head, bool by_pair) {
   t.slot = 0;
   const int r = (blockIdx.y * kWarps + warp) / per_head, share = warp & (per_head - 1);
   const bool have = r < min(a.tile_heads, a.group - t.tile * a.tile_heads);
+  // the part's place in the workspace; one past the last slot reads the first
   auto place = [&](int i) {
-    return (int64_t)(i == 0 ? 2 * cta + 1 : 2 * (cta + i)) * a.tile_heads + r;
+    const int64_t at = (int64_t)(i == 0 ? 2 * cta + 1 : 2 * (cta + i)) * a.tile_heads + r;
+    return MXQ_IN_RANGE(kChkAttendWs, at, 2ll * n_ctas * a.tile_heads) ? at : (int64_t)0;
   };
   float top = kLowest, sum = 0.0f, val[NC][VEC];
 #pragma unroll

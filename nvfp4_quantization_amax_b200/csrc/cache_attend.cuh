@@ -145,7 +145,7 @@ struct Span {
 
 __device__ __forceinline__ Span span_of(const Args& a, int64_t b) {
   Span s;
-  s.len = __ldg(a.c.lengths + b);
+  s.len = MXQ_IN_RANGE(kChkAttendTable, b, a.c.n_seqs) ? __ldg(a.c.lengths + b) : 0;
   if (s.len < 0 || s.len > a.c.max_pages * a.c.page) {
     if (a.c.status) *a.c.status = MXQ_ERR_BAD_PAGE;
     s.len = 0;
@@ -205,7 +205,15 @@ __device__ __forceinline__ bool live(const Args& a, const Span& s, int64_t pos) 
   return pos >= 0 && pos < s.len && (a.window == 0 || pos >= s.len - a.window);
 }
 
+// Whether elements [i, i + n) are a query's.
+__device__ __forceinline__ bool is_q(const Args& a, int64_t i, int n) {
+  [[maybe_unused]] const int64_t all =
+      (a.c.n_seqs - 1) * a.q_stride + (int64_t)a.q_heads * a.c.dim;
+  return MXQ_IN_RANGE(kChkAttendQuery, i, all) && MXQ_IN_RANGE(kChkAttendQuery, i + n - 1, all);
+}
+
 __device__ __forceinline__ float load_q(const Args& a, int dt, int64_t i) {
+  if (!is_q(a, i, 1)) return 0.0f;
   if (dt == kBF16) return elem_to_f32<kBF16>(((const uint16_t*)a.q)[i]);
   if (dt == kF16) return elem_to_f32<kF16>(((const uint16_t*)a.q)[i]);
   return ((const float*)a.q)[i];
@@ -318,7 +326,8 @@ __device__ __forceinline__ void put(const Args& a, int dt, const Target& t, int 
     const int64_t i = (t.b * a.q_heads + qh) * a.c.dim + ch;
     if (MXQ_IN_RANGE(kChkAttendOut, i, a.c.n_seqs * a.q_heads * a.c.dim)) store_out(a, dt, i, v);
   } else {
-    a.part_o[((int64_t)t.slot * a.tile_heads + r) * a.c.dim + ch] = v;
+    const int64_t i = ((int64_t)t.slot * a.tile_heads + r) * a.c.dim + ch;
+    if (MXQ_IN_RANGE(kChkAttendWs, i, 2ll * gridDim.x * a.tile_heads * a.c.dim)) a.part_o[i] = v;
   }
 }
 // sum times 2^top; a partial keeps the two apart, as their sum would lose the
@@ -327,11 +336,13 @@ __device__ __forceinline__ void put_weight(const Args& a, const Target& t, int r
                                            float sum) {
   if (t.whole) {
     const int64_t qh = (int64_t)t.head * a.group + t.tile * a.tile_heads + r;
-    if (a.lse)
+    if (a.lse && MXQ_IN_RANGE(kChkAttendOut, t.b * a.q_heads + qh, a.c.n_seqs * a.q_heads))
       a.lse[t.b * a.q_heads + qh] =
           sum == 0.0f ? __int_as_float(0xFF800000) : (top + log2f(sum)) * kLn2;
   } else {
-    a.part_w[(int64_t)t.slot * a.tile_heads + r] = make_float2(top, sum);
+    const int64_t i = (int64_t)t.slot * a.tile_heads + r;
+    if (MXQ_IN_RANGE(kChkAttendWs, i, 2ll * gridDim.x * a.tile_heads))
+      a.part_w[i] = make_float2(top, sum);
   }
 }
 

@@ -244,7 +244,9 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
     if (q_mine && q_wide) {
 #pragma unroll
       for (int k = 0; k < T::KS; ++k)
-        q_raw[k] = __ldg((const uint2*)((const uint16_t*)a.q + q_from + q_channel(k)));
+        q_raw[k] = is_q(a, q_from + q_channel(k), 4)
+                       ? __ldg((const uint2*)((const uint16_t*)a.q + q_from + q_channel(k)))
+                       : make_uint2(0u, 0u);
     }
 #pragma unroll
     for (int i = 0; i < T::STAGES - 1; ++i) issue(i);

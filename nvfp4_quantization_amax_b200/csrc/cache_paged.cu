@@ -37,7 +37,7 @@ struct AppendArgs {
 // offs lies above t), or -1: padding, or a row whose position or page is out of
 // range (reported).  The rows of the other heads lie S apart.
 __device__ __forceinline__ int64_t row_of(const AppendArgs& a, int64_t t, int b) {
-  if (b == a.c.n_seqs) return -1;
+  if (b == a.c.n_seqs || !MXQ_IN_RANGE(kChkAppendTable, b, a.c.n_seqs)) return -1;
   const int64_t end = __ldg(a.offs + b), begin = b > 0 ? __ldg(a.offs + b - 1) : 0;
   const int64_t len = __ldg(a.c.lengths + b), pos = len - (end - t);
   if (begin < 0 || begin > t || end > a.rows) {
@@ -49,7 +49,8 @@ __device__ __forceinline__ int64_t row_of(const AppendArgs& a, int64_t t, int b)
   if (pos >= 0 && len <= a.c.max_pages * a.c.page) {  // positions end at 2^30
     const uint32_t j = (uint32_t)pos / (uint32_t)a.c.page;
     at = (uint32_t)pos - j * (uint32_t)a.c.page;
-    page = __ldg(a.c.page_table + b * a.c.max_pages + j);
+    if (MXQ_IN_RANGE(kChkAppendTable, j, a.c.max_pages))
+      page = __ldg(a.c.page_table + b * a.c.max_pages + j);
   }
   if (page < 0 || page >= a.c.num_pages) {
     if (a.c.status) *a.c.status = MXQ_ERR_BAD_PAGE;
@@ -157,7 +158,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, AppendPl
       const uint32_t item = base + u * kThreads + lane;
       if (item >= n_items) continue;
       const uint32_t tok = plan.per_tok.div(item), rem = item - tok * plan.per_tok.d;
-      if (!MXQ_IN_RANGE(kChkAppendIn, t0 + tok, a.rows)) continue;
+      if (!MXQ_IN_RANGE(kChkAppendIn, t0 + tok, a.rows) ||
+          !MXQ_IN_RANGE(kChkAppendIn, rem, plan.per_tok.d))
+        continue;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (s == 1 && !a.v) break;
@@ -256,7 +259,12 @@ __global__ void __launch_bounds__(kThreads) append_general_kernel(AppendArgs a) 
     const int64_t dense = (t * c.heads + head) * c.dim + g * B;
     uint8_t* codes = (is_v ? c.v_codes : c.k_codes) + row * rb;
     void* out = is_v ? a.v_out : a.k_out;
-    if (!MXQ_IN_RANGE(kChkAppendIn, t, a.rows) || !MXQ_IN_RANGE(kChkAppendOut, row, n_rows))
+    if (!MXQ_IN_RANGE(kChkAppendIn, t, a.rows) || !MXQ_IN_RANGE(kChkAppendOut, row, n_rows) ||
+        !MXQ_IN_RANGE(kChkAppendScale, row * nb + g, n_rows * nb) ||
+        !MXQ_IN_RANGE(kChkAppendIn, head * c.dim + g * B + B - 1, c.heads * c.dim) ||
+        !MXQ_IN_RANGE(kChkAppendOut, row * rb + (FMT == MXQ_FMT_FP8 ? g * B + B : (g + 1) * B / 2) - 1,
+                      n_rows * rb) ||
+        !MXQ_IN_RANGE(kChkAppendOut, dense + B - 1, a.rows * c.heads * c.dim))
       continue;
     uint32_t m = 0;
     for (int j = 0; j < B; ++j) m = max(m, mag_as_f32_bits<DT>(elem_bits_at<DT>(in, src + j)));
@@ -382,6 +390,7 @@ __global__ void __launch_bounds__(kBoundThreads) bound_kernel(BoundArgs a) {
   const int n_pages = ((uint32_t)len + c.page - 1) / (uint32_t)c.page;
   const int j = n_pages - 1 - (int)(blockIdx.x * (kBoundThreads / 32) + (threadIdx.x >> 5));
   if (j < 0 || (int64_t)(j + 1) * c.page <= len - a.new_tokens) return;
+  if (!MXQ_IN_RANGE(kChkBoundTable, j, c.max_pages)) return;
   const int64_t page = c.page_table[b * c.max_pages + j];
   if (page < 0 || page >= c.num_pages) {
     if (c.status) *c.status = MXQ_ERR_BAD_PAGE;
@@ -412,7 +421,9 @@ __global__ void __launch_bounds__(kBoundThreads) bound_kernel(BoundArgs a) {
           const uint8_t* ps = scales + (uint32_t)(s * nb) + sb;
           // past the end: the batch's first row again, which changes no bound
           const int left = (rows - s + at_once - 1) / at_once;
-          if (!MXQ_IN_RANGE(kChkBoundIn, row0 + s + (min(left, UNROLL) - 1) * at_once, n_rows))
+          [[maybe_unused]] const int64_t last = row0 + s + (min(left, UNROLL) - 1) * at_once;
+          if (!MXQ_IN_RANGE(kChkBoundIn, last * rb + (cv + 1) * (WORDS * 4) - 1, n_rows * rb) ||
+              !MXQ_IN_RANGE(kChkBoundScale, last * nb + sb, n_rows * nb))
             break;
 #pragma unroll
           for (int u = 0; u < UNROLL; ++u) {
@@ -455,7 +466,8 @@ __global__ void __launch_bounds__(kBoundThreads) bound_kernel(BoundArgs a) {
           if (r == 0) lo[i] = fminf(lo[i], l), hi[i] = fmaxf(hi[i], h);
         }
       }
-      if (r == 0 && MXQ_IN_RANGE(kChkBoundOut, page, c.num_pages)) {
+      if (r == 0 && MXQ_IN_RANGE(kChkBoundOut, page, c.num_pages) &&
+          MXQ_IN_RANGE(kChkBoundOut, cv * VEC + VEC - 1, c.dim)) {
 #pragma unroll
         for (int x = 0; x < VEC / 8; ++x) {
           store8<kBF16>(out + cv * VEC + 8 * x, 0, lo + 8 * x);
@@ -467,11 +479,14 @@ __global__ void __launch_bounds__(kBoundThreads) bound_kernel(BoundArgs a) {
     for (int ch = lane; ch < c.dim; ch += 32) {
       float lo = inf, hi = -inf;
       for (int s = 0; s < rows; ++s) {
-        if (!MXQ_IN_RANGE(kChkBoundIn, row0 + s, n_rows)) continue;
+        if (!MXQ_IN_RANGE(kChkBoundIn, row0 + s, n_rows) ||
+            !MXQ_IN_RANGE(kChkBoundScale, ch / c.block, nb))
+          continue;
         const float v = value_at<FMT>(codes + (int64_t)s * rb, scales + (int64_t)s * nb, ch, c.block);
         lo = fminf(lo, v);
         hi = fmaxf(hi, v);
       }
+      if (!MXQ_IN_RANGE(kChkBoundOut, page, c.num_pages)) continue;
       out[ch] = (uint16_t)(pack2<kBF16>(lo, 0.0f) & 0xFFFFu);
       out[c.dim + ch] = (uint16_t)(pack2<kBF16>(hi, 0.0f) & 0xFFFFu);
     }

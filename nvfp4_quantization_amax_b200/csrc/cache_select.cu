@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(kThreads) score_kernel(SelectArgs a, int dt) {
   [[maybe_unused]] const int64_t n_bounds = c.num_pages * c.heads;
   const int p0 = (blockIdx.x * kWarps + warp) * kPagesPerWarp;
   int mine = -1;  // the page of p0 + lane, or -1
-  if (lane < kPagesPerWarp && p0 + lane < n) {
+  if (lane < kPagesPerWarp && p0 + lane < n &&
+      MXQ_IN_RANGE(kChkSelectTable, p0 + lane, c.max_pages)) {
     mine = __ldg(c.page_table + b * c.max_pages + p0 + lane);
     if (mine < 0 || mine >= c.num_pages) {
       mine = -1;
@@ -116,6 +117,9 @@ __global__ void __launch_bounds__(kThreads) score_kernel(SelectArgs a, int dt) {
     const int64_t at = b * a.q_stride + (int64_t)head * a.group * D + ch;
 #pragma unroll 4
     for (int g = 0; g < a.group; ++g) {
+      if (!MXQ_IN_RANGE(kChkSelectQuery, at + (int64_t)g * D,
+                        (c.n_seqs - 1) * a.q_stride + (int64_t)c.heads * a.group * D))
+        continue;
       const double x = (double)q_at(a.q, dt, at + (int64_t)g * D);
       neg += x < 0.0 ? x : 0.0;
       pos += x < 0.0 ? 0.0 : x;
@@ -196,14 +200,17 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
   const int p0 = min(n, (int)threadIdx.x * per), p1 = min(n, p0 + per);
   uint64_t k8[kHeld];
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) k8[i] = held && p0 + i < p1 ? keys[p0 + i] : 0ull;
+  for (int i = 0; i < kHeld; ++i)
+    k8[i] = held && p0 + i < p1 && MXQ_IN_RANGE(kChkSelectWs, p0 + i, c.max_pages) ? keys[p0 + i]
+                                                                                   : 0ull;
   auto each = [&](auto f) {  // f(place, key) of this thread's places in order
     if (held) {
 #pragma unroll
       for (int i = 0; i < kHeld; ++i)
         if (p0 + i < p1) f(p0 + i, k8[i]);
     } else {
-      for (int p = p0; p < p1; ++p) f(p, keys[p]);
+      for (int p = p0; p < p1; ++p)
+        if (MXQ_IN_RANGE(kChkSelectWs, p, c.max_pages)) f(p, keys[p]);
     }
   };
   // the bits in which the scored keys differ, and how many pages are kept anyway

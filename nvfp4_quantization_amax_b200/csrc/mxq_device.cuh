@@ -49,6 +49,7 @@ enum MxqCheckId {
   kChkAppendIn, kChkAppendOut, kChkAppendScale, kChkBoundIn, kChkBoundScale, kChkBoundOut,
   kChkSelectIn, kChkSelectWs, kChkSelectOut,
   kChkAttendIn, kChkAttendScale, kChkAttendOut, kChkAttendWs, kChkAttendTable,
+  kChkAppendTable, kChkBoundTable, kChkSelectTable, kChkSelectQuery, kChkAttendQuery,
   kChkSelfTest = 99
 };
 

@@ -382,3 +382,17 @@ def test_append_to_as_many_sequences_as_are_counted(block):
             w[i + 1, :, i] = rows[i]
     for got, w in zip(cache, want):
         assert torch.equal(got.cpu(), w)
+
+
+# ------------------------------------------------------------ index checks
+
+def test_debug_variant_without_a_failed_check():
+    """The cases above on the library's debug variant, whose kernels check
+    their indexes (tests/conftest.py asks for its record after each)."""
+    from nvfp4_quantization_amax_b200 import build
+
+    env = dict(os.environ, MXQ_LIBRARY=build.build(debug=True), MXQ_EXPECT_CLEAN_CHECKS="1")
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-p", "no:cacheprovider", "-m", "gpu",
+                        "-k", "not debug_variant", os.path.abspath(__file__)],
+                       cwd=ROOT, env=env, capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0 and " passed" in r.stdout, r.stdout[-3000:] + r.stderr[-1000:]
