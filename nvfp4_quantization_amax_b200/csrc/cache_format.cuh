@@ -104,22 +104,22 @@ __device__ __forceinline__ void decode_word(uint32_t w, uint32_t* r) {
   }
 }
 
-// The codes and their values as f16 pairs.  Each conversion back takes the
-// byte that its conversion made: decode_word on a word that e2m1x8 has just
-// packed gave zeros for the upper bytes (nvcc 12.9), so decode_word is for
-// words read from memory.
+// The codes and their values as f16 pairs.  Each conversion back takes what its
+// conversion made, inside one asm for fp4: unpacking the four bytes of a word
+// that e2m1x8 had just packed from four .b8 registers gave zeros for the upper
+// bytes (nvcc 12.9; the reason is not known).  decode_word takes words that were
+// read from memory or made by operations on whole registers.
 template <int FMT>
 __device__ __forceinline__ uint2 encode8(const float* x, float inv, uint32_t* h) {
-  if constexpr (FMT == MXQ_FMT_FP8) {
-    const uint2 c = encode8<FMT>(x, inv);
-    decode_word<FMT>(c.x, h);
-    decode_word<FMT>(c.y, h + 2);
-    return c;
-  } else {
-    uint32_t b[4];
+  uint32_t b[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float v0, v1;
+  for (int j = 0; j < 4; ++j) {
+    float v0, v1;
+    if constexpr (FMT == MXQ_FMT_FP8) {
+      mul2_rn(v0, v1, x[2 * j], x[2 * j + 1], inv, inv);
+      b[j] = e4m3x2(v0, v1);
+      h[j] = e4m3x2_to_f16x2(b[j]);
+    } else {
       fma2_rn_zero(v0, v1, x[2 * j], x[2 * j + 1], inv, inv);
       asm("{\n\t.reg .b8 t;\n\t"
           "cvt.rn.satfinite.e2m1x2.f32 t, %3, %2;\n\t"
@@ -128,8 +128,11 @@ __device__ __forceinline__ uint2 encode8(const float* x, float inv, uint32_t* h)
           : "=r"(b[j]), "=r"(h[j])
           : "f"(v0), "f"(v1));
     }
-    return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, 0u);
   }
+  if constexpr (FMT == MXQ_FMT_FP8)
+    return make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+  else
+    return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, 0u);
 }
 
 // Eight decoded values, f16 code values (pairs) times the scale, exact in f32.
