@@ -21,6 +21,8 @@
 //   scale), quantize_cache, _power_of_two_ceiling.
 //  "nemo_automodel.components.quantization.mxfp4": module docstring (low
 //   nibble = even column).
+#include <type_traits>
+
 #include "cache_format.cuh"
 #include "mxq.h"
 #include "mxq_device.cuh"
@@ -39,18 +41,23 @@ pack_cache_kernel(const void* __restrict__ in, void* __restrict__ codes,
                   uint8_t* __restrict__ scales, int64_t n_items) {
   const int lane = threadIdx.x & 31;
   const int64_t stride = (int64_t)gridDim.x * kThreads;
-  for (int64_t base = (int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31); base < n_items;
-       base += stride * kUnroll) {
+  // The items of a turn: all of them there, whose loads then go out together, or
+  // only some (loads that may be left out were not all issued before the first
+  // result: 524288 rows of 512 in bf16, fp8/128 183 us against 149 so, mxfp4
+  // 140 against 129, nvfp4 144 against 134).
+  auto turn = [&](auto all, int64_t base) {
+    constexpr bool ALL = decltype(all)::value;
     uint32_t bits[kUnroll][8];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t item = base + u * stride + lane;
-      if (item < n_items && MXQ_IN_RANGE(kChkPackIn, item, n_items)) load8<DT>(in, item, bits[u]);
+      if ((ALL || item < n_items) && MXQ_IN_RANGE(kChkPackIn, item, n_items))
+        load8<DT>(in, item, bits[u]);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t item = base + u * stride + lane;
-      const bool valid = item < n_items;
+      const bool valid = ALL || item < n_items;
       uint32_t m = 0;
       if (valid) {
 #pragma unroll
@@ -68,6 +75,11 @@ pack_cache_kernel(const void* __restrict__ in, void* __restrict__ codes,
       if ((lane & (LPB - 1)) == 0 && MXQ_IN_RANGE(kChkPackScale, item / LPB, n_items / LPB))
         scales[item / LPB] = (uint8_t)scale_byte<FMT>(k);
     }
+  };
+  for (int64_t base = (int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31); base < n_items;
+       base += stride * kUnroll) {
+    if (base + (kUnroll - 1) * stride + 32 <= n_items) turn(std::true_type(), base);
+    else turn(std::false_type(), base);
   }
 }
 
