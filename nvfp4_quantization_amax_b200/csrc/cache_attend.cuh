@@ -8,9 +8,8 @@
 // the same time, without a plan made on the host.  A block that holds all
 // units of a pair writes its output; where a pair's units fall to several
 // blocks, each writes a partial (the normalised sum in f32 and its weight) to
-// one of its two workspace slots: slot 2i for a pair that
-// began in an earlier block, slot 2i + 1 for one that begins here.  A second,
-// small kernel joins them: the block after which a pair's first part lies
+// one of its two workspace slots: slot 2i for a pair that began in an earlier
+// block, slot 2i + 1 for one that begins here.  A second, small kernel joins them: the block after which a pair's first part lies
 // looks through the slots of the blocks behind it.
 #pragma once
 
@@ -26,9 +25,11 @@ namespace attend {
 constexpr int kUnit = 128;  // positions
 // What a pair costs beside its units (queries, the first loads' latency, the
 // join of the warps), in units: the line is laid in units plus this.  Measured
-// on 32 ragged sequences of up to 8192 tokens x 8 heads in fp8: 83.6 us with 0,
-// 61.3 us with 2, 63.1 us with 6; 96 even ones in mxfp4: 122.3, 121.2, 125.3.
-constexpr int kPairCost = 2;
+// with 0, 2, 4 and 6, us: 32 ragged sequences of up to 8192 tokens x 8 heads in
+// fp8 88.6, 60.0, 58.7, 59.2; 96 even ones x 4 in mxfp4 119.7, 118.8, 119.4,
+// 122.9; one of 131071 in nvfp4 47.0, 45.3, 45.1, 45.1; 16 in f16 with a window
+// of 5001 33.2, 28.2, 28.1, 30.2; 24 with 32 listed pages 55.3, 53.3, 53.4, 55.3.
+constexpr int kPairCost = 4;
 // Before any token: finite, so that no difference of two of them is NaN.
 constexpr float kLowest = -3.0e38f;
 constexpr float kLn2 = 0.6931471805599453f;
