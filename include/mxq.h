@@ -289,13 +289,17 @@ uint64_t attend_cache_paged_workspace_bytes(int64_t q_heads, int64_t kv_heads, i
  *           the logits; -infinity without tokens.
  *  workspace  device, 16-byte aligned, attend_cache_paged_workspace_bytes;
  *           clobbered, not shared by calls that overlap on the GPU.
- *  A query that is not finite, or a logit beyond f32's range, makes its
- *  head's row of out and lse NaN (not where the sequence has no tokens).
+ *  A query that is not finite makes its head's row of out and lse NaN (not
+ *  where the sequence has no tokens), and so may a logit, or a sum of products
+ *  of keys and the query scaled to 2^14 at its largest, beyond f32's range.
  *  Logits, softmax statistics and sums are f32.  Queries enter the products
  *  with all bits of a bf16 or f16 element and 22 of an f32 one, but none below
  *  2^-38 of the head's largest; every block of the keys counts, however far
- *  its scale lies below the others.  A token's value blocks whose
- *  scale is below 2^-18 of the token's largest one lose bits.
+ *  its scale lies below the others.  Weights multiply the values with 11 bits
+ *  where the result is bf16, else with 22, none below 2^-35 of the largest
+ *  (fp8, mxfp4: of the largest product of a weight and its token's largest
+ *  value scale).  Value blocks whose scale is below 2^-18 (mxfp4: 2^-23) of
+ *  their token's largest one may count as zero.
  *  Fast path: head_dim 64, 128 or 256, page_size a multiple of 16, block_size
  *  a power of two of at least 32 (fp8), 32 (mxfp4) or 16 (nvfp4), codes and
  *  scales 16-byte aligned; anything else valid runs a slower general kernel.

@@ -6,11 +6,13 @@
 // A byte of K or V meets the G query heads of its kv head, 4 G flop with fp8:
 // at G = 8 and the speed of HBM more than f32 arithmetic gives, and far less
 // than the tensor cores'.  So the codes go to f16 in registers (E4M3 and E2M1
-// are exact there) and through mma.m16n8k16 with f32 sums; the kernel is bound
-// by HBM, and its second limit is the issue of the conversions.  (A tcgen05
-// tile needs 128 rows of one operand: with tokens as rows it would leave the
-// head side, 8 wide, no better filled and the codes would have to be decoded
-// into TMEM first.)
+// are exact there) and through mma.m16n8k16 with f32 sums.  In fp8 the kernel
+// runs at 0.73 of a copy's rate, in mxfp4 at 0.55: there no unit is saturated
+// (issue slots 61 % busy, ALU 55 %, DRAM 47 % of peak), with 2.7 warps a
+// scheduler each waiting for the chain of its own turn.  (tcgen05's block-scaled
+// kinds would take K's codes as they are, with E8M0 scales per 32 channels and
+// queries as two E4M3 terms, 128 tokens a tile and the head side, 8 wide, no
+// better filled; V's scales lie across its product and leave it to be decoded.)
 //
 // Per warp, 16 tokens at a time (one tile; a page holds whole tiles):
 //  - S = K Q^T: rows are tokens, columns 8 heads.  K comes from shared memory
@@ -81,8 +83,8 @@ __host__ __device__ constexpr int place(int row, int col) {
 // FMT; D: channels; NB: scales of a row; NT: tiles of 8 heads a warp carries;
 // TERMS: f16 terms of queries and weights.  A warp takes U tiles of 16 tokens
 // at a time: two, so that the loop's own instructions are shared and two chains
-// run side by side (32 ragged sequences in fp8: 56.0 us against 57.8 with one),
-// or one of fp8 where two would not leave room for two buffers.
+// run side by side (32 ragged sequences in fp8, when chosen: 56.0 us replayed
+// against 57.8 with one; 56.1 now), or one of fp8 where two would not leave room for two buffers.
 template <int FMT, int D, int NB, int NT, int TERMS>
 struct Tc {
   static constexpr int RB = FMT == MXQ_FMT_FP8 ? D : D / 2;  // bytes of a row
@@ -91,8 +93,9 @@ struct Tc {
   static constexpr int SC = 16 * NB;  // scale bytes of a tile
   static constexpr int SCALES = U * 32 * RB;               // where a buffer's scales begin
   static constexpr int STAGE = U * 2 * (16 * RB + SC);     // [tile][K, V], then their scales
-  // Three blocks an SM leave 168 registers a thread: 96 x 8192 in mxfp4 take
-  // 117.0 us, with four (128 registers, some spilled) 121.0, with five 132.3.
+  // Three blocks an SM leave 168 registers a thread: 96 x 8192 in mxfp4 took
+  // 117.0 us when this was chosen (119.0 now), with four (128 registers, some
+  // spilled) 121.0, with five 132.3.
   static constexpr int MIN_CTAS = NT == 1 && TERMS == 1 && D <= 128 ? 3 : 2;
   static constexpr int SMEM = (MIN_CTAS == 3 ? 74 : 110) * 1024;
   static constexpr int INFO = 32 * 16;  // bytes: a warp's ring of tile places

@@ -134,6 +134,21 @@ def test_keys_with_empty_blocks(fmt, block):
     check_attend(cache, queries(3, 4, 64, torch.float32))
 
 
+@pytest.mark.parametrize("fmt,block,D,S", [("fp8", 32, 128, 16), ("mxfp4", 32, 64, 16),
+                                           ("fp8", 8, 40, 10), ("mxfp4", 20, 80, 24)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_values_with_a_block_as_far_below_as_still_counts(fmt, block, D, S, dtype):
+    # 18 binades (mxfp4: 23) beneath the token's largest scale: every bit, in
+    # channels of its own
+    down = 18 if fmt == "fp8" else 23
+    cache = ref.Cache([70, 1, 333], 2, D, S, fmt, block, seed=D)
+    scales = cache.v[1]
+    live = scales[..., 1] != 0xFF
+    top = scales.int().amax(-1)
+    scales[..., 1] = torch.where(live, (top - down).to(torch.uint8), scales[..., 1])
+    check_attend(cache, queries(3, 4, D, dtype))
+
+
 @pytest.mark.parametrize("fmt,block,D,S", KERNELS)
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
 def test_first_logits_far_below_the_others(fmt, block, D, S, dtype):
