@@ -60,17 +60,18 @@ int resident_ctas(const void* kernel, int threads, size_t smem) {
 
 cudaError_t allow_dynamic_smem(const void* kernel, int bytes) {
   static std::mutex mu;
-  static std::map<std::tuple<const void*, int, int>, cudaError_t> done;
+  // the largest allowed so far: the attribute holds what it was last set to, and
+  // a kernel may be launched with several sizes, in any order
+  static std::map<std::tuple<const void*, int>, int> allowed;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
-  const auto key = std::make_tuple(kernel, dev, bytes);
   std::lock_guard<std::mutex> lock(mu);
-  const auto it = done.find(key);
-  if (it != done.end()) return it->second;
+  int& most = allowed[std::make_tuple(kernel, dev)];
+  if (bytes <= most) return cudaSuccess;
   const cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (err != cudaSuccess) (void)cudaGetLastError();  // reported by the return value
-  done[key] = err;
+  if (err == cudaSuccess) most = bytes;
+  else (void)cudaGetLastError();  // reported by the return value
   return err;
 }
 

@@ -347,6 +347,14 @@ def test_a_refused_launch_is_reported_once(dim, page):
     assert r.returncode == 0 and "next call ok" in r.stdout, r.stdout + r.stderr
 
 
+@pytest.mark.parametrize("fmt,block", [("fp8", 16), ("fp8", 2), ("mxfp4", 32), ("nvfp4", 4)])
+def test_head_sizes_in_any_order(fmt, block):
+    # one kernel with more, less and again more shared memory
+    for D in (384, 512, 320, 512, 384):
+        cache = ref.Cache([33, 2], 1, D, 16, fmt, block, seed=D)
+        check_attend(cache, queries(2, 2, D, torch.bfloat16))
+
+
 # ------------------------------------------------------------ bad offs
 
 def test_bad_offs_touch_no_slot_outside_the_sequences():
