@@ -334,7 +334,7 @@ attend_general_kernel(Args a, int dt, int pad) {
       if (__any_sync(0xffffffffu, relate() > kWeightExp + kLag)) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float e = fmaxf(kLowest, fmaxf(d[j] + rf[0], d[j + 2] + rf[1]));
+          float e = fmaxf(kFloor, fmaxf(d[j] + rf[0], d[j + 2] + rf[1]));
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, w));
           const float En = fmaxf(E[j], e), fo = ex2(E[j] - En);

@@ -32,6 +32,11 @@ constexpr int kUnit = 128;  // positions
 constexpr int kPairCost = 4;
 // Before any token: finite, so that no difference of two of them is NaN.
 constexpr float kLowest = -3.0e38f;
+// The least exponent that weighted sums are held at, counted from the largest
+// logit: what lies below is no f32 beside it.  (A band of values may hold only
+// tokens far below that logit; taken from them, the exponent would have lost
+// the scales' bits, and weights would overflow f16.)
+constexpr float kFloor = -512.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr int kTcThreads = 128;

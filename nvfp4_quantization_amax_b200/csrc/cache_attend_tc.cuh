@@ -608,7 +608,7 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 // the column's largest s - m + r of this band
-                float e = kLowest;
+                float e = kFloor;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll

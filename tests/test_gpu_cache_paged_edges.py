@@ -202,6 +202,57 @@ def test_logits_so_large_that_a_scale_is_lost_beside_them(fmt, block, D, S, dtyp
         assert not out[0].any() and torch.isneginf(lse[0]).all()
 
 
+def weight_error(cache, q, scale):
+    """[n, Hq]: what weights held to f16's smallest step add to a result.  The
+    largest product of a weight and a value scale is at 2^11 or above, a
+    weight off by at most half of 2^-24 there: 2^-36 of that product for each
+    token, times the largest code.  Tokens with several scales of values are
+    taken together where these lie within 2^20, with the largest of them all,
+    so the product may be 2^20 above a token's own; and a token's largest value
+    is at least half of the largest code times its scale."""
+    n, Hq, D = q.shape
+    step = np.zeros((n, Hq))
+    together = 2.0 ** 20 if cache.fmt != "nvfp4" and cache.block < D else 1.0
+    for b in range(n):
+        for j in range(Hq):
+            h = j * cache.H // Hq
+            k, v = cache.values(cache.k, b, h), cache.values(cache.v, b, h)
+            if len(k):
+                z = scale * (k @ q[b, j].double().numpy())
+                w = np.exp(z - z.max()) / np.exp(z - z.max()).sum()
+                step[b, j] = 2.0 ** -35 * together * len(z) * (w * np.abs(v).max(1)).max()
+    return step
+
+
+@pytest.mark.parametrize("fmt,block,D,S", KERNELS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_values_far_apart_beside_large_logits(fmt, block, D, S, dtype):
+    # tokens' values over forty binades, so that turns are taken in bands, and
+    # logits of up to 2^28 of either sign: a band may hold none of the largest
+    for seed in range(6):
+        cache = ref.Cache([0, 700, 35], 1, D, S, fmt, block, seed=seed)
+        if fmt != "nvfp4":
+            g = torch.Generator().manual_seed(seed)
+            live = cache.k[1] != 0xFF
+            most = 8 if dtype == torch.float16 else 20
+            k = torch.randint(0, 26, live.shape[:3] + (1,), generator=g)
+            v = torch.randint(-20, most + 1, live.shape[:3] + (1,), generator=g)
+            for which, add in ((cache.k, k), (cache.v, v)):
+                which[1][:] = torch.where(live, (which[1].int() + add).to(torch.uint8), which[1])
+        q = queries(3, 3, D, dtype, seed=seed)
+        out, lse = mxq.attend_cache_paged(dev(q), dev(cache.k), dev(cache.v), dev(cache.table),
+                                          dev(cache.lengths), fmt, block, return_lse=True)
+        want, wl, spread, reach = ref.attend(cache, q)
+        tol = ref.out_tolerance(dtype, D, 700, want, spread, reach)
+        tol = tol + weight_error(cache, q, D ** -0.5)[..., None]
+        got = as_f64(out)
+        over = np.isinf(got)  # of f16 results alone
+        assert (np.abs(want)[over] + tol[over] >= torch.finfo(dtype).max).all()
+        assert (np.abs(got - want)[~over] <= tol[~over]).all(), seed
+        tol = ref.lse_tolerance(D, 700, wl, reach)
+        assert (np.abs(as_f64(lse)[1:] - wl[1:]) <= tol[1:]).all(), seed
+
+
 # ---------------------------------------------------------- host arguments
 
 def busy():
