@@ -297,8 +297,9 @@ uint64_t attend_cache_paged_workspace_bytes(int64_t q_heads, int64_t kv_heads, i
  *  2^-38 of the head's largest; every block of the keys counts, however far
  *  its scale lies below the others.  Weights multiply the values with 11 bits
  *  where the result is bf16, else with 22, none below 2^-35 of the largest
- *  (fp8, mxfp4: of the largest product of a weight and its token's largest
- *  value scale).  Value blocks whose scale is below 2^-18 (mxfp4: 2^-23) of
+ *  (fp8, mxfp4: of the largest product of a weight and a value scale; with
+ *  several scales a row, tokens whose scales lie within 2^20, or 2^8 where the
+ *  result is not bf16, may count with the largest of them).  Value blocks whose scale is below 2^-18 (mxfp4: 2^-23) of
  *  their token's largest one may count as zero.
  *  Fast path: head_dim 64, 128 or 256, page_size a multiple of 16, block_size
  *  a power of two of at least 32 (fp8), 32 (mxfp4) or 16 (nvfp4), codes and

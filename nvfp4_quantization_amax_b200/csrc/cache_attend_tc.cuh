@@ -34,8 +34,9 @@
 // row r is the token's.  With several it is the largest of the turn's tokens,
 // found by a lane looking at 1/32 of their scale bytes, and what is left of a
 // block's scale, 2^(k - r), multiplies the codes in f16 (exactly, as long as
-// k - r >= -21); where a scale byte of the turn lies more than 20 below the
-// largest, its tokens are taken in bands of nearly one r, each a pass over V.
+// k - r >= -21); where a scale byte of the turn lies more than 20 (results of
+// f16 and f32: 8) below the largest, its tokens are taken in bands of nearly one
+// r, each a pass over V.
 // E4M3 scales (nvfp4) times E2M1 codes are exact in f16.
 //
 // Rounding.  Q is scaled by a power of two into f16 and held in TERMS terms
@@ -54,9 +55,8 @@
 namespace mxq {
 namespace attend {
 
-// Scale bytes of V: how far a turn's may lie below its largest to be taken
-// together, and how far tokens' largest ones in one band.
-constexpr int kBand = 20, kSpan = 4;
+// How far scale bytes of V may lie apart in a band: its tokens' largest ones.
+constexpr int kSpan = 4;
 
 // Two E8M0 bytes (low first) as f32.
 __device__ __forceinline__ void e8m0x2(uint32_t two, float& lo, float& hi) {
@@ -119,6 +119,10 @@ struct Tc {
   static constexpr bool kRelative = !kAbsolute && NB > 1;
   static constexpr int B = D / NB;    // channels of a scale
   static constexpr int OFF = !kRelative ? 0 : FMT == MXQ_FMT_FP8 ? 7 : 12;
+  // How far a turn's scale bytes of V may lie below its largest to be taken
+  // together.  A weight is held to 2^-36 of the largest product of one and a
+  // scale, the turn's: 2^-16 of a token's own for bf16 results, 2^-28 for others.
+  static constexpr int BAND = TERMS == 1 ? 20 : 8;
   static_assert(STAGES >= 2 && STAGES <= 8, "too few buffers");
 
   // Channel of the i-th value of V that the lanes of group g hold, and where a
@@ -554,7 +558,7 @@ __device__ __forceinline__ void attend_tc_body(const Args& a, int dt) {
           lo2 = min(lo2 & 0xFFFFu, lo2 >> 16);
         }
         r = (int)__reduce_max_sync(0xffffffffu, hi2);
-        wide = part || __any_sync(0xffffffffu, (int)lo2 < r - kBand);
+        wide = part || __any_sync(0xffffffffu, (int)lo2 < r - T::BAND);
         if (wide) {
 #pragma unroll
           for (int u = 0; u < U; ++u)

@@ -207,12 +207,15 @@ def weight_error(cache, q, scale):
     largest product of a weight and a value scale is at 2^11 or above, a
     weight off by at most half of 2^-24 there: 2^-36 of that product for each
     token, times the largest code.  Tokens with several scales of values are
-    taken together where these lie within 2^20, with the largest of them all,
-    so the product may be 2^20 above a token's own; and a token's largest value
-    is at least half of the largest code times its scale."""
+    taken together where these lie within 2^20 (2^8 for f16 and f32 results),
+    with the largest of them all, so the product may be that much above a
+    token's own; and a token's largest value is at least half of the largest
+    code times its scale."""
     n, Hq, D = q.shape
     step = np.zeros((n, Hq))
-    together = 2.0 ** 20 if cache.fmt != "nvfp4" and cache.block < D else 1.0
+    together = 2.0 ** (20 if q.dtype == torch.bfloat16 else 8)
+    if cache.fmt == "nvfp4" or cache.block == D:
+        together = 1.0
     for b in range(n):
         for j in range(Hq):
             h = j * cache.H // Hq
@@ -251,6 +254,45 @@ def test_values_far_apart_beside_large_logits(fmt, block, D, S, dtype):
         assert (np.abs(got - want)[~over] <= tol[~over]).all(), seed
         tol = ref.lse_tolerance(D, 700, wl, reach)
         assert (np.abs(as_f64(lse)[1:] - wl[1:]) <= tol[1:]).all(), seed
+
+
+@pytest.mark.parametrize("fmt,block,D,S", [("fp8", 128, 128, 16), ("fp8", 32, 128, 16),
+                                           ("mxfp4", 32, 64, 16), ("fp8", 32, 256, 32),
+                                           ("fp8", 8, 40, 10), ("mxfp4", 20, 80, 24)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_small_weights_of_large_values(fmt, block, D, S, dtype):
+    """16 tokens of weight about 1/16 and 48 of about 2^-40 whose values are
+    2^17 times as large: 2^-14 of the result, which f32's weights have to hold.
+    A token's error is relative to what it adds."""
+    cache = ref.Cache([64], 1, D, S, fmt, block, seed=D, spread=0.0)
+    q = queries(1, 1, D, dtype)
+    u = q[0, 0].double()
+    row = (u * (-25.3 * D ** 0.5 / (u @ u))).to(torch.bfloat16)
+    first = [int(x) for x in torch.arange(64) % 4 == 0]  # in one turn with the others
+    for t in range(64):
+        page, slot = int(cache.table[0, t // S]), t % S
+        codes, scales = ref.pack((0 * row if first[t] else row).view(1, D), fmt, block)
+        cache.k[0][page, 0, slot], cache.k[1][page, 0, slot] = codes[0], scales[0]
+        if not first[t]:  # the values of the first token, larger
+            at = int(cache.table[0, 0])
+            cache.v[0][page, 0, slot] = cache.v[0][at, 0, 0]
+            cache.v[1][page, 0, slot] = cache.v[1][at, 0, 0] + 17
+    out = mxq.attend_cache_paged(dev(q), dev(cache.k), dev(cache.v), dev(cache.table),
+                                 dev(cache.lengths), fmt, block)
+    want, _, _, _ = ref.attend(cache, q)
+    k, v = cache.values(cache.k, 0, 0), np.abs(cache.values(cache.v, 0, 0))
+    z = (k @ u.numpy()) / D ** 0.5
+    w = np.exp(z - z.max()) / np.exp(z - z.max()).sum()
+    assert 2.0 ** -44 < w[1] < 2.0 ** -39
+    reach = (np.abs(k) @ np.abs(u.numpy())) / D ** 0.5
+    delta = reach * ((D + 8) * 2.0 ** -24 + 2.0 ** -22) + 2.0 ** -20 + 64 * 2.0 ** -24
+    delta += 2.0 ** -11 if dtype == torch.bfloat16 else 2.0 ** -21
+    # as weight_error, with tokens of f16 and f32 results taken together where
+    # their scales lie within 2^8
+    together = 2.0 ** (20 if dtype == torch.bfloat16 else 8) if block < D else 1.0
+    least = 64 * 2.0 ** -35 * together * (w[:, None] * v).max()
+    tol = torch.finfo(dtype).eps / 2 * np.abs(want[0, 0]) + 2 * ((w * delta) @ v) + least
+    assert (np.abs(as_f64(out)[0, 0] - want[0, 0]) <= tol).all()
 
 
 # ---------------------------------------------------------- host arguments
